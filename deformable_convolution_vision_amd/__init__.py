@@ -21,6 +21,8 @@ import torch
 __all__ = ["Desc", "dcn_output_hw", "dcn_workspace_bytes", "dcn_forward", "dcn_stage",
            "dcn_forward_staged", "dcn_variant_name", "dcn_plan_describe", "dcn_status_str", "deform_conv2d",
            "dcn_offset_mask_workspace_bytes", "dcn_offset_mask", "offset_mask", "dcn_forward_noalloc",
+           "dcn_cross_attention_workspace_bytes", "dcn_cross_attention", "cross_attention",
+           "dcn_cross_attention_backward_workspace_bytes", "dcn_cross_attention_backward", "cross_attention_backward",
            "DcnError", "library_path", "load_library", "F32", "BF16"]
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -32,7 +34,8 @@ NOALLOC_SCRATCH_BYTES = 32 << 20   # DCN_NOALLOC_SCRATCH_BYTES of dcn.h
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 _EXPORTS = ("dcn_output_hw", "dcn_workspace_bytes", "dcn_forward", "dcn_stage", "dcn_forward_staged",
             "dcn_variant_name", "dcn_plan_describe", "dcn_status_str", "dcn_offset_mask_workspace_bytes",
-            "dcn_offset_mask")
+            "dcn_offset_mask", "dcn_cross_attention_workspace_bytes", "dcn_cross_attention",
+            "dcn_cross_attention_backward_workspace_bytes", "dcn_cross_attention_backward")
 
 
 class DcnError(RuntimeError):
@@ -66,6 +69,14 @@ class PsRoiDesc(ctypes.Structure):
                 ("width", ctypes.c_int64), ("num_rois", ctypes.c_int64), ("pooled_size", ctypes.c_int64),
                 ("samples", ctypes.c_int64), ("offset_groups", ctypes.c_int64), ("spatial_scale", ctypes.c_float),
                 ("gamma", ctypes.c_float), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class AttnDesc(ctypes.Structure):
+    """Mirror of ``dcn_attn_desc``."""
+    _fields_ = [("batch", ctypes.c_int64), ("query_len", ctypes.c_int64), ("key_len", ctypes.c_int64),
+                ("query_heads", ctypes.c_int64), ("key_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+                ("mask_stride", ctypes.c_int64), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -119,6 +130,14 @@ def load_library() -> ctypes.CDLL:
     lib.dcn_ps_roi_pool.restype = ctypes.c_int
     lib.dcn_ps_roi_pool_workspace_bytes.argtypes = [ctypes.POINTER(PsRoiDesc), ctypes.POINTER(ctypes.c_size_t)]
     lib.dcn_ps_roi_pool_workspace_bytes.restype = ctypes.c_int
+    A = ctypes.POINTER(AttnDesc)
+    lib.dcn_cross_attention_workspace_bytes.argtypes = [A, ctypes.POINTER(S)]
+    lib.dcn_cross_attention.argtypes = [A, P, P, P, P, P, P, P, S, P]
+    lib.dcn_cross_attention_backward_workspace_bytes.argtypes = [A, ctypes.POINTER(S)]
+    lib.dcn_cross_attention_backward.argtypes = [A, P, P, P, P, P, P, P, P, P, P, P, S, P]
+    for name in ("dcn_cross_attention_workspace_bytes", "dcn_cross_attention",
+                 "dcn_cross_attention_backward_workspace_bytes", "dcn_cross_attention_backward"):
+        getattr(lib, name).restype = ctypes.c_int
     for name in ("dcn_output_hw", "dcn_workspace_bytes", "dcn_forward", "dcn_forward_staged", "dcn_stage"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
@@ -557,3 +576,121 @@ def deform_conv2d_layer(input, weight_om, bias_om, weight, bias=None, stride=1, 
         dcn_layer_forward(desc, input, weight_om, bias_om, weight, bias, offset, mask, out,
                           workspace if nbytes else None, nbytes)
     return out, offset, mask
+
+
+def attention_desc(query, key, value, key_mask=None, scale=None) -> AttnDesc:
+    """Descriptor of a cross attention call after checks of the tensors' shapes, types, devices
+    and strides (elements of a head adjacent; the other strides free)."""
+    dtype = _DTYPES.get(query.dtype)
+    if dtype is None:
+        raise TypeError(f"unsupported dtype {query.dtype}; use float32 or bfloat16")
+    if key.dtype != query.dtype or value.dtype != query.dtype:
+        raise TypeError(f"query is {query.dtype}, key {key.dtype}, value {value.dtype}: all share one dtype")
+    if query.dim() != 4 or key.dim() != 4 or value.dim() != 4:
+        raise ValueError("query must be [B,Lq,Hq,D], key and value [B,Lk,Hkv,D]")
+    B, Lq, Hq, D = query.shape
+    Bk, Lk, Hkv, Dk = key.shape
+    if Bk != B or Dk != D or value.shape != key.shape:
+        raise ValueError(f"key {tuple(key.shape)} and value {tuple(value.shape)} do not match query "
+                         f"{tuple(query.shape)}")
+    if Hkv == 0 or Hq == 0 or Hq % Hkv != 0:
+        raise ValueError(f"{Hq} query heads do not share {Hkv} key heads evenly")
+    device = query.device
+    if not query.is_cuda or key.device != device or value.device != device:
+        raise ValueError("query, key and value must be on one GPU")
+    qs, ks, vs = query.stride(), key.stride(), value.stride()
+    if D > 1 and (qs[3] != 1 or ks[3] != 1 or vs[3] != 1):
+        raise ValueError("the elements of a head (the last dimension) must be adjacent")
+    ms = 0
+    if key_mask is not None:
+        if key_mask.dtype != torch.bool and key_mask.dtype != torch.uint8:
+            raise TypeError(f"key_mask must be bool or uint8, got {key_mask.dtype}")
+        if tuple(key_mask.shape) != (B, Lk):
+            raise ValueError(f"key_mask must be {(B, Lk)}, got {tuple(key_mask.shape)}")
+        if key_mask.device != device:
+            raise ValueError("key_mask must be on the query's GPU")
+        ms, inner = key_mask.stride()
+        if Lk > 1 and inner != 1:
+            raise ValueError("the positions of key_mask must be adjacent")
+    if scale is None:
+        scale = D ** -0.5 if D else 1.0
+    return AttnDesc(B, Lq, Lk, Hq, Hkv, D, qs[:3], ks[:3], vs[:3], ms, scale, dtype)
+
+
+def dcn_cross_attention_workspace_bytes(desc: AttnDesc) -> int:
+    n = ctypes.c_size_t()
+    rc = load_library().dcn_cross_attention_workspace_bytes(ctypes.byref(desc), ctypes.byref(n))
+    if rc != OK:
+        raise DcnError(rc, "dcn_cross_attention_workspace_bytes")
+    return n.value
+
+
+def dcn_cross_attention(desc: AttnDesc, q, k, v, key_mask, out, lse, workspace, workspace_bytes: int,
+                        stream=None) -> None:
+    """Raw call: tensors (or integer device addresses) laid out as dcn.h states."""
+    rc = load_library().dcn_cross_attention(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(key_mask), _ptr(out),
+                                            _ptr(lse), _ptr(workspace), workspace_bytes, _stream(stream))
+    if rc != OK:
+        raise DcnError(rc, "dcn_cross_attention")
+
+
+def cross_attention(query, key, value, key_mask=None, scale=None, return_lse=False, out=None, workspace=None):
+    """Cross attention on the GPU: query [B,Lq,Hq,D] attends to the Lk states key, value
+    [B,Lk,Hkv,D] (Hkv divides Hq: heads h*Hq/Hkv .. share key head h), softmax over the positions
+    that key_mask [B,Lk] (bool or uint8; None: all) keeps, of scale * q.k (scale: 1/sqrt(D) by
+    default).  float32 or bfloat16, D <= 128, elements of a head adjacent, other strides free (a
+    slice of a fused projection or of a longer cache).  A batch element without a kept position
+    gives zeros.  Returns out [B,Lq,Hq,D], or (out, lse) with lse [B,Hq,Lq] float32, which
+    cross_attention_backward takes."""
+    desc = attention_desc(query, key, value, key_mask, scale)
+    device = query.device
+    if out is None:
+        out = torch.empty(query.shape, dtype=query.dtype, device=device)
+    else:
+        _check_out(out, query.shape, query.dtype, device)
+    lse = torch.empty((desc.batch, desc.query_heads, desc.query_len), dtype=torch.float32,
+                      device=device) if return_lse else None
+    nbytes = dcn_cross_attention_workspace_bytes(desc)
+    if nbytes or workspace is not None:
+        workspace = _workspace(workspace, nbytes, device)
+    with torch.cuda.device(device):
+        dcn_cross_attention(desc, query, key, value, key_mask, out, lse, workspace if nbytes else None, nbytes)
+    return (out, lse) if return_lse else out
+
+
+def dcn_cross_attention_backward_workspace_bytes(desc: AttnDesc) -> int:
+    n = ctypes.c_size_t()
+    rc = load_library().dcn_cross_attention_backward_workspace_bytes(ctypes.byref(desc), ctypes.byref(n))
+    if rc != OK:
+        raise DcnError(rc, "dcn_cross_attention_backward_workspace_bytes")
+    return n.value
+
+
+def dcn_cross_attention_backward(desc: AttnDesc, q, k, v, key_mask, out, lse, grad_out, grad_q, grad_k, grad_v,
+                                 workspace, workspace_bytes: int, stream=None) -> None:
+    """Raw call: tensors (or integer device addresses) laid out as dcn.h states; any gradient
+    may be None (not computed)."""
+    rc = load_library().dcn_cross_attention_backward(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(key_mask),
+                                                     _ptr(out), _ptr(lse), _ptr(grad_out), _ptr(grad_q), _ptr(grad_k),
+                                                     _ptr(grad_v), _ptr(workspace), workspace_bytes, _stream(stream))
+    if rc != OK:
+        raise DcnError(rc, "dcn_cross_attention_backward")
+
+
+def cross_attention_backward(grad_out, query, key, value, out, lse, key_mask=None, scale=None, workspace=None):
+    """Gradients of cross_attention on the GPU from its inputs, its out and lse, and the upstream
+    gradient grad_out [B,Lq,Hq,D]: returns dense (grad_query, grad_key, grad_value)."""
+    desc = attention_desc(query, key, value, key_mask, scale)
+    device = query.device
+    _check_out(grad_out, query.shape, query.dtype, device, "grad_out")
+    _check_out(out, query.shape, query.dtype, device)
+    _check_out(lse, (desc.batch, desc.query_heads, desc.query_len), torch.float32, device, "lse")
+    gq = torch.empty(query.shape, dtype=query.dtype, device=device)
+    gk = torch.empty(key.shape, dtype=query.dtype, device=device)
+    gv = torch.empty(key.shape, dtype=query.dtype, device=device)
+    nbytes = dcn_cross_attention_backward_workspace_bytes(desc)
+    workspace = _workspace(workspace, nbytes, device)
+    with torch.cuda.device(device):
+        dcn_cross_attention_backward(desc, query, key, value, key_mask, out, lse, grad_out, gq, gk, gv,
+                                     workspace if nbytes else None, nbytes)
+    return gq, gk, gv

@@ -295,6 +295,59 @@ int dcn_ps_roi_pool_workspace_bytes(const dcn_ps_roi_desc* desc, size_t* bytes);
 int dcn_ps_roi_pool(const dcn_ps_roi_desc* desc, const void* x, const float* rois, const void* offset,
                     const void* mask, void* out, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* Cross attention of query rows to an encoder's states of another length (the states of a
+ * feature map, [positions][channels], are what a detector's object queries, the positions of
+ * another map, or the tokens of a decoder attend to).  For batch element b, query position i
+ * and query head h, with n = h / (query_heads / key_heads) the key head that it shares, and
+ * over the positions j whose key_mask byte is not 0 (every j < key_len when key_mask is NULL):
+ *   s_j = scale * sum_d q[b,i,h,d] * k[b,j,n,d]
+ *   out[b,i,h,:] = sum_j exp(s_j) v[b,j,n,:] / sum_j exp(s_j),  lse[b,h,i] = log sum_j exp(s_j)
+ * No such j (key_len 0, or every byte 0): out is 0 and lse is -infinity.  What k and v hold at
+ * masked positions does not matter, infinities and NaN included.
+ *  - q [B,Lq,Hq,D], k and v [B,Lk,Hkv,D] of desc->dtype: elements d are adjacent, the strides of
+ *    batch, position and head (in elements, >= 0; 0 repeats) are the descriptor's, so slices of a
+ *    fused projection or of a longer cache are passed as they are.  key_mask [B,Lk] bytes with
+ *    mask_stride between batch elements (0 repeats).  out [B,Lq,Hq,D] dense in desc->dtype;
+ *    lse [B,Hq,Lq] float32 or NULL.
+ *  - Rows whose addresses and strides are multiples of 16 bytes are read 16 bytes at a time;
+ *    others element by element.
+ *  - Arithmetic: scores, softmax statistics and sums in fp32; for bf16 the weights exp(s - max)
+ *    are rounded to bf16 as an operand of the second product, and out is rounded once.
+ *  - The workspace (256-byte aligned, dcn_cross_attention_workspace_bytes, 0 for many
+ *    descriptors) holds the parts of keys split over workgroups; they are added in a fixed
+ *    order, so equal calls give equal bits.
+ * DCN_E_ARG: an invalid descriptor (query_heads % key_heads != 0, scale not finite or <= 0, a
+ * negative size or stride) or a NULL required pointer; DCN_E_UNSUPPORTED: another dtype,
+ * head_dim > 128, or row counts beyond 32 bits (strides and addresses are 64-bit: caches beyond
+ * 2^31 elements are fine); DCN_E_WORKSPACE, DCN_E_HIP as elsewhere; all checked before any
+ * launch.  batch or query_len 0: nothing is launched. */
+typedef struct dcn_attn_desc {
+  int64_t batch, query_len, key_len;
+  int64_t query_heads, key_heads, head_dim;
+  int64_t q_stride[3], k_stride[3], v_stride[3];   /* elements: batch, position, head */
+  int64_t mask_stride;                             /* bytes: batch */
+  float scale;
+  int32_t dtype;                                   /* enum dcn_dtype */
+} dcn_attn_desc;
+int dcn_cross_attention_workspace_bytes(const dcn_attn_desc* desc, size_t* bytes);
+int dcn_cross_attention(const dcn_attn_desc* desc, const void* q, const void* k, const void* v,
+                        const uint8_t* key_mask, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream);
+
+/* Gradients of dcn_cross_attention for the upstream gradient grad_out [B,Lq,Hq,D] (dense), from
+ * the forward's inputs, its out and its lse: grad_q [B,Lq,Hq,D], grad_k and grad_v [B,Lk,Hkv,D],
+ * dense, in desc->dtype.  Any gradient pointer may be NULL (not computed).  Heads that share a
+ * key head add up in grad_k and grad_v; an input repeated by a stride of 0 gets the gradient of
+ * every repetition.  Masked positions get zeros, and so do rows with no key.  Arithmetic: the
+ * weights are formed again from the scores and lse in fp32; for bf16 the weights and the score
+ * gradients are rounded to bf16 as operands of the second products; sums in fp32 in a fixed
+ * order (no atomics).  Workspace and errors as for dcn_cross_attention. */
+int dcn_cross_attention_backward_workspace_bytes(const dcn_attn_desc* desc, size_t* bytes);
+int dcn_cross_attention_backward(const dcn_attn_desc* desc, const void* q, const void* k, const void* v,
+                                 const uint8_t* key_mask, const void* out, const float* lse,
+                                 const void* grad_out, void* grad_q, void* grad_k, void* grad_v,
+                                 void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 const char* dcn_status_str(int status);
 
 #ifdef __cplusplus
