@@ -23,6 +23,8 @@ __all__ = ["Desc", "dcn_output_hw", "dcn_workspace_bytes", "dcn_forward", "dcn_s
            "dcn_offset_mask_workspace_bytes", "dcn_offset_mask", "offset_mask", "dcn_forward_noalloc",
            "dcn_cross_attention_workspace_bytes", "dcn_cross_attention", "cross_attention",
            "dcn_cross_attention_backward_workspace_bytes", "dcn_cross_attention_backward", "cross_attention_backward",
+           "dcn_group_norm_workspace_bytes", "dcn_group_norm", "group_norm_act",
+           "dcn_group_norm_backward_workspace_bytes", "dcn_group_norm_backward", "group_norm_act_backward",
            "DcnError", "library_path", "load_library", "F32", "BF16"]
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -35,7 +37,9 @@ _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 _EXPORTS = ("dcn_output_hw", "dcn_workspace_bytes", "dcn_forward", "dcn_stage", "dcn_forward_staged",
             "dcn_variant_name", "dcn_plan_describe", "dcn_status_str", "dcn_offset_mask_workspace_bytes",
             "dcn_offset_mask", "dcn_cross_attention_workspace_bytes", "dcn_cross_attention",
-            "dcn_cross_attention_backward_workspace_bytes", "dcn_cross_attention_backward")
+            "dcn_cross_attention_backward_workspace_bytes", "dcn_cross_attention_backward",
+            "dcn_group_norm_workspace_bytes", "dcn_group_norm", "dcn_group_norm_backward_workspace_bytes",
+            "dcn_group_norm_backward")
 
 
 class DcnError(RuntimeError):
@@ -78,6 +82,15 @@ class AttnDesc(ctypes.Structure):
                 ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
                 ("mask_stride", ctypes.c_int64), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
 
+
+class NormDesc(ctypes.Structure):
+    """Mirror of ``dcn_norm_desc``."""
+    _fields_ = [("batch", ctypes.c_int64), ("positions", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("groups", ctypes.c_int64), ("eps", ctypes.c_float), ("activation", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
 _lib = None
 
@@ -135,8 +148,15 @@ def load_library() -> ctypes.CDLL:
     lib.dcn_cross_attention.argtypes = [A, P, P, P, P, P, P, P, S, P]
     lib.dcn_cross_attention_backward_workspace_bytes.argtypes = [A, ctypes.POINTER(S)]
     lib.dcn_cross_attention_backward.argtypes = [A, P, P, P, P, P, P, P, P, P, P, P, S, P]
+    N = ctypes.POINTER(NormDesc)
+    lib.dcn_group_norm_workspace_bytes.argtypes = [N, ctypes.POINTER(S)]
+    lib.dcn_group_norm.argtypes = [N, P, P, P, P, P, P, P, S, P]
+    lib.dcn_group_norm_backward_workspace_bytes.argtypes = [N, ctypes.POINTER(S)]
+    lib.dcn_group_norm_backward.argtypes = [N, P, P, P, P, P, P, P, P, P, P, S, P]
     for name in ("dcn_cross_attention_workspace_bytes", "dcn_cross_attention",
-                 "dcn_cross_attention_backward_workspace_bytes", "dcn_cross_attention_backward"):
+                 "dcn_cross_attention_backward_workspace_bytes", "dcn_cross_attention_backward",
+                 "dcn_group_norm_workspace_bytes", "dcn_group_norm", "dcn_group_norm_backward_workspace_bytes",
+                 "dcn_group_norm_backward"):
         getattr(lib, name).restype = ctypes.c_int
     for name in ("dcn_output_hw", "dcn_workspace_bytes", "dcn_forward", "dcn_forward_staged", "dcn_stage"):
         getattr(lib, name).restype = ctypes.c_int
@@ -694,3 +714,107 @@ def cross_attention_backward(grad_out, query, key, value, out, lse, key_mask=Non
         dcn_cross_attention_backward(desc, query, key, value, key_mask, out, lse, grad_out, gq, gk, gv,
                                      workspace if nbytes else None, nbytes)
     return gq, gk, gv
+
+
+def _norm_desc(input, num_groups, weight, bias, eps, activation) -> NormDesc:
+    dtype = _DTYPES.get(input.dtype)
+    if dtype is None:
+        raise TypeError(f"unsupported dtype {input.dtype}; use float32 or bfloat16")
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {activation!r}")
+    shape = input.shape
+    if len(shape) < 2:
+        raise ValueError("input must be [B, ..., C], channels last")
+    if not input.is_cuda or not input.is_contiguous():
+        raise ValueError("input must be a contiguous GPU tensor (channels last)")
+    C = shape[-1]
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is None:
+            continue
+        if t.shape != (C,) or t.dtype != input.dtype or t.device != input.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {input.dtype} tensor of {C} channels on the input's device")
+    P = 1
+    for n in shape[1:-1]:
+        P *= n
+    return NormDesc(shape[0], P, C, int(num_groups), eps, act, dtype, 0)
+
+
+def dcn_group_norm_workspace_bytes(desc: NormDesc) -> int:
+    n = ctypes.c_size_t()
+    rc = load_library().dcn_group_norm_workspace_bytes(ctypes.byref(desc), ctypes.byref(n))
+    if rc != OK:
+        raise DcnError(rc, "dcn_group_norm_workspace_bytes")
+    return n.value
+
+
+def dcn_group_norm(desc: NormDesc, x, weight, bias, out, mean, rstd, workspace, workspace_bytes: int,
+                   stream=None) -> None:
+    """Raw call: tensors (or integer device addresses) laid out as dcn.h states."""
+    rc = load_library().dcn_group_norm(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(out), _ptr(mean),
+                                       _ptr(rstd), _ptr(workspace), workspace_bytes, _stream(stream))
+    if rc != OK:
+        raise DcnError(rc, "dcn_group_norm")
+
+
+def group_norm_act(input, num_groups, weight=None, bias=None, eps=1e-5, activation="none", return_stats=False,
+                   out=None, workspace=None):
+    """Group normalisation of a channels-last map on the GPU, with the activation after it: input
+    [B, ..., C] (float32 or bfloat16, contiguous), num_groups groups of adjacent channels, weight
+    and bias [C] or None, activation "none", "relu", "silu" or "gelu".  Returns the input's shape
+    and dtype, or (out, mean, rstd) with the statistics [B, num_groups] in float32, which
+    group_norm_act_backward takes."""
+    desc = _norm_desc(input, num_groups, weight, bias, eps, activation)
+    device = input.device
+    if out is None:
+        out = torch.empty_like(input)
+    else:
+        _check_out(out, input.shape, input.dtype, device)
+    nbytes = dcn_group_norm_workspace_bytes(desc)
+    mean = rstd = None
+    if return_stats:
+        mean, rstd = (torch.empty((desc.batch, desc.groups), dtype=torch.float32, device=device) for _ in range(2))
+    workspace = _workspace(workspace, nbytes, device)
+    with torch.cuda.device(device):
+        dcn_group_norm(desc, input, weight, bias, out, mean, rstd, workspace, nbytes)
+    return (out, mean, rstd) if return_stats else out
+
+
+def dcn_group_norm_backward_workspace_bytes(desc: NormDesc) -> int:
+    n = ctypes.c_size_t()
+    rc = load_library().dcn_group_norm_backward_workspace_bytes(ctypes.byref(desc), ctypes.byref(n))
+    if rc != OK:
+        raise DcnError(rc, "dcn_group_norm_backward_workspace_bytes")
+    return n.value
+
+
+def dcn_group_norm_backward(desc: NormDesc, x, weight, bias, mean, rstd, grad_out, grad_x, grad_weight, grad_bias,
+                            workspace, workspace_bytes: int, stream=None) -> None:
+    """Raw call: tensors (or integer device addresses) laid out as dcn.h states; any gradient
+    may be None (not computed)."""
+    rc = load_library().dcn_group_norm_backward(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(mean),
+                                                _ptr(rstd), _ptr(grad_out), _ptr(grad_x), _ptr(grad_weight),
+                                                _ptr(grad_bias), _ptr(workspace), workspace_bytes, _stream(stream))
+    if rc != OK:
+        raise DcnError(rc, "dcn_group_norm_backward")
+
+
+def group_norm_act_backward(grad_out, input, mean, rstd, num_groups, weight=None, bias=None, activation="none",
+                            workspace=None):
+    """Gradients of group_norm_act on the GPU from its input, parameters and statistics, and the
+    upstream gradient grad_out of the input's shape: returns (grad_input, grad_weight, grad_bias),
+    None for a parameter that is None."""
+    desc = _norm_desc(input, num_groups, weight, bias, 0.0, activation)
+    device = input.device
+    _check_out(grad_out, input.shape, input.dtype, device, "grad_out")
+    nbytes = dcn_group_norm_backward_workspace_bytes(desc)
+    stats = (desc.batch, desc.groups)
+    _check_out(mean, stats, torch.float32, device, "mean")
+    _check_out(rstd, stats, torch.float32, device, "rstd")
+    gx = torch.empty_like(input)
+    gw = None if weight is None else torch.empty_like(weight)
+    gb = None if bias is None else torch.empty_like(bias)
+    workspace = _workspace(workspace, nbytes, device)
+    with torch.cuda.device(device):
+        dcn_group_norm_backward(desc, input, weight, bias, mean, rstd, grad_out, gx, gw, gb, workspace, nbytes)
+    return gx, gw, gb

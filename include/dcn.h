@@ -348,6 +348,45 @@ int dcn_cross_attention_backward(const dcn_attn_desc* desc, const void* q, const
                                  const void* grad_out, void* grad_q, void* grad_k, void* grad_v,
                                  void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* Group normalisation of a channels-last map (what follows a deformable layer in detection heads
+ * and the projections of its maps to an encoder's states) with the activation after it.
+ * x [B][P][C] (P positions: height times width), groups of channels / groups adjacent channels,
+ * statistics over the positions and channels of a group of one batch element:
+ *   n = (x - mean) * rstd,  rstd = 1 / sqrt(var + eps) (var over all N values, not N - 1),
+ *   out = act(n * weight[c] + bias[c])
+ * weight [C] and bias [C] or NULL (1 and 0); act one of dcn_activation (gelu by the error
+ * function); mean and rstd [B][groups] float32 are written where not NULL (the backward takes
+ * them).  x, weight, bias and out dense in desc->dtype; out may be x.  Arithmetic: fp32, out
+ * rounded once.  Rows that start on 16 bytes (C a multiple of 8 bf16 or 4 fp32 elements) are
+ * read 16 bytes at a time, others element by element.  Equal calls give equal bits.
+ * DCN_E_ARG: an invalid descriptor (positions < 1, channels % groups != 0, eps negative or not
+ * finite, an activation that is none) or a NULL x or out; DCN_E_UNSUPPORTED: another dtype,
+ * more than 8192 channels or 65534 batch elements, or 2^31 positions (addresses are 64-bit);
+ * DCN_E_WORKSPACE, DCN_E_HIP as elsewhere; all checked before any launch.  batch 0: nothing is
+ * launched. */
+enum dcn_activation { DCN_ACT_NONE = 0, DCN_ACT_RELU = 1, DCN_ACT_SILU = 2, DCN_ACT_GELU = 3 };
+typedef struct dcn_norm_desc {
+  int64_t batch, positions, channels, groups;
+  float eps;
+  int32_t activation;   /* enum dcn_activation */
+  int32_t dtype;        /* enum dcn_dtype */
+  int32_t reserved;     /* 0 */
+} dcn_norm_desc;
+int dcn_group_norm_workspace_bytes(const dcn_norm_desc* desc, size_t* bytes);
+int dcn_group_norm(const dcn_norm_desc* desc, const void* x, const void* weight, const void* bias, void* out,
+                   float* mean, float* rstd, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Gradients of dcn_group_norm for the upstream gradient grad_out [B][P][C], from the forward's x,
+ * weight, bias, mean and rstd (desc->eps is not read again): grad_x [B][P][C], grad_weight [C],
+ * grad_bias [C] in desc->dtype.  Any gradient pointer may be NULL (not computed).  relu has the
+ * slope 0 at 0.  Arithmetic: fp32 in a fixed order (no atomics), each gradient rounded once.
+ * Errors as for dcn_group_norm; batch 0: grad_weight and grad_bias are written as zeros. */
+int dcn_group_norm_backward_workspace_bytes(const dcn_norm_desc* desc, size_t* bytes);
+int dcn_group_norm_backward(const dcn_norm_desc* desc, const void* x, const void* weight, const void* bias,
+                            const float* mean, const float* rstd, const void* grad_out, void* grad_x,
+                            void* grad_weight, void* grad_bias, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream);
+
 const char* dcn_status_str(int status);
 
 #ifdef __cplusplus

@@ -1,0 +1,90 @@
+"""Host side of the group normalisation entry points: descriptor, pointer and workspace checks.
+No GPU: every call here returns before its first HIP call."""
+
+import ctypes
+import os
+
+import pytest
+
+import deformable_convolution_vision_amd as dcn
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(dcn.LIB_PATH):
+        from deformable_convolution_vision_amd import build
+        build.build()
+    return dcn.load_library()
+
+
+def desc(**over):
+    d = dcn.NormDesc(2, 4200, 256, 32, 1e-5, 2, dcn.BF16, 0)
+    for n, v in over.items():
+        setattr(d, n, v)
+    return d
+
+
+FAKE, WS = 0x10000, 0x20000
+
+
+def status(lib, d, backward, x=FAKE, out=FAKE, mean=FAKE, rstd=FAKE, go=FAKE, ws=WS, nb=1 << 40):
+    r = ctypes.byref(d) if d is not None else None
+    if backward:
+        return lib.dcn_group_norm_backward(r, x, None, None, mean, rstd, go, FAKE, None, None, ws, nb, None)
+    return lib.dcn_group_norm(r, x, None, None, out, None, None, ws, nb, None)
+
+
+def workspace(lib, d, backward):
+    n = ctypes.c_size_t(12345)
+    f = lib.dcn_group_norm_backward_workspace_bytes if backward else lib.dcn_group_norm_workspace_bytes
+    return f(ctypes.byref(d), ctypes.byref(n)), n.value
+
+
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("bad", [
+    dict(batch=-1), dict(positions=0), dict(channels=0), dict(groups=0), dict(groups=-1), dict(groups=3),
+    dict(groups=512), dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(activation=-1),
+    dict(activation=4)], ids=str)
+def test_invalid_descriptors(lib, bad, backward):
+    d = desc(**bad)
+    assert workspace(lib, d, backward) == (dcn.E_ARG, 12345)
+    assert status(lib, d, backward) == dcn.E_ARG
+
+
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("bad", [dict(dtype=7), dict(channels=8224), dict(batch=65535), dict(positions=1 << 31)], ids=str)
+def test_unsupported_descriptors(lib, bad, backward):
+    d = desc(**bad)
+    assert workspace(lib, d, backward) == (dcn.E_UNSUPPORTED, 12345)
+    assert status(lib, d, backward) == dcn.E_UNSUPPORTED
+
+
+def test_null_pointers_and_workspace(lib):
+    d = desc()
+    for n in ("x", "out"):
+        assert status(lib, d, False, **{n: None}) == dcn.E_ARG, n
+    for n in ("x", "mean", "rstd", "go"):
+        assert status(lib, d, True, **{n: None}) == dcn.E_ARG, n
+    for backward in (False, True):
+        assert status(lib, None, backward) == dcn.E_ARG
+        rc, nb = workspace(lib, d, backward)
+        assert rc == dcn.OK and nb > 0 and nb % 256 == 0 and workspace(lib, d, backward) == (dcn.OK, nb)
+        assert status(lib, d, backward, ws=None, nb=nb) == dcn.E_WORKSPACE
+        assert status(lib, d, backward, nb=nb - 1) == dcn.E_WORKSPACE
+        assert status(lib, d, backward, ws=WS + 16, nb=nb) == dcn.E_WORKSPACE
+    assert lib.dcn_group_norm_workspace_bytes(ctypes.byref(d), None) == dcn.E_ARG
+    assert lib.dcn_group_norm_backward_workspace_bytes(ctypes.byref(d), None) == dcn.E_ARG
+
+
+def test_an_empty_batch_launches_nothing(lib):
+    d = desc(batch=0)
+    assert lib.dcn_group_norm(ctypes.byref(d), None, None, None, None, None, None, None, 0, None) == dcn.OK
+    assert lib.dcn_group_norm_backward(ctypes.byref(d), *[None] * 10, 0, None) == dcn.OK
+
+
+def test_binding_refuses_what_is_not_on_a_gpu(lib):
+    import torch
+    with pytest.raises(ValueError):
+        dcn.group_norm_act(torch.zeros(1, 4, 8), 2)
+    with pytest.raises(TypeError):
+        dcn.group_norm_act(torch.zeros(1, 4, 8).half(), 2)
