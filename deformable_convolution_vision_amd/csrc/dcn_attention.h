@@ -34,8 +34,8 @@ struct Args {
   const uint8_t* mask;         // [B][Lk] bytes, 0: the key is padding; or null
   void* out;                   // [B][Lq][Hq][D]
   float* lse;                  // [B][Hq][Lq] or null
-  float* part;                 // forward: partial outputs [S][B][Hkv][R][DP], not yet divided by their sums
-  float* part_ml;              // ... with each row's maximum and sum, [S][B][Hkv][R][2]
+  float* part;                 // forward: partial outputs [split tile][split][row][DP], not yet divided by their sums
+  float* part_ml;              // ... with each row's maximum and sum, [split tile][split][row][2]
   const void* dout;            // backward: [B][Lq][Hq][D]
   const float* delta;          // backward: [B][Hkv][R][2]: lse in powers of two, and sum(dout * out)
   void *dq, *dk, *dv;
@@ -43,8 +43,10 @@ struct Args {
   int64_t ms;                  // the mask's batch stride
   int B, Lq, Lk, Hq, Hkv, g, D;
   int R;                       // query rows of one key head: g * Lq, row r = position r / g, head r % g
-  int splits;                  // parts the keys (dK, dV: the rows) are split into
-  int per_split;               // tiles of one part
+  int tiles;                   // row tiles (dK, dV: key tiles) of all batch elements and key heads
+  int full;                    // tiles below this one have a workgroup each; the inner loop of each of the others
+  int splits;                  // is split over this many workgroups,
+  int per_split;               // of so many steps
   float c;                     // scale * log2(e): softmax runs in powers of two
   float scale;
 };
@@ -56,14 +58,11 @@ template <typename T>
 struct Elem;
 template <>
 struct Elem<uint16_t> {
-  static constexpr int kVec = 8;   // elements of 16 bytes
-  static constexpr int kPad = 16;  // LDS rows DP + 16 long: 32-byte offsets that neither the 16-byte row reads nor
-                                   // the transposing reads of 4 rows find on the same banks
+  static constexpr int kVec = 8;
 };
 template <>
 struct Elem<float> {
   static constexpr int kVec = 4;
-  static constexpr int kPad = 4;
 };
 
 // 8 consecutive elements, one lane's share of an operand
@@ -95,14 +94,33 @@ __device__ __forceinline__ f32x16 mma(const Frag<float>& a, const Frag<float>& b
   return c;
 }
 
-// A zero accumulator the compiler cannot see through: it may otherwise place an operand
-// of the first product in the product's own result registers.
 __device__ __forceinline__ f32x16 zero_acc() {
   f32x16 z;
 #pragma unroll
   for (int r = 0; r < 16; ++r) z[r] = 0.f;
-  asm volatile("" : "+v"(z));
   return z;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+// Which of 64 blocks of 32 keys hold attended keys: lane i receives the mask bits of keys
+// first + i * step .. + 31 as one word (0 beyond `end`); mp null: every key below Lk counts.
+__device__ __forceinline__ uint32_t key_words(const uint8_t* mp, int64_t first, int64_t step, int64_t end, int Lk) {
+  const int64_t k0 = first + (threadIdx.x & 63) * step;
+  if (k0 >= end || k0 >= Lk) return 0;
+  const int n = static_cast<int>(min(static_cast<int64_t>(32), Lk - k0));
+  uint32_t word = n == 32 ? 0xffffffffu : (1u << n) - 1u;
+  if (mp == nullptr) return word;
+  uint32_t kept = 0;
+  if (n == 32) {
+    uint32_t w[8];
+    __builtin_memcpy(w, mp + k0, 32);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) kept |= ((w[i / 4] >> (8 * (i % 4))) & 0xffu) != 0 ? 1u << i : 0u;
+  } else {
+    for (int i = 0; i < n; ++i) kept |= mp[k0 + i] != 0 ? 1u << i : 0u;
+  }
+  return word & kept;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -152,52 +170,35 @@ struct Vec16 {
   };
 };
 
-// elements d .. d+kVec-1 of a row of D elements; zeros beyond D, and everywhere when !live.
-// VEC: rows are 16-byte aligned and D is a multiple of the vector.
+// Elements d .. d+kVec-1 (of D) of a row that starts `offset` elements after base; zeros beyond
+// D, and everywhere when !live.  VEC: rows are 16-byte aligned, D is a multiple of the vector
+// and the offset in bytes fits 32 bits, so that the load takes a scalar base and one register.
 template <typename T, bool VEC>
-__device__ __forceinline__ Vec16<T> load_vec(const T* row, int d, int D, bool live) {
+__device__ __forceinline__ Vec16<T> load_vec(const T* base, int64_t offset, int d, int D, bool live) {
   Vec16<T> v;
   v.u = make_uint4(0, 0, 0, 0);
   if (VEC) {
-    if (live && d < D) v.u = *reinterpret_cast<const uint4*>(row + d);
+    const uint32_t at = static_cast<uint32_t>(offset + d) * static_cast<uint32_t>(sizeof(T));
+    if (live && d < D) v.u = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(base) + at);
   } else {
 #pragma unroll
     for (int j = 0; j < Elem<T>::kVec; ++j)
-      if (live && d + j < D) v.e[j] = row[d + j];
+      if (live && d + j < D) v.e[j] = base[offset + d + j];
   }
   return v;
 }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ Frag<T> load_frag(const T* row, int d, int D, bool live);
-template <>
-__device__ __forceinline__ Frag<uint16_t> load_frag<uint16_t, true>(const uint16_t* row, int d, int D, bool live) {
-  Frag<uint16_t> f;
-  f.u = load_vec<uint16_t, true>(row, d, D, live).u;
-  return f;
-}
-template <>
-__device__ __forceinline__ Frag<uint16_t> load_frag<uint16_t, false>(const uint16_t* row, int d, int D, bool live) {
-  Frag<uint16_t> f;
-  f.u = load_vec<uint16_t, false>(row, d, D, live).u;
-  return f;
-}
-template <>
-__device__ __forceinline__ Frag<float> load_frag<float, true>(const float* row, int d, int D, bool live) {
-  Frag<float> f;
+// A lane's fragments of its row: elements 16 i + 8 half .. + 7 for every i.
+template <typename T, int DP, bool VEC>
+__device__ __forceinline__ void load_frags(const T* base, int64_t offset, int D, bool live, Frag<T> (&f)[DP / 16]) {
+  const int d0 = 8 * ((threadIdx.x & 63) >> 5);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint4 u = load_vec<float, true>(row, d + 4 * h, D, live).u;
-    f.u[h] = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
-  }
-  return f;
-}
-template <>
-__device__ __forceinline__ Frag<float> load_frag<float, false>(const float* row, int d, int D, bool live) {
-  Frag<float> f;
+  for (int i = 0; i < DP / 16; ++i)
 #pragma unroll
-  for (int j = 0; j < 8; ++j) f.f[j] = (live && d + j < D) ? row[d + j] : 0.f;
-  return f;
+    for (int h = 0; h < 8 / Elem<T>::kVec; ++h) {
+      const uint4 u = load_vec<T, VEC>(base, offset, 16 * i + d0 + Elem<T>::kVec * h, D, live).u;
+      __builtin_memcpy(reinterpret_cast<char*>(&f[i]) + 16 * h, &u, 16);
+    }
 }
 
 // one lane's fragment of a row-major LDS tile: 8 consecutive elements of a row
@@ -213,11 +214,74 @@ __device__ __forceinline__ Frag<float> lds_frag(const float* p) {
   return f;
 }
 
+// ---- tiles in LDS
+//
+// Tiles of rows are moved by buffer -> LDS loads, which hold no registers: lane i of a 1 KB
+// load fills the 16 bytes i of its kilobyte, so rows stand one after the other without padding,
+// and it is the choice of what a lane fetches that spreads them over the banks: vector j of row
+// r is kept in place j ^ swz(r).  The swizzle serves both readers: 16 rows at one vector (the
+// row fragments, 256 bytes a cycle) and 4 rows at 4 adjacent vectors (the transposing reads).
+template <typename T, int DP>
+struct Tile {
+  static constexpr int kVecs = DP * static_cast<int>(sizeof(T)) / 16;   // 16-byte vectors of a row: 4 .. 32
+  __device__ static __forceinline__ int swz(int r) {
+    if (kVecs == 4) return (r >> 2) & 3;
+    if (kVecs == 8) return ((r >> 1) & 1) << 2 | ((r >> 2) & 1) << 1 | ((r >> 3) & 1);
+    return (r & 3) << 2 | ((r >> 2) & 3);
+  }
+  // element d of row r
+  __device__ static __forceinline__ int at(int r, int d) {
+    constexpr int V = 16 / static_cast<int>(sizeof(T));
+    return r * DP + ((d / V) ^ swz(r)) * V + d % V;
+  }
+};
+
+typedef __attribute__((address_space(3))) void lds_void;
+constexpr uint32_t kOutside = 0xfffffff0u;   // a byte offset beyond every buffer: the load gives zeros
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, 0x7fffffff, 0x00020000);
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// waits for this wave's LDS reads and writes, but not for its loads, and for the other waves
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Rows 0 .. ROWS-1 of a tile into LDS by NT threads (thread `tid` of them): row r from base + r * stride (elements),
+// zeros where bit r of `live` is 0 and beyond D.  VEC: asynchronous, (ROWS * DP * sizeof(T)) /
+// (16 * NT) loads of each wave; otherwise element by element and done on return (but for a barrier).
+template <typename T, int DP, int ROWS, int NT, bool VEC>
+__device__ __forceinline__ void fetch_tile(T* lds, const T* base, int64_t stride, uint64_t live, int D, int tid) {
+  using L = Tile<T, DP>;
+  constexpr int N = ROWS * L::kVecs / NT, KV = Elem<T>::kVec;
+  static_assert(ROWS * L::kVecs % NT == 0 && ROWS <= 64, "whole loads");
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if constexpr (VEC) {
+    const __amdgpu_buffer_rsrc_t rs = rsrc_of(base);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = i * NT + tid, r = at / L::kVecs, d = ((at % L::kVecs) ^ L::swz(r)) * KV;
+      const uint32_t ofs = (static_cast<uint32_t>(r) * static_cast<uint32_t>(stride) + d) * static_cast<uint32_t>(sizeof(T));
+      const bool in = ((live >> r) & 1u) && d < D;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + (i * NT + wave * 64) * KV), 16,
+                                               in ? ofs : kOutside, 0, 0, 0);
+    }
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < N; ++i) {
+      const int at = i * NT + tid, r = at / L::kVecs, d = ((at % L::kVecs) ^ L::swz(r)) * KV;
+      const Vec16<T> v = load_vec<T, false>(base, r * stride, d, D, (live >> r) & 1u);
+      *reinterpret_cast<uint4*>(lds + at * KV) = v.u;
+    }
+  }
+}
+
 // The second product of an attention step takes the first one's result registers as its B
 // operand as they are (no exchange between lanes): register r of a lane is row
 // acc_row(r, half) of the 32 rows, so the A operand has to hold the same rows in the same
-// order.  acc += sum over the 32 rows of tile[row][d0 + (l & 31)] * p[r]; `tile` points at
-// the first of the 32 rows.  bf16 reads 4 rows x 16 columns at a time transposed (lane i of
+// order.  acc += sum over the 32 rows of tile[row][d0 + (l & 31)] * p[r].  bf16 reads 4 rows x 16 columns at a time transposed (lane i of
 // 16 hands in the address of row i / 4, columns 4*(i % 4), and receives column i of the 4
 // rows); p is rounded to bf16, the operand type of the product.
 struct PFrag16 {
@@ -243,44 +307,62 @@ struct POperand<uint16_t> { using type = PFrag16; };
 template <>
 struct POperand<float> { using type = PFrag32; };
 
-__device__ __forceinline__ f32x16 mma_rows(const uint16_t* tile, int stride, int d0, const PFrag16& p, f32x16 acc) {
+// r0: the first of the 32 rows, a multiple of 32
+template <int DP>
+__device__ __forceinline__ f32x16 mma_rows(const uint16_t* tile, int r0, int d0, const PFrag16& p, f32x16 acc) {
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-  const int l = threadIdx.x & 63, i = l & 15;
-  const uint16_t* at = tile + (4 * (l >> 5) + (i >> 2)) * stride + d0 + 16 * ((l >> 4) & 1) + 4 * (i & 3);
+  const int l = threadIdx.x & 63, i = l & 15, r = r0 + 4 * (l >> 5) + (i >> 2), d = d0 + 16 * ((l >> 4) & 1) + 4 * (i & 3);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     Frag<uint16_t> a;
-    a.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + (16 * h) * stride));
-    a.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + (16 * h + 8) * stride));
+    a.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + Tile<uint16_t, DP>::at(r + 16 * h, d)));
+    a.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + Tile<uint16_t, DP>::at(r + 16 * h + 8, d)));
     acc = mma(a, p.f[h], acc);
   }
   return acc;
 }
-__device__ __forceinline__ f32x16 mma_rows(const float* tile, int stride, int d0, const PFrag32& p, f32x16 acc) {
+template <int DP>
+__device__ __forceinline__ f32x16 mma_rows(const float* tile, int r0, int d0, const PFrag32& p, f32x16 acc) {
   const int l = threadIdx.x & 63, half = l >> 5;
-  const float* at = tile + d0 + (l & 31);
 #pragma unroll
   for (int r = 0; r < 16; ++r)
-    acc = __builtin_amdgcn_mfma_f32_32x32x2f32(at[acc_row(r, half) * stride], p.p[r], acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x2f32(tile[Tile<float, DP>::at(r0 + acc_row(r, half), d0 + (l & 31))], p.p[r],
+                                               acc, 0, 0, 0);
   return acc;
+}
+// A lane's fragment of row r0 + (lane & 31) at the 16-wide step i.
+template <int DP>
+__device__ __forceinline__ Frag<uint16_t> row_frag(const uint16_t* tile, int r0, int i) {
+  const int l = threadIdx.x & 63;
+  return lds_frag(tile + Tile<uint16_t, DP>::at(r0 + (l & 31), 16 * i + 8 * (l >> 5)));
+}
+template <int DP>
+__device__ __forceinline__ Frag<float> row_frag(const float* tile, int r0, int i) {
+  const int l = threadIdx.x & 63, r = r0 + (l & 31), d = 16 * i + 8 * (l >> 5);
+  Frag<float> f;
+  f.u[0] = *reinterpret_cast<const float4*>(tile + Tile<float, DP>::at(r, d));
+  f.u[1] = *reinterpret_cast<const float4*>(tile + Tile<float, DP>::at(r, d + 4));
+  return f;
 }
 
 // ---- host side
 
 struct Plan {
   int dp;        // head size the kernel is built for: 32, 64 or 128
-  int wide;      // 1: four waves of 32 rows share each key tile; 0: four waves split the keys of 32 rows
-  int splits;    // workgroups that share the keys of a row tile
-  int per_split; // key tiles of each
-  int tile;      // keys of a tile
+  bool wide;     // waves of different rows share the key tiles (else waves of the same rows take different keys)
+  int waves;     // of a workgroup
+  int rows;      // rows of a tile
+  int step;      // keys of one step of the inner loop
+  int tiles, full, splits, per_split;
 };
 
 // Descriptor checks of every attention entry point: DCN_OK or a negative dcn_status.
 int check(const dcn_attn_desc* d);
-// 16-byte row accesses are possible for a tensor of these strides at this address
+// 16-byte row accesses at 32-bit offsets are possible for a tensor of these strides at this address
 inline bool vec_ok(const void* p, const int64_t* s, int64_t D, int es) {
   const int64_t n = 16 / es;
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && D % n == 0 && s[0] % n == 0 && s[1] % n == 0 && s[2] % n == 0;
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && D % n == 0 && s[0] % n == 0 && s[1] % n == 0 && s[2] % n == 0 &&
+         s[1] <= int64_t{1} << 22;   // 128 rows within 32 bits of bytes of each other
 }
 void fill_args(const dcn_attn_desc* d, Args* a);
 

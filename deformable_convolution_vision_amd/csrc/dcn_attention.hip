@@ -15,10 +15,12 @@
 // The heads that share a key head are rows of one problem (row r: position r / g, head r % g),
 // so a single token of many heads reads each key once.
 //
-// Two forms of one kernel: `wide`, four waves of 32 rows share a 64-key tile; and narrow, 32
-// rows, four waves take 32 keys each of a 128-key tile and join at the end.  Narrow launches
-// may also split the keys over workgroups: each writes its maximum, sum and undivided output,
-// and attn_join_kernel adds them up in split order.
+// Two forms.  attn_rows_kernel: 128 rows in four waves, which share a ring of key tiles that
+// buffer -> LDS loads fill ahead of use.  attn_few_rows_kernel: 32 rows, whose keys the waves of
+// a workgroup take in turn, each at its own pace, and join at the end.  Where there are fewer
+// row tiles than the chip holds (and for the last, incomplete round of them) the keys of a tile
+// are also split over workgroups: each writes its maximum, sum and undivided output, and
+// attn_join_kernel adds them up in split order.
 //
 // Arithmetic: products of bf16 (exact) or fp32 added in fp32; the softmax in fp32; for bf16
 // the weights exp(s - m) are rounded to bf16 as the second product's operand (their sum is
@@ -29,6 +31,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 
 #include "dcn.h"
 #include "dcn_attention.h"
@@ -37,264 +40,451 @@ namespace dcn {
 namespace attn {
 namespace {
 
-template <typename T, int DP, int WQ, int WK, bool VEC>
-__global__ __launch_bounds__(64 * WQ * WK) void attn_fwd_kernel(Args a) {
-  constexpr int NT = 64 * WQ * WK, KV = Elem<T>::kVec, ST = DP + Elem<T>::kPad;
-  constexpr int SUB = WK == 1 ? 2 : 1;         // 32-key blocks of a tile that one wave takes
-  constexpr int KT = 32 * SUB * WK;            // keys of a tile
-  constexpr int VPR = DP / KV;                 // 16-byte vectors of a row
-  constexpr int NV = KT * VPR / NT;            // of a tile, per thread
-  constexpr int DT = DP / 32;
-  constexpr int OST = DP + 4;                  // LDS row of the joined output
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  T* ks = reinterpret_cast<T*>(smem);
-  T* vs = ks + KT * ST;
-  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, wave = tid >> 6;
-  const int wq = wave / WK, wk = wave % WK;
-  // consecutive workgroups are consecutive (batch, head) pairs: the row tiles that read the
-  // same keys then run on the same XCD when the pairs are a multiple of 8
-  const int nbh = a.B * a.Hkv;
-  int id = blockIdx.x;
-  const int bh = id % nbh;
-  id /= nbh;
-  const int split = id % a.splits, rt = id / a.splits;
-  const int b = bh / a.Hkv, hk = bh % a.Hkv;
-  const T* kp = static_cast<const T*>(a.k) + b * a.ks[0] + hk * a.ks[2];
-  const T* vp = static_cast<const T*>(a.v) + b * a.vs[0] + hk * a.vs[2];
-  const uint8_t* mp = a.mask == nullptr ? nullptr : a.mask + b * a.ms;
-
-  // this lane's row
-  const int row = rt * 32 * WQ + wq * 32 + (lane & 31);
-  Frag<T> qf[DP / 16];
-  {
-    const bool live = row < a.R;
-    const int pos = live ? row / a.g : 0, head = hk * a.g + (live ? row % a.g : 0);
-    const T* qp = static_cast<const T*>(a.q) + b * a.qs[0] + pos * a.qs[1] + head * a.qs[2];
-#pragma unroll
-    for (int i = 0; i < DP / 16; ++i) qf[i] = load_frag<T, VEC>(qp, 16 * i + 8 * half, a.D, live);
+// One workgroup's part of the problem: a tile of rows of one (batch element, key head), and
+// steps s0 .. s1 - 1 of its keys.  Consecutive workgroups are consecutive pairs: the row tiles
+// that read the same keys then run on the same XCD when the pairs are a multiple of 8.
+struct Work {
+  int b, hk, row0, split, tail;   // tail: index of a split tile, or -1
+  int s0, s1;
+};
+__device__ __forceinline__ Work work_of(const Args& a, int rows, int steps) {
+  Work w;
+  int tile = blockIdx.x;
+  w.tail = -1;
+  w.split = 0;
+  w.s0 = 0;
+  w.s1 = steps;
+  if (tile >= a.full) {
+    const int n = a.tiles - a.full, at = tile - a.full;
+    w.tail = at % n;
+    w.split = at / n;
+    tile = a.full + w.tail;
+    w.s0 = w.split * a.per_split;
+    w.s1 = min(steps, w.s0 + a.per_split);
   }
+  const int nbh = a.B * a.Hkv, bh = tile % nbh;
+  w.b = bh / a.Hkv;
+  w.hk = bh % a.Hkv;
+  w.row0 = tile / nbh * rows;
+  return w;
+}
 
-  f32x16 o[DT];
-#pragma unroll
-  for (int i = 0; i < DT; ++i) o[i] = zero_acc();
+// A lane's row in registers.
+template <typename T, int DP, bool VEC>
+__device__ __forceinline__ void load_row(const Args& a, const Work& w, int row, Frag<T> (&f)[DP / 16]) {
+  const bool live = row < a.R;
+  const int pos = live ? row / a.g : 0, head = w.hk * a.g + (live ? row % a.g : 0);
+  load_frags<T, DP, VEC>(static_cast<const T*>(a.q) + w.b * a.qs[0] + pos * a.qs[1] + head * a.qs[2], 0, a.D, live, f);
+}
+
+// A lane's running softmax: the maximum (in powers of two) of its row, and the sum of its own
+// half of the weights.
+struct Running {
   float m = kNegInf, l = 0.f;
+};
 
-  const int tiles = (a.Lk + KT - 1) / KT;
-  const int t0 = split * a.per_split, t1 = min(tiles, t0 + a.per_split);
-  Vec16<T> kr[NV], vr[NV];
-  const auto load_tile = [&](int t) {
+// Scores of keys that do not count become -inf.  The word is the same for all lanes, so which
+// lanes keep register r are two runs of 32 lanes: bit acc_row(r, 0) and, for the upper half,
+// acc_row(r, 1), spread by the scalar unit.
+__device__ __forceinline__ void mask_scores(f32x16& s, uint32_t word) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int at = tid + i * NT, key = t * KT + at / VPR, d = (at % VPR) * KV;
-      bool live = key < a.Lk;
-      kr[i] = load_vec<T, VEC>(kp + key * a.ks[1], d, a.D, live);
-      // a padded key's weight is exactly 0, but 0 times an infinity or NaN in its value row
-      // would not be: such rows are taken as zeros
-      if (mp != nullptr && live) live = mp[key] != 0;
-      vr[i] = load_vec<T, VEC>(vp + key * a.vs[1], d, a.D, live);
-    }
-  };
-  if (t0 < t1) load_tile(t0);
-  for (int t = t0; t < t1; ++t) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int at = tid + i * NT, key = at / VPR, d = (at % VPR) * KV;
-      *reinterpret_cast<uint4*>(ks + key * ST + d) = kr[i].u;
-      *reinterpret_cast<uint4*>(vs + key * ST + d) = vr[i].u;
-    }
-    __syncthreads();
-    if (t + 1 < t1) load_tile(t + 1);
-    // which of the wave's keys count: bit i of word is key k0 + i
-    const int k0 = t * KT + wk * 32 * SUB;
-    uint64_t word;
-    {
-      const int key = k0 + lane;
-      bool live = lane < 32 * SUB && key < a.Lk;
-      if (mp != nullptr && live) live = mp[key] != 0;
-      word = __ballot(live);
-    }
-    if (word == 0) continue;
-    float p[SUB][16];
-    float mt = kNegInf;
-#pragma unroll
-    for (int s = 0; s < SUB; ++s) {
-      f32x16 acc = zero_acc();
-      const T* krow = ks + (wk * 32 * SUB + s * 32 + (lane & 31)) * ST + 8 * half;
-#pragma unroll
-      for (int i = 0; i < DP / 16; ++i) acc = mma(lds_frag(krow + 16 * i), qf[i], acc);
-      const uint32_t w = static_cast<uint32_t>(word >> (32 * s));
-#pragma unroll
-      for (int r = 0; r < 16; ++r) p[s][r] = acc[r];
-      if (w != 0xffffffffu) {
-        const uint32_t wh = w >> (4 * half);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) p[s][r] = (wh >> acc_row(r, 0)) & 1u ? p[s][r] : kNegInf;
-      }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) mt = fmaxf(mt, p[s][r]);
-    }
-    mt = max_halves(mt);
-    const float mn = fmaxf(m, mt * a.c);
-    const float ms = mn == kNegInf ? 0.f : mn;   // no key counted yet: exp2(-inf) = 0 below
-    const float alpha = exp2_fast(m - ms);
-    m = mn;
-    float sum = 0.f;
-#pragma unroll
-    for (int s = 0; s < SUB; ++s)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        p[s][r] = exp2_fast(fmaf(p[s][r], a.c, -ms));
-        sum += p[s][r];
-      }
-    l = fmaf(l, alpha, sum);
-    if (__any(alpha != 1.f)) {
-#pragma unroll
-      for (int i = 0; i < DT; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) o[i][r] *= alpha;
-    }
-#pragma unroll
-    for (int s = 0; s < SUB; ++s) {
-      typename POperand<T>::type pf;
-      to_operand(p[s], pf);
-#pragma unroll
-      for (int i = 0; i < DT; ++i) o[i] = mma_rows(vs + (wk * 32 * SUB + s * 32) * ST, ST, 32 * i, pf, o[i]);
-    }
-  }
-
-  // join the waves that took different keys of the same rows, through LDS (which also turns
-  // the transposed registers into rows)
-  l = sum_halves(l);
-  float* os = reinterpret_cast<float*>(smem);             // [WQ*WK][32][OST]
-  float* ml = os + WQ * WK * 32 * OST;                    // [WQ*WK][32][2]
-  __syncthreads();
-  if (half == 0) {
-    ml[(wave * 32 + lane) * 2] = m;
-    ml[(wave * 32 + lane) * 2 + 1] = l;
-  }
-#pragma unroll
-  for (int i = 0; i < DT; ++i)
-#pragma unroll
-    for (int r4 = 0; r4 < 4; ++r4)
-      *reinterpret_cast<float4*>(os + (wave * 32 + (lane & 31)) * OST + 32 * i + acc_row(4 * r4, half)) =
-          make_float4(o[i][4 * r4], o[i][4 * r4 + 1], o[i][4 * r4 + 2], o[i][4 * r4 + 3]);
-  __syncthreads();
-  constexpr int V4 = DP / 4;
-  for (int at = tid; at < WQ * 32 * V4; at += NT) {
-    const int rr = at / V4, d = (at % V4) * 4, grp = rr / 32, ri = rr % 32;
-    const int orow = rt * 32 * WQ + rr;
-    if (orow >= a.R) continue;
-    float mm = kNegInf, ll = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < WK; ++w) mm = fmaxf(mm, ml[((grp * WK + w) * 32 + ri) * 2]);
-    const float ms = mm == kNegInf ? 0.f : mm;
-#pragma unroll
-    for (int w = 0; w < WK; ++w) {
-      const int slot = (grp * WK + w) * 32 + ri;
-      const float f = exp2_fast(ml[slot * 2] - ms);
-      const float4 v = *reinterpret_cast<const float4*>(os + slot * OST + d);
-      ll = fmaf(f, ml[slot * 2 + 1], ll);
-      acc.x = fmaf(f, v.x, acc.x);
-      acc.y = fmaf(f, v.y, acc.y);
-      acc.z = fmaf(f, v.z, acc.z);
-      acc.w = fmaf(f, v.w, acc.w);
-    }
-    if (a.splits > 1) {
-      const int64_t prow = (static_cast<int64_t>(split) * nbh + bh) * a.R + orow;
-      *reinterpret_cast<float4*>(a.part + prow * DP + d) = acc;
-      if (d == 0) {
-        a.part_ml[prow * 2] = mm;
-        a.part_ml[prow * 2 + 1] = ll;
-      }
-      continue;
-    }
-    const int pos = orow / a.g, head = hk * a.g + orow % a.g;
-    const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);   // no key: zeros; a NaN sum stays NaN
-    T* op = static_cast<T*>(a.out) + ((static_cast<int64_t>(b) * a.Lq + pos) * a.Hq + head) * a.D;
-    const float vals[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (d + j < a.D) op[d + j] = narrow<T>(vals[j]);
-    if (d == 0 && a.lse != nullptr)
-      a.lse[(static_cast<int64_t>(b) * a.Hq + head) * a.Lq + pos] =
-          ll == 0.f ? kNegInf : fmaf(ms, kLn2, logf(ll));
+  for (int r = 0; r < 16; ++r) {
+    const uint32_t lo = (word >> acc_row(r, 0)) & 1u ? 0xffffffffu : 0u, hi = (word >> acc_row(r, 1)) & 1u ? 0xffffffffu : 0u;
+    const uint64_t keep = (static_cast<uint64_t>(hi) << 32) | lo;
+    s[r] = __builtin_amdgcn_inverse_ballot_w64(keep) ? s[r] : kNegInf;
   }
 }
 
-// Adds up the parts of split keys: one thread for 4 elements of a row.
-template <typename T, int DP>
-__global__ __launch_bounds__(256) void attn_join_kernel(Args a) {
-  constexpr int V4 = DP / 4;
-  const int nbh = a.B * a.Hkv;
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t rows = static_cast<int64_t>(nbh) * a.R, prow = at / V4;
-  const int d = static_cast<int>(at % V4) * 4;
-  if (prow >= rows) return;
-  float mm = kNegInf, ll = 0.f;
-  for (int s = 0; s < a.splits; ++s) mm = fmaxf(mm, a.part_ml[(s * rows + prow) * 2]);
-  const float ms = mm == kNegInf ? 0.f : mm;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < a.splits; ++s) {
-    const float f = exp2_fast(a.part_ml[(s * rows + prow) * 2] - ms);
-    const float4 v = *reinterpret_cast<const float4*>(a.part + (s * rows + prow) * DP + d);
-    ll = fmaf(f, a.part_ml[(s * rows + prow) * 2 + 1], ll);
-    acc[0] = fmaf(f, v.x, acc[0]);
-    acc[1] = fmaf(f, v.y, acc[1]);
-    acc[2] = fmaf(f, v.z, acc[2]);
-    acc[3] = fmaf(f, v.w, acc[3]);
+// Takes N blocks of 32 scores in (raw products; word: the attended keys of each), gives the
+// weights as the second product's operands, and rescales the output accumulators when the
+// maximum rises.  Maximum and sum run in four strands each: one would wait for itself.
+template <typename T, int N, int DT>
+__device__ __forceinline__ void softmax_step(f32x16 (&s)[N], const uint32_t (&word)[N], float c, Running& run,
+                                             f32x16 (&o)[DT], typename POperand<T>::type (&pf)[N]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    if (word[n] != 0xffffffffu) mask_scores(s[n], word[n]);
+  float mt[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) mt[j] = fmaxf(s[0][4 * j], s[0][4 * j + 1]);
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (n > 0) mt[j] = max3(mt[j], s[n][4 * j], s[n][4 * j + 1]);
+      mt[j] = max3(mt[j], s[n][4 * j + 2], s[n][4 * j + 3]);
+    }
+  const float mn = fmaxf(run.m, max_halves(fmaxf(max3(mt[0], mt[1], mt[2]), mt[3])) * c);
+  if (__any(mn != run.m)) {
+    const float alpha = run.m == kNegInf ? 0.f : exp2_fast(run.m - mn);
+    run.m = mn;
+    run.l *= alpha;
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[i][r] *= alpha;
   }
-  const int bh = static_cast<int>(prow / a.R), r = static_cast<int>(prow % a.R);
-  const int b = bh / a.Hkv, pos = r / a.g, head = (bh % a.Hkv) * a.g + r % a.g;
-  const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);
-  T* op = static_cast<T*>(a.out) + ((static_cast<int64_t>(b) * a.Lq + pos) * a.Hq + head) * a.D;
+  const float ms = run.m == kNegInf ? 0.f : run.m;   // no key counted yet: exp2(-inf) = 0
+  float sum[4] = {run.l, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    float p[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      p[r] = exp2_fast(fmaf(s[n][r], c, -ms));
+      sum[r & 3] += p[r];
+    }
+    to_operand(p, pf[n]);
+  }
+  run.l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+}
+
+// Writes 4 elements of a finished row, or its part.
+template <typename T, int DP>
+__device__ __forceinline__ void put4(const Args& a, const Work& w, int rows, int rr, int d, float m, float l, float4 v) {
+  const int row = w.row0 + rr;
+  if (row >= a.R) return;
+  if (w.tail >= 0) {
+    const int64_t prow = (static_cast<int64_t>(w.tail) * a.splits + w.split) * rows + rr;
+    *reinterpret_cast<float4*>(a.part + prow * DP + d) = v;
+    if (d == 0) *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(m, l);
+    return;
+  }
+  const int pos = row / a.g, head = w.hk * a.g + row % a.g;
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // no key: zeros; a NaN sum stays NaN
+  T* op = static_cast<T*>(a.out) + ((static_cast<int64_t>(w.b) * a.Lq + pos) * a.Hq + head) * a.D;
+  const float vals[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    if (d + j < a.D) op[d + j] = narrow<T>(acc[j] * inv);
+    if (d + j < a.D) op[d + j] = narrow<T>(vals[j]);
   if (d == 0 && a.lse != nullptr)
-    a.lse[(static_cast<int64_t>(b) * a.Hq + head) * a.Lq + pos] = ll == 0.f ? kNegInf : fmaf(ms, kLn2, logf(ll));
+    a.lse[(static_cast<int64_t>(w.b) * a.Hq + head) * a.Lq + pos] =
+        l == 0.f ? kNegInf : fmaf(m == kNegInf ? 0.f : m, kLn2, logf(l));
+}
+
+// Joins the W waves that took different keys of the same 32 rows, 32 elements of the head at a
+// time, through LDS (which also turns the transposed registers into rows).  Called by all waves
+// of the workgroup, G groups of W; `rr0`: the group's first row in the tile.
+template <typename T, int DP, int W, int G, int DT>
+__device__ __forceinline__ void join_waves(const Args& a, const Work& w, int rows, float m, float l,
+                                           const f32x16 (&o)[DT], unsigned char* smem) {
+  constexpr int OST = 36, NT = 64 * W * G;
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  float* os = reinterpret_cast<float*>(smem);             // [G][W][32][OST]
+  float* fs = os + G * W * 32 * OST;                      // [G][W][32] maxima, then each wave's factor
+  float* ls = fs + G * W * 32;                            // [G][W][32] sums
+  __syncthreads();
+  if (half == 0) {
+    fs[wave * 32 + lane] = m;
+    ls[wave * 32 + lane] = l;
+  }
+  float mm = kNegInf, ll = 0.f;                            // of the row that this thread writes
+  constexpr int RT = G * 32 * 8;                          // threads that write: 4 elements each
+  float f[W];
+#pragma unroll
+  for (int i = 0; i < DT; ++i) {
+    if (i > 0) __syncthreads();
+#pragma unroll
+    for (int r4 = 0; r4 < 4; ++r4)
+      *reinterpret_cast<float4*>(os + (wave * 32 + (lane & 31)) * OST + acc_row(4 * r4, half)) =
+          make_float4(o[i][4 * r4], o[i][4 * r4 + 1], o[i][4 * r4 + 2], o[i][4 * r4 + 3]);
+    __syncthreads();
+#pragma unroll
+    for (int at = tid; at < RT; at += NT) {
+      const int rr = at / 8, d = (at % 8) * 4, g = rr / 32, ri = rr % 32;
+      if (i == 0 || RT > NT) {
+        mm = kNegInf;
+        ll = 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) mm = fmaxf(mm, fs[(g * W + j) * 32 + ri]);
+        const float ms = mm == kNegInf ? 0.f : mm;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          f[j] = exp2_fast(fs[(g * W + j) * 32 + ri] - ms);
+          ll = fmaf(f[j], ls[(g * W + j) * 32 + ri], ll);
+        }
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const float4 v = *reinterpret_cast<const float4*>(os + ((g * W + j) * 32 + ri) * OST + d);
+        acc.x = fmaf(f[j], v.x, acc.x);
+        acc.y = fmaf(f[j], v.y, acc.y);
+        acc.z = fmaf(f[j], v.z, acc.z);
+        acc.w = fmaf(f[j], v.w, acc.w);
+      }
+      put4<T, DP>(a, w, rows, rr, 32 * i + d, mm, ll, acc);
+    }
+  }
+}
+constexpr size_t join_lds(int waves) { return static_cast<size_t>(waves) * 32 * (36 + 2) * 4; }
+
+// 32 rows; the W waves of a workgroup take every W-th block of 32 keys and join at the end, so
+// no wave waits for another inside the loop.  A lane's key row comes straight from memory as
+// the first product's operand; values go through two places in the LDS that are the wave's own.
+// The next block's rows are on their way while one is worked on.
+template <typename T, int DP, int W, bool VEC>
+__global__ __launch_bounds__(64 * W) void attn_few_rows_kernel(Args a) {
+  constexpr int DT = DP / 32, KL = DP * static_cast<int>(sizeof(T)) / 32, VL = 32 * Tile<T, DP>::kVecs / 64;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  T* const lds = reinterpret_cast<T*>(smem) + wave * 2 * 32 * DP;
+  const Work w = work_of(a, 32, (a.Lk + 32 * W - 1) / (32 * W));
+  const T* kp = static_cast<const T*>(a.k) + w.b * a.ks[0] + w.hk * a.ks[2];
+  const T* vp = static_cast<const T*>(a.v) + w.b * a.vs[0] + w.hk * a.vs[2];
+  const uint8_t* mp = a.mask == nullptr ? nullptr : a.mask + w.b * a.ms;
+  Frag<T> qf[DP / 16];
+  load_row<T, DP, VEC>(a, w, w.row0 + (lane & 31), qf);
+  f32x16 o[DT];
+#pragma unroll
+  for (int i = 0; i < DT; ++i) o[i] = zero_acc();
+  Running run;
+
+  Frag<T> kf[DP / 16], kn[DP / 16];
+  // Rows of padded keys are taken as zeros and not read: a padded key's weight is exactly 0,
+  // but 0 times an infinity or NaN in its value row would not be.
+  const auto load_keys = [&](int64_t k0, uint32_t word, Frag<T> (&f)[DP / 16]) {
+    const bool in = (word >> (lane & 31)) & 1u;
+    if constexpr (VEC) {
+      const __amdgpu_buffer_rsrc_t rs = rsrc_of(kp + k0 * a.ks[1]);
+      const uint32_t ofs = (static_cast<uint32_t>(lane & 31) * static_cast<uint32_t>(a.ks[1]) + 8 * half) *
+                           static_cast<uint32_t>(sizeof(T));
+#pragma unroll
+      for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+        for (int h = 0; h < static_cast<int>(sizeof(T)) / 2; ++h) {
+          const bool at = in && 16 * i + 8 * half + h * Elem<T>::kVec < a.D;
+          const auto u = __builtin_amdgcn_raw_buffer_load_b128(
+              rs, at ? ofs + 16 * i * static_cast<uint32_t>(sizeof(T)) + 16 * h : kOutside, 0, 0);
+          __builtin_memcpy(reinterpret_cast<char*>(&f[i]) + 16 * h, &u, 16);
+        }
+    } else {
+      load_frags<T, DP, false>(kp + k0 * a.ks[1], (lane & 31) * a.ks[1], a.D, in, f);
+    }
+  };
+  const auto load_values = [&](int64_t k0, uint32_t word, int slot) {
+    fetch_tile<T, DP, 32, 64, VEC>(lds + slot * 32 * DP, vp + k0 * a.vs[1], a.vs[1], word, a.D, lane);
+  };
+
+  const int64_t step = 32 * W, end = w.s1 * step;
+  for (int64_t win = w.s0 * step + 32 * wave; win < end && win < a.Lk; win += 64 * step) {
+    const uint32_t words = key_words(mp, win, step, end, a.Lk);
+    uint64_t live = __ballot(words != 0);
+    int at = live ? __builtin_ctzll(live) : 0, slot = 0;
+    uint32_t word[1] = {static_cast<uint32_t>(__builtin_amdgcn_readlane(words, at))};
+    if (live) {
+      load_keys(win + at * step, word[0], kf);
+      load_values(win + at * step, word[0], 0);
+    }
+    while (live) {
+      live &= live - 1;
+      at = live ? __builtin_ctzll(live) : 0;
+      const uint32_t word_next = __builtin_amdgcn_readlane(words, at);
+      if (live) {
+        load_keys(win + at * step, word_next, kn);
+        load_values(win + at * step, word_next, slot ^ 1);
+      }
+      f32x16 s[1] = {zero_acc()};
+#pragma unroll
+      for (int i = 0; i < DP / 16; ++i) s[0] = mma(kf[i], qf[i], s[0]);
+      typename POperand<T>::type pf[1];
+      softmax_step<T>(s, word, a.c, run, o, pf);
+      // this block's values are there when only the next block's loads are under way
+      if constexpr (VEC) {
+        if (live) wait_loads<KL + VL>();
+        else wait_loads<0>();
+      }
+#pragma unroll
+      for (int i = 0; i < DT; ++i) o[i] = mma_rows<DP>(lds + slot * 32 * DP, 0, 32 * i, pf[0], o[i]);
+#pragma unroll
+      for (int i = 0; i < DP / 16; ++i) kf[i] = kn[i];
+      word[0] = word_next;
+      slot ^= 1;
+    }
+  }
+  join_waves<T, DP, W, 1>(a, w, 32, run.m, sum_halves(run.l), o, smem);
+}
+
+// Waves of a SIMD that the rows form leaves registers for (accumulators then stay in the ordinary
+// registers: with more of them than needed the compiler moves them to the others and back).
+constexpr int waves_per_simd(int row_bytes) { return row_bytes <= 64 ? 4 : row_bytes <= 128 ? 3 : row_bytes <= 256 ? 2 : 1; }
+
+// Rows of 128 in four waves, which share a ring of STAGES key tiles of 64 in the LDS: while one
+// is worked on, the next STAGES - 1 are on their way.
+template <typename T, int DP, int STAGES, bool VEC>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(waves_per_simd(sizeof(T) * DP)))) void attn_rows_kernel(Args a) {
+  constexpr int KT = 64, DT = DP / 32, BUF = 2 * KT * DP, LOADS = 2 * KT * Tile<T, DP>::kVecs / 256, AHEAD = STAGES - 1;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  T* const lds = reinterpret_cast<T*>(smem);              // [STAGES][keys, values][KT][DP]
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const Work w = work_of(a, 128, (a.Lk + KT - 1) / KT);
+  const T* kp = static_cast<const T*>(a.k) + w.b * a.ks[0] + w.hk * a.ks[2];
+  const T* vp = static_cast<const T*>(a.v) + w.b * a.vs[0] + w.hk * a.vs[2];
+  const uint8_t* mp = a.mask == nullptr ? nullptr : a.mask + w.b * a.ms;
+  Frag<T> qf[DP / 16];
+  load_row<T, DP, VEC>(a, w, w.row0 + wave * 32 + (lane & 31), qf);
+  f32x16 o[DT];
+#pragma unroll
+  for (int i = 0; i < DT; ++i) o[i] = zero_acc();
+  Running run;
+
+  int win = w.s0;               // the 32 tiles whose mask words the lanes hold start here
+  uint32_t words = 0;
+  const auto fill = [&](int t) {
+    win = t;
+    words = key_words(mp, static_cast<int64_t>(t) * KT, 32, static_cast<int64_t>(w.s1) * KT, a.Lk);
+  };
+  int t = w.s0;                 // the next tile to look at
+  // the next tile that holds an attended key (the same for every wave) is sent for; its mask
+  // bits, or 0 when there is none
+  const auto send = [&](int slot) {
+    uint64_t word = 0;
+    for (; t < w.s1 && word == 0; ++t) {
+      if (t >= win + 32) fill(t);
+      const int i = 2 * (t - win);
+      word = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(words, i))) |
+             static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(words, i + 1))) << 32;
+    }
+    if (word != 0) {
+      const int64_t k0 = static_cast<int64_t>(t - 1) * KT;
+      fetch_tile<T, DP, KT, 256, VEC>(lds + slot * BUF, kp + k0 * a.ks[1], a.ks[1], word, a.D, tid);
+      fetch_tile<T, DP, KT, 256, VEC>(lds + slot * BUF + KT * DP, vp + k0 * a.vs[1], a.vs[1], word, a.D, tid);
+    }
+    return word;
+  };
+  fill(w.s0);
+  uint64_t word[AHEAD + 1];
+#pragma unroll
+  for (int j = 0; j < AHEAD; ++j) word[j] = send(j);
+  int slot = 0;
+  while (word[0] != 0) {
+    // this wave's share of the tile is there when only the later tiles' loads are under way
+    if constexpr (AHEAD == 2) {
+      if (word[1] != 0) wait_loads<LOADS>();
+      else wait_loads<0>();
+    } else {
+      wait_loads<0>();
+    }
+    lds_barrier();              // the other waves' shares too; and the tile before is no longer read
+    word[AHEAD] = send(slot == 0 ? STAGES - 1 : slot - 1);
+    const T* ks = lds + slot * BUF;
+    const T* vs = ks + KT * DP;
+    f32x16 s[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      s[n] = zero_acc();
+#pragma unroll
+      for (int i = 0; i < DP / 16; ++i) s[n] = mma(row_frag<DP>(ks, 32 * n, i), qf[i], s[n]);
+    }
+    const uint32_t both[2] = {static_cast<uint32_t>(word[0]), static_cast<uint32_t>(word[0] >> 32)};
+    typename POperand<T>::type pf[2];
+    softmax_step<T>(s, both, a.c, run, o, pf);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < DT; ++i) o[i] = mma_rows<DP>(vs, 32 * n, 32 * i, pf[n], o[i]);
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) word[j] = word[j + 1];
+    slot = slot == STAGES - 1 ? 0 : slot + 1;
+  }
+  join_waves<T, DP, 1, 4>(a, w, 128, run.m, sum_halves(run.l), o, smem);
+}
+
+// Adds up the parts of split tiles: one thread for 4 elements of a row.
+template <typename T, int DP>
+__global__ __launch_bounds__(256) void attn_join_kernel(Args a, int rows) {
+  constexpr int V4 = DP / 4;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, prow = at / V4;
+  Work w;
+  const int tail = static_cast<int>(prow / rows), rr = static_cast<int>(prow % rows), tile = a.full + tail;
+  if (tile >= a.tiles) return;
+  const int nbh = a.B * a.Hkv, bh = tile % nbh, d = static_cast<int>(at % V4) * 4;
+  w.b = bh / a.Hkv;
+  w.hk = bh % a.Hkv;
+  w.row0 = tile / nbh * rows;
+  w.tail = -1;
+  if (w.row0 + rr >= a.R) return;
+  const int64_t p0 = static_cast<int64_t>(tail) * a.splits * rows + rr;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + p0;
+  const float* part = a.part + p0 * DP + d;
+  float mm = kNegInf, ll = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) mm = fmaxf(mm, ml[static_cast<int64_t>(s) * rows].x);
+  const float ms = mm == kNegInf ? 0.f : mm;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) {
+    const float2 x = ml[static_cast<int64_t>(s) * rows];
+    const float f = exp2_fast(x.x - ms);
+    const float4 v = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(s) * rows * DP);
+    ll = fmaf(f, x.y, ll);
+    acc.x = fmaf(f, v.x, acc.x);
+    acc.y = fmaf(f, v.y, acc.y);
+    acc.z = fmaf(f, v.z, acc.z);
+    acc.w = fmaf(f, v.w, acc.w);
+  }
+  put4<T, DP>(a, w, rows, rr, d, mm, ll, acc);
 }
 
 constexpr int kCUs = 256;
 
+// Waves of the few-rows form: as many as the registers of a CU hold at this head size.
+template <typename T, int DP>
+constexpr int kWaves = sizeof(T) == 2 ? (DP == 32 ? 16 : 8) : (DP == 128 ? 4 : DP == 64 ? 8 : 16);
+
+int waves_of(int es, int dp) { return es == 2 ? (dp == 32 ? 16 : 8) : (dp == 128 ? 4 : dp == 64 ? 8 : 16); }
+
 Plan make_plan(const dcn_attn_desc* d) {
   Plan p{};
+  const int es = d->dtype == DCN_BF16 ? 2 : 4;
   p.dp = d->head_dim <= 32 ? 32 : d->head_dim <= 64 ? 64 : 128;
   const int64_t nbh = d->batch * d->key_heads, R = d->query_len * (d->query_heads / d->key_heads);
-  p.wide = R > 96 && nbh * ((R + 127) / 128) >= 2 * kCUs;
-  p.tile = p.wide ? 64 : 128;
-  const int64_t tiles = std::max<int64_t>(1, (d->key_len + p.tile - 1) / p.tile);
-  int64_t splits = 1;
-  if (!p.wide) {
-    const int64_t groups = nbh * ((R + 31) / 32);
-    splits = std::min<int64_t>(std::max<int64_t>(1, 2 * kCUs / groups), std::max<int64_t>(1, tiles / 2));
+  const int64_t few = nbh * ((R + 31) / 32);
+  p.wide = R > 96 && few > 2 * kCUs;
+  int64_t want = 0;
+  if (const char* f = std::getenv("DCN_ATTN_FORM")) {   // "rows" or "few", and a number of splits
+    if (f[0] == 'r') p.wide = true;
+    if (f[0] == 'f') p.wide = false;
+    while (*f != '\0' && (*f < '0' || *f > '9')) ++f;
+    want = std::atoi(f);
   }
-  p.per_split = static_cast<int>((tiles + splits - 1) / splits);
-  p.splits = static_cast<int>((tiles + p.per_split - 1) / p.per_split);
+  p.waves = p.wide ? 4 : waves_of(es, p.dp);
+  p.rows = p.wide ? 128 : 32;
+  p.step = p.wide ? 64 : 32 * p.waves;
+  const int64_t tiles = nbh * ((R + p.rows - 1) / p.rows);
+  const int64_t steps = std::max<int64_t>(1, (d->key_len + p.step - 1) / p.step);
+  const int64_t slots = p.wide ? 2 * kCUs : 2 * kCUs * 8 / p.waves;
+  p.tiles = static_cast<int>(tiles);
+  int64_t full = tiles / slots * slots, tail = tiles - full;
+  int64_t splits = tail == 0 ? 1 : std::min<int64_t>(slots / tail, std::max<int64_t>(1, steps / 2));
+  if (want > 0) splits = std::min(want, steps);
+  p.per_split = static_cast<int>((steps + splits - 1) / splits);
+  p.splits = static_cast<int>((steps + p.per_split - 1) / p.per_split);
+  p.full = static_cast<int>(p.splits > 1 ? full : tiles);
   return p;
 }
 
+// Key tiles in the LDS of the rows form: three, where two workgroups of a CU have room for them.
+constexpr int stages_of(int es, int dp) { return es * dp <= 128 ? 3 : 2; }
+
 size_t lds_bytes(const Plan& p, int es) {
-  const int pad = es == 2 ? 16 : 4;
-  const size_t tile = static_cast<size_t>(2) * p.tile * (p.dp + pad) * es;
-  const size_t join = static_cast<size_t>(4) * 32 * (p.dp + 4 + 2) * 4;
-  return std::max(tile, join);
+  const size_t row = static_cast<size_t>(p.dp) * es;
+  return std::max((p.wide ? stages_of(es, p.dp) * 2 * 64 : p.waves * 2 * 32) * row, join_lds(p.waves));
 }
 
-size_t part_bytes(const dcn_attn_desc* d, const Plan& p, size_t* ml_at) {
-  const size_t rows = static_cast<size_t>(p.splits) * d->batch * d->query_heads * d->query_len;
-  *ml_at = (rows * p.dp * 4 + 255) / 256 * 256;
-  return p.splits > 1 ? *ml_at + (rows * 8 + 255) / 256 * 256 : 0;
+size_t part_bytes(const Plan& p, size_t* ml_at) {
+  const size_t rows = static_cast<size_t>(p.tiles - p.full) * p.splits * p.rows;
+  *ml_at = rows * p.dp * 4;
+  return (*ml_at + rows * 8 + 255) / 256 * 256;
 }
 
 template <typename T, int DP>
 const void* fwd_kernel(bool wide, bool vec) {
   if (wide)
-    return vec ? reinterpret_cast<const void*>(&attn_fwd_kernel<T, DP, 4, 1, true>)
-               : reinterpret_cast<const void*>(&attn_fwd_kernel<T, DP, 4, 1, false>);
-  return vec ? reinterpret_cast<const void*>(&attn_fwd_kernel<T, DP, 1, 4, true>)
-             : reinterpret_cast<const void*>(&attn_fwd_kernel<T, DP, 1, 4, false>);
+    return vec ? reinterpret_cast<const void*>(&attn_rows_kernel<T, DP, stages_of(sizeof(T), DP), true>)
+               : reinterpret_cast<const void*>(&attn_rows_kernel<T, DP, stages_of(sizeof(T), DP), false>);
+  return vec ? reinterpret_cast<const void*>(&attn_few_rows_kernel<T, DP, kWaves<T, DP>, true>)
+             : reinterpret_cast<const void*>(&attn_few_rows_kernel<T, DP, kWaves<T, DP>, false>);
 }
 template <typename T>
 const void* fwd_kernel(int dp, bool wide, bool vec) {
@@ -361,7 +551,7 @@ extern "C" int dcn_cross_attention_workspace_bytes(const dcn_attn_desc* d, size_
     return DCN_OK;
   }
   size_t at;
-  *bytes = dcn::attn::part_bytes(d, dcn::attn::make_plan(d), &at);
+  *bytes = dcn::attn::part_bytes(dcn::attn::make_plan(d), &at);
   return DCN_OK;
 }
 
@@ -375,7 +565,7 @@ extern "C" int dcn_cross_attention(const dcn_attn_desc* d, const void* q, const 
   if (q == nullptr || out == nullptr || (d->key_len > 0 && (k == nullptr || v == nullptr))) return DCN_E_ARG;
   const Plan p = make_plan(d);
   size_t ml_at;
-  const size_t need = part_bytes(d, p, &ml_at);
+  const size_t need = part_bytes(p, &ml_at);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 256 != 0))
     return DCN_E_WORKSPACE;
   Args a{};
@@ -386,6 +576,8 @@ extern "C" int dcn_cross_attention(const dcn_attn_desc* d, const void* q, const 
   a.mask = key_mask;
   a.out = out;
   a.lse = lse;
+  a.tiles = p.tiles;
+  a.full = p.full;
   a.splits = p.splits;
   a.per_split = p.per_split;
   if (need > 0) {
@@ -396,16 +588,20 @@ extern "C" int dcn_cross_attention(const dcn_attn_desc* d, const void* q, const 
   const int es = bf16 ? 2 : 4;
   const bool vec = vec_ok(q, d->q_stride, d->head_dim, es) && vec_ok(k, d->k_stride, d->head_dim, es) &&
                    vec_ok(v, d->v_stride, d->head_dim, es);
-  const int rows = p.wide ? 128 : 32;
-  const int64_t grid = static_cast<int64_t>(a.B) * a.Hkv * ((a.R + rows - 1) / rows) * p.splits;
+  const int tail = p.tiles - p.full;
+  const int64_t grid = p.full + static_cast<int64_t>(tail) * p.splits;
   void* args[] = {&a};
   const void* fn = bf16 ? fwd_kernel<uint16_t>(p.dp, p.wide, vec) : fwd_kernel<float>(p.dp, p.wide, vec);
-  if (hipLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(256), args, lds_bytes(p, es), stream) != hipSuccess)
+  if (hipLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(64 * p.waves), args,
+                      lds_bytes(p, es), stream) !=
+      hipSuccess)
     return DCN_E_HIP;
-  if (p.splits > 1) {
-    const int64_t n = static_cast<int64_t>(a.B) * a.Hkv * a.R * (p.dp / 4);
+  if (tail > 0) {
+    const int64_t n = static_cast<int64_t>(tail) * p.rows * (p.dp / 4);
+    int rows = p.rows;
+    void* join_args[] = {&a, &rows};
     fn = bf16 ? join_kernel<uint16_t>(p.dp) : join_kernel<float>(p.dp);
-    if (hipLaunchKernel(fn, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), args, 0, stream) != hipSuccess)
+    if (hipLaunchKernel(fn, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), join_args, 0, stream) != hipSuccess)
       return DCN_E_HIP;
   }
   return DCN_OK;

@@ -100,7 +100,7 @@ __device__ __forceinline__ void store4(T* p, int d, int D, float4 v, float f) {
 
 template <typename T, int DP, int WQ, int WK, bool VEC>
 __global__ __launch_bounds__(64 * WQ * WK) void attn_dq_kernel(Args a) {
-  constexpr int NT = 64 * WQ * WK, KV = Elem<T>::kVec, ST = DP + Elem<T>::kPad;
+  constexpr int NT = 64 * WQ * WK, KV = Elem<T>::kVec, ST = DP;
   constexpr int SUB = WK == 1 ? 2 : 1, KT = 32 * SUB * WK, VPR = DP / KV, NV = KT * VPR / NT, DT = DP / 32;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   T* ks = reinterpret_cast<T*>(smem);
@@ -125,11 +125,8 @@ __global__ __launch_bounds__(64 * WQ * WK) void attn_dq_kernel(Args a) {
     const int pos = live ? row / a.g : 0, head = hk * a.g + (live ? row % a.g : 0);
     const T* qp = static_cast<const T*>(a.q) + b * a.qs[0] + pos * a.qs[1] + head * a.qs[2];
     const T* gp = static_cast<const T*>(a.dout) + ((static_cast<int64_t>(b) * a.Lq + pos) * a.Hq + head) * a.D;
-#pragma unroll
-    for (int i = 0; i < DP / 16; ++i) {
-      qf[i] = load_frag<T, VEC>(qp, 16 * i + 8 * half, a.D, live);
-      gf[i] = load_frag<T, VEC>(gp, 16 * i + 8 * half, a.D, live);
-    }
+    load_frags<T, DP, VEC>(qp, 0, a.D, live, qf);
+    load_frags<T, DP, VEC>(gp, 0, a.D, live, gf);
     if (live) {
       const int64_t prow = static_cast<int64_t>(bh) * a.R + row;
       lse2 = a.delta[prow * 2];
@@ -150,8 +147,8 @@ __global__ __launch_bounds__(64 * WQ * WK) void attn_dq_kernel(Args a) {
       // rows of padded keys are taken as zeros: their weight is 0, and 0 times a NaN is none
       bool live = key < a.Lk;
       if (mp != nullptr && live) live = mp[key] != 0;
-      kr[i] = load_vec<T, VEC>(kp + key * a.ks[1], d, a.D, live);
-      vr[i] = load_vec<T, VEC>(vp + key * a.vs[1], d, a.D, live);
+      kr[i] = load_vec<T, VEC>(kp + key * a.ks[1], 0, d, a.D, live);
+      vr[i] = load_vec<T, VEC>(vp + key * a.vs[1], 0, d, a.D, live);
     }
   };
   if (t0 < t1) load_tile(t0);
@@ -160,8 +157,8 @@ __global__ __launch_bounds__(64 * WQ * WK) void attn_dq_kernel(Args a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int at = tid + i * NT, key = at / VPR, d = (at % VPR) * KV;
-      *reinterpret_cast<uint4*>(ks + key * ST + d) = kr[i].u;
-      *reinterpret_cast<uint4*>(vs + key * ST + d) = vr[i].u;
+      *reinterpret_cast<uint4*>(ks + Tile<T, DP>::at(key, d)) = kr[i].u;
+      *reinterpret_cast<uint4*>(vs + Tile<T, DP>::at(key, d)) = vr[i].u;
     }
     __syncthreads();
     if (t + 1 < t1) load_tile(t + 1);
@@ -179,12 +176,10 @@ __global__ __launch_bounds__(64 * WQ * WK) void attn_dq_kernel(Args a) {
       if (w == 0) continue;
       const int r0 = wk * 32 * SUB + s * 32;
       f32x16 sa = zero_acc(), pa = zero_acc();
-      const T* krow = ks + (r0 + (lane & 31)) * ST + 8 * half;
-      const T* vrow = vs + (r0 + (lane & 31)) * ST + 8 * half;
 #pragma unroll
       for (int i = 0; i < DP / 16; ++i) {
-        sa = mma(lds_frag(krow + 16 * i), qf[i], sa);
-        pa = mma(lds_frag(vrow + 16 * i), gf[i], pa);
+        sa = mma(row_frag<DP>(ks, r0, i), qf[i], sa);
+        pa = mma(row_frag<DP>(vs, r0, i), gf[i], pa);
       }
       float ds[16];
       const uint32_t wh = w >> (4 * half);
@@ -196,7 +191,7 @@ __global__ __launch_bounds__(64 * WQ * WK) void attn_dq_kernel(Args a) {
       typename POperand<T>::type pf;
       to_operand(ds, pf);
 #pragma unroll
-      for (int i = 0; i < DT; ++i) o[i] = mma_rows(ks + r0 * ST, ST, 32 * i, pf, o[i]);
+      for (int i = 0; i < DT; ++i) o[i] = mma_rows<DP>(ks, r0, 32 * i, pf, o[i]);
     }
   }
   join_sum<DP, WQ, WK>(o, reinterpret_cast<float*>(smem), [&](int rr, int d, float4 v) {
@@ -217,7 +212,7 @@ __global__ __launch_bounds__(64 * WQ * WK) void attn_dq_kernel(Args a) {
 // tile and the same keys.
 template <typename T, int DP, int WC, int WS, bool VEC>
 __global__ __launch_bounds__(64 * WC * WS) void attn_dkv_kernel(Args a) {
-  constexpr int NT = 64 * WC * WS, KV = Elem<T>::kVec, ST = DP + Elem<T>::kPad;
+  constexpr int NT = 64 * WC * WS, KV = Elem<T>::kVec, ST = DP;
   constexpr int SUB = WS == 1 ? 2 : 1, RT = 32 * SUB * WS, VPR = DP / KV, NV = RT * VPR / NT, DT = DP / 32;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   T* qs = reinterpret_cast<T*>(smem);
@@ -241,11 +236,8 @@ __global__ __launch_bounds__(64 * WC * WS) void attn_dkv_kernel(Args a) {
   {
     const T* kp = static_cast<const T*>(a.k) + b * a.ks[0] + hk * a.ks[2] + (live ? key : 0) * a.ks[1];
     const T* vp = static_cast<const T*>(a.v) + b * a.vs[0] + hk * a.vs[2] + (live ? key : 0) * a.vs[1];
-#pragma unroll
-    for (int i = 0; i < DP / 16; ++i) {
-      kf[i] = load_frag<T, VEC>(kp, 16 * i + 8 * half, a.D, live);
-      vf[i] = load_frag<T, VEC>(vp, 16 * i + 8 * half, a.D, live);
-    }
+    load_frags<T, DP, VEC>(kp, 0, a.D, live, kf);
+    load_frags<T, DP, VEC>(vp, 0, a.D, live, vf);
   }
   f32x16 ok[DT], ov[DT];
 #pragma unroll
@@ -266,8 +258,8 @@ __global__ __launch_bounds__(64 * WC * WS) void attn_dkv_kernel(Args a) {
       const int at = tid + i * NT, row = t * RT + at / VPR, d = (at % VPR) * KV;
       const bool in = row < a.R;
       const int pos = in ? row / a.g : 0, head = hk * a.g + (in ? row % a.g : 0);
-      qr[i] = load_vec<T, VEC>(qp + pos * a.qs[1] + head * a.qs[2], d, a.D, in);
-      gr[i] = load_vec<T, VEC>(gp + (static_cast<int64_t>(pos) * a.Hq + head) * a.D, d, a.D, in);
+      qr[i] = load_vec<T, VEC>(qp + pos * a.qs[1] + head * a.qs[2], 0, d, a.D, in);
+      gr[i] = load_vec<T, VEC>(gp + (static_cast<int64_t>(pos) * a.Hq + head) * a.D, 0, d, a.D, in);
     }
     if (tid < 2 * RT) {
       const int row = t * RT + (tid >> 1);
@@ -282,8 +274,8 @@ __global__ __launch_bounds__(64 * WC * WS) void attn_dkv_kernel(Args a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int at = tid + i * NT, row = at / VPR, d = (at % VPR) * KV;
-      *reinterpret_cast<uint4*>(qs + row * ST + d) = qr[i].u;
-      *reinterpret_cast<uint4*>(gs + row * ST + d) = gr[i].u;
+      *reinterpret_cast<uint4*>(qs + Tile<T, DP>::at(row, d)) = qr[i].u;
+      *reinterpret_cast<uint4*>(gs + Tile<T, DP>::at(row, d)) = gr[i].u;
     }
     if (tid < 2 * RT) ls[(tid & 1) * RT + (tid >> 1)] = lr;
     __syncthreads();
@@ -293,12 +285,10 @@ __global__ __launch_bounds__(64 * WC * WS) void attn_dkv_kernel(Args a) {
     for (int s = 0; s < SUB; ++s) {
       const int r0 = wr * 32 * SUB + s * 32;
       f32x16 sa = zero_acc(), pa = zero_acc();
-      const T* qrow = qs + (r0 + (lane & 31)) * ST + 8 * half;
-      const T* grow = gs + (r0 + (lane & 31)) * ST + 8 * half;
 #pragma unroll
       for (int i = 0; i < DP / 16; ++i) {
-        sa = mma(lds_frag(qrow + 16 * i), kf[i], sa);
-        pa = mma(lds_frag(grow + 16 * i), vf[i], pa);
+        sa = mma(row_frag<DP>(qs, r0, i), kf[i], sa);
+        pa = mma(row_frag<DP>(gs, r0, i), vf[i], pa);
       }
       float p[16], ds[16];
 #pragma unroll
@@ -318,8 +308,8 @@ __global__ __launch_bounds__(64 * WC * WS) void attn_dkv_kernel(Args a) {
       to_operand(ds, df);
 #pragma unroll
       for (int i = 0; i < DT; ++i) {
-        ov[i] = mma_rows(gs + r0 * ST, ST, 32 * i, pf, ov[i]);
-        ok[i] = mma_rows(qs + r0 * ST, ST, 32 * i, df, ok[i]);
+        ov[i] = mma_rows<DP>(gs, r0, 32 * i, pf, ov[i]);
+        ok[i] = mma_rows<DP>(qs, r0, 32 * i, df, ok[i]);
       }
     }
   }
@@ -372,9 +362,12 @@ __global__ __launch_bounds__(256) void attn_add_kernel(Args a) {
 
 constexpr int kCUs = 256;
 
+struct GradPlan {
+  int dp, wide, splits, per_split, tile;
+};
 // `outer` rows (or keys) held by the waves, `inner` looped over.
-Plan make_plan(int64_t nbh, int64_t outer, int64_t inner, int64_t D) {
-  Plan p{};
+GradPlan make_plan(int64_t nbh, int64_t outer, int64_t inner, int64_t D) {
+  GradPlan p{};
   p.dp = D <= 32 ? 32 : D <= 64 ? 64 : 128;
   p.wide = outer > 96 && nbh * ((outer + 127) / 128) >= 2 * kCUs;
   p.tile = p.wide ? 64 : 128;
@@ -389,16 +382,15 @@ Plan make_plan(int64_t nbh, int64_t outer, int64_t inner, int64_t D) {
   return p;
 }
 
-size_t lds_bytes(const Plan& p, int es) {
-  const int pad = es == 2 ? 16 : 4;
-  const size_t tile = static_cast<size_t>(2) * p.tile * (p.dp + pad) * es + static_cast<size_t>(p.tile) * 8;
+size_t lds_bytes(const GradPlan& p, int es) {
+  const size_t tile = static_cast<size_t>(2) * p.tile * p.dp * es + static_cast<size_t>(p.tile) * 8;
   return std::max(tile, static_cast<size_t>(4) * 32 * (p.dp + 4) * 4);
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Layout {
-  Plan q, kv;
+  GradPlan q, kv;
   size_t part_at, bytes;   // row values first, then the parts of whichever kernel runs
 };
 
