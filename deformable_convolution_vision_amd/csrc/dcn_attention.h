@@ -94,10 +94,15 @@ __device__ __forceinline__ f32x16 mma(const Frag<float>& a, const Frag<float>& b
   return c;
 }
 
+// Zeros that the compiler takes for unknown values.  A product whose accumulator it can prove
+// zero takes the constant instead, and its result registers may then be placed over those of
+// its operands, which has given wrong products; with these, kept in registers of their own
+// for a kernel's whole time, a product of a new sum starts from them without writing zeros.
 __device__ __forceinline__ f32x16 zero_acc() {
   f32x16 z;
 #pragma unroll
   for (int r = 0; r < 16; ++r) z[r] = 0.f;
+  asm volatile("" : "+v"(z));
   return z;
 }
 

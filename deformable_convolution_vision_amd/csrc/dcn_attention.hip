@@ -284,7 +284,7 @@ __global__ __launch_bounds__(64 * W) void attn_few_rows_kernel(Args a) {
         load_keys(win + at * step, word_next, kn);
         load_values(win + at * step, word_next, slot ^ 1);
       }
-      f32x16 s[1] = {zero_acc()};
+      f32x16 s[1] = {zero_acc()};   // (registers for standing zeros are not to spare here)
 #pragma unroll
       for (int i = 0; i < DP / 16; ++i) s[0] = mma(kf[i], qf[i], s[0]);
       typename POperand<T>::type pf[1];
@@ -327,6 +327,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(waves_per_s
 #pragma unroll
   for (int i = 0; i < DT; ++i) o[i] = zero_acc();
   Running run;
+  const f32x16 zeros = zero_acc();
 
   int win = w.s0;               // the 32 tiles whose mask words the lanes hold start here
   uint32_t words = 0;
@@ -372,7 +373,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(waves_per_s
     f32x16 s[2];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      s[n] = zero_acc();
+      s[n] = zeros;
 #pragma unroll
       for (int i = 0; i < DP / 16; ++i) s[n] = mma(row_frag<DP>(ks, 32 * n, i), qf[i], s[n]);
     }
