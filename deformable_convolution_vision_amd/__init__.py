@@ -14,6 +14,7 @@ calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -598,25 +599,37 @@ def deform_conv2d_layer(input, weight_om, bias_om, weight, bias=None, stride=1, 
     return out, offset, mask
 
 
-def attention_desc(query, key, value, key_mask=None, scale=None) -> AttnDesc:
-    """Descriptor of a cross attention call after checks of the tensors' shapes, types, devices
-    and strides (elements of a head adjacent; the other strides free)."""
+def _call(name: str, device, *args) -> None:
+    """An entry point of the library on the current stream of `device`."""
+    fn = getattr(load_library(), name)
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if rc != OK:
+        raise DcnError(rc, name)
+
+
+def _attention_key(query, key, value, key_mask, scale):
+    """The fields of a descriptor after checks of the tensors' shapes, types, devices and strides
+    (elements of a head adjacent; the other strides free)."""
     dtype = _DTYPES.get(query.dtype)
     if dtype is None:
         raise TypeError(f"unsupported dtype {query.dtype}; use float32 or bfloat16")
     if key.dtype != query.dtype or value.dtype != query.dtype:
         raise TypeError(f"query is {query.dtype}, key {key.dtype}, value {value.dtype}: all share one dtype")
-    if query.dim() != 4 or key.dim() != 4 or value.dim() != 4:
+    qshape, kshape = query.shape, key.shape
+    if len(qshape) != 4 or len(kshape) != 4:
         raise ValueError("query must be [B,Lq,Hq,D], key and value [B,Lk,Hkv,D]")
-    B, Lq, Hq, D = query.shape
-    Bk, Lk, Hkv, Dk = key.shape
-    if Bk != B or Dk != D or value.shape != key.shape:
-        raise ValueError(f"key {tuple(key.shape)} and value {tuple(value.shape)} do not match query "
-                         f"{tuple(query.shape)}")
+    B, Lq, Hq, D = qshape
+    Bk, Lk, Hkv, Dk = kshape
+    if Bk != B or Dk != D or value.shape != kshape:
+        raise ValueError(f"key {tuple(kshape)} and value {tuple(value.shape)} do not match query {tuple(qshape)}")
     if Hkv == 0 or Hq == 0 or Hq % Hkv != 0:
         raise ValueError(f"{Hq} query heads do not share {Hkv} key heads evenly")
     device = query.device
-    if not query.is_cuda or key.device != device or value.device != device:
+    if device.type != "cuda" or key.device != device or value.device != device:
         raise ValueError("query, key and value must be on one GPU")
     qs, ks, vs = query.stride(), key.stride(), value.stride()
     if D > 1 and (qs[3] != 1 or ks[3] != 1 or vs[3] != 1):
@@ -625,16 +638,28 @@ def attention_desc(query, key, value, key_mask=None, scale=None) -> AttnDesc:
     if key_mask is not None:
         if key_mask.dtype != torch.bool and key_mask.dtype != torch.uint8:
             raise TypeError(f"key_mask must be bool or uint8, got {key_mask.dtype}")
-        if tuple(key_mask.shape) != (B, Lk):
+        if key_mask.shape != (B, Lk):
             raise ValueError(f"key_mask must be {(B, Lk)}, got {tuple(key_mask.shape)}")
         if key_mask.device != device:
             raise ValueError("key_mask must be on the query's GPU")
         ms, inner = key_mask.stride()
         if Lk > 1 and inner != 1:
             raise ValueError("the positions of key_mask must be adjacent")
-    if scale is None:
-        scale = D ** -0.5 if D else 1.0
-    return AttnDesc(B, Lq, Lk, Hq, Hkv, D, qs[:3], ks[:3], vs[:3], ms, scale, dtype)
+    return B, Lq, Lk, Hq, Hkv, D, qs[:3], ks[:3], vs[:3], ms, scale if scale is not None else (D or 1) ** -0.5, dtype
+
+
+def attention_desc(query, key, value, key_mask=None, scale=None) -> AttnDesc:
+    """Descriptor of a cross attention call, for the raw entry points."""
+    return AttnDesc(*_attention_key(query, key, value, key_mask, scale))
+
+
+# Descriptor (as a pointer argument) and workspace sizes of a call, by its sizes and strides: a
+# program repeats few of them, and building one costs as much host time as a launch.
+@functools.lru_cache(maxsize=256)
+def _attention_plan(*fields):
+    desc = AttnDesc(*fields)
+    return ctypes.byref(desc), dcn_cross_attention_workspace_bytes(desc), \
+        dcn_cross_attention_backward_workspace_bytes(desc)
 
 
 def dcn_cross_attention_workspace_bytes(desc: AttnDesc) -> int:
@@ -662,19 +687,18 @@ def cross_attention(query, key, value, key_mask=None, scale=None, return_lse=Fal
     slice of a fused projection or of a longer cache).  A batch element without a kept position
     gives zeros.  Returns out [B,Lq,Hq,D], or (out, lse) with lse [B,Hq,Lq] float32, which
     cross_attention_backward takes."""
-    desc = attention_desc(query, key, value, key_mask, scale)
+    fields = _attention_key(query, key, value, key_mask, scale)
+    desc, nbytes, _ = _attention_plan(*fields)
     device = query.device
     if out is None:
         out = torch.empty(query.shape, dtype=query.dtype, device=device)
     else:
         _check_out(out, query.shape, query.dtype, device)
-    lse = torch.empty((desc.batch, desc.query_heads, desc.query_len), dtype=torch.float32,
-                      device=device) if return_lse else None
-    nbytes = dcn_cross_attention_workspace_bytes(desc)
+    lse = torch.empty((fields[0], fields[3], fields[1]), dtype=torch.float32, device=device) if return_lse else None
     if nbytes or workspace is not None:
         workspace = _workspace(workspace, nbytes, device)
-    with torch.cuda.device(device):
-        dcn_cross_attention(desc, query, key, value, key_mask, out, lse, workspace if nbytes else None, nbytes)
+    _call("dcn_cross_attention", device, desc, query.data_ptr(), key.data_ptr(), value.data_ptr(), _ptr(key_mask),
+          out.data_ptr(), _ptr(lse), workspace.data_ptr() if nbytes else None, nbytes)
     return (out, lse) if return_lse else out
 
 
@@ -700,23 +724,23 @@ def dcn_cross_attention_backward(desc: AttnDesc, q, k, v, key_mask, out, lse, gr
 def cross_attention_backward(grad_out, query, key, value, out, lse, key_mask=None, scale=None, workspace=None):
     """Gradients of cross_attention on the GPU from its inputs, its out and lse, and the upstream
     gradient grad_out [B,Lq,Hq,D]: returns dense (grad_query, grad_key, grad_value)."""
-    desc = attention_desc(query, key, value, key_mask, scale)
+    fields = _attention_key(query, key, value, key_mask, scale)
+    desc, _, nbytes = _attention_plan(*fields)
     device = query.device
     _check_out(grad_out, query.shape, query.dtype, device, "grad_out")
     _check_out(out, query.shape, query.dtype, device)
-    _check_out(lse, (desc.batch, desc.query_heads, desc.query_len), torch.float32, device, "lse")
+    _check_out(lse, (fields[0], fields[3], fields[1]), torch.float32, device, "lse")
     gq = torch.empty(query.shape, dtype=query.dtype, device=device)
     gk = torch.empty(key.shape, dtype=query.dtype, device=device)
     gv = torch.empty(key.shape, dtype=query.dtype, device=device)
-    nbytes = dcn_cross_attention_backward_workspace_bytes(desc)
     workspace = _workspace(workspace, nbytes, device)
-    with torch.cuda.device(device):
-        dcn_cross_attention_backward(desc, query, key, value, key_mask, out, lse, grad_out, gq, gk, gv,
-                                     workspace if nbytes else None, nbytes)
+    _call("dcn_cross_attention_backward", device, desc, query.data_ptr(), key.data_ptr(), value.data_ptr(),
+          _ptr(key_mask), out.data_ptr(), lse.data_ptr(), grad_out.data_ptr(), gq.data_ptr(), gk.data_ptr(),
+          gv.data_ptr(), workspace.data_ptr() if nbytes else None, nbytes)
     return gq, gk, gv
 
 
-def _norm_desc(input, num_groups, weight, bias, eps, activation) -> NormDesc:
+def _norm_key(input, num_groups, weight, bias, eps, activation):
     dtype = _DTYPES.get(input.dtype)
     if dtype is None:
         raise TypeError(f"unsupported dtype {input.dtype}; use float32 or bfloat16")
@@ -726,18 +750,30 @@ def _norm_desc(input, num_groups, weight, bias, eps, activation) -> NormDesc:
     shape = input.shape
     if len(shape) < 2:
         raise ValueError("input must be [B, ..., C], channels last")
-    if not input.is_cuda or not input.is_contiguous():
+    device = input.device
+    if device.type != "cuda" or not input.is_contiguous():
         raise ValueError("input must be a contiguous GPU tensor (channels last)")
     C = shape[-1]
     for name, t in (("weight", weight), ("bias", bias)):
         if t is None:
             continue
-        if t.shape != (C,) or t.dtype != input.dtype or t.device != input.device or not t.is_contiguous():
+        if t.shape != (C,) or t.dtype != input.dtype or t.device != device or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {input.dtype} tensor of {C} channels on the input's device")
     P = 1
     for n in shape[1:-1]:
         P *= n
-    return NormDesc(shape[0], P, C, int(num_groups), eps, act, dtype, 0)
+    return shape[0], P, C, int(num_groups), eps, act, dtype, 0
+
+
+def norm_desc(input, num_groups, weight=None, bias=None, eps=1e-5, activation="none") -> NormDesc:
+    """Descriptor of a group normalisation call, for the raw entry points."""
+    return NormDesc(*_norm_key(input, num_groups, weight, bias, eps, activation))
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_plan(*fields):
+    desc = NormDesc(*fields)
+    return ctypes.byref(desc), dcn_group_norm_workspace_bytes(desc), dcn_group_norm_backward_workspace_bytes(desc)
 
 
 def dcn_group_norm_workspace_bytes(desc: NormDesc) -> int:
@@ -764,19 +800,20 @@ def group_norm_act(input, num_groups, weight=None, bias=None, eps=1e-5, activati
     and bias [C] or None, activation "none", "relu", "silu" or "gelu".  Returns the input's shape
     and dtype, or (out, mean, rstd) with the statistics [B, num_groups] in float32, which
     group_norm_act_backward takes."""
-    desc = _norm_desc(input, num_groups, weight, bias, eps, activation)
+    fields = _norm_key(input, num_groups, weight, bias, eps, activation)
+    desc, nbytes, _ = _norm_plan(*fields)
     device = input.device
     if out is None:
         out = torch.empty_like(input)
     else:
         _check_out(out, input.shape, input.dtype, device)
-    nbytes = dcn_group_norm_workspace_bytes(desc)
     mean = rstd = None
     if return_stats:
-        mean, rstd = (torch.empty((desc.batch, desc.groups), dtype=torch.float32, device=device) for _ in range(2))
-    workspace = _workspace(workspace, nbytes, device)
-    with torch.cuda.device(device):
-        dcn_group_norm(desc, input, weight, bias, out, mean, rstd, workspace, nbytes)
+        mean, rstd = (torch.empty((fields[0], fields[3]), dtype=torch.float32, device=device) for _ in range(2))
+    if nbytes or workspace is not None:
+        workspace = _workspace(workspace, nbytes, device)
+    _call("dcn_group_norm", device, desc, input.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(), _ptr(mean),
+          _ptr(rstd), workspace.data_ptr() if nbytes else None, nbytes)
     return (out, mean, rstd) if return_stats else out
 
 
@@ -804,17 +841,19 @@ def group_norm_act_backward(grad_out, input, mean, rstd, num_groups, weight=None
     """Gradients of group_norm_act on the GPU from its input, parameters and statistics, and the
     upstream gradient grad_out of the input's shape: returns (grad_input, grad_weight, grad_bias),
     None for a parameter that is None."""
-    desc = _norm_desc(input, num_groups, weight, bias, 0.0, activation)
+    fields = _norm_key(input, num_groups, weight, bias, 0.0, activation)
+    desc, _, nbytes = _norm_plan(*fields)
     device = input.device
     _check_out(grad_out, input.shape, input.dtype, device, "grad_out")
-    nbytes = dcn_group_norm_backward_workspace_bytes(desc)
-    stats = (desc.batch, desc.groups)
+    stats = (fields[0], fields[3])
     _check_out(mean, stats, torch.float32, device, "mean")
     _check_out(rstd, stats, torch.float32, device, "rstd")
     gx = torch.empty_like(input)
     gw = None if weight is None else torch.empty_like(weight)
     gb = None if bias is None else torch.empty_like(bias)
-    workspace = _workspace(workspace, nbytes, device)
-    with torch.cuda.device(device):
-        dcn_group_norm_backward(desc, input, weight, bias, mean, rstd, grad_out, gx, gw, gb, workspace, nbytes)
+    if nbytes or workspace is not None:
+        workspace = _workspace(workspace, nbytes, device)
+    _call("dcn_group_norm_backward", device, desc, input.data_ptr(), _ptr(weight), _ptr(bias), mean.data_ptr(),
+          rstd.data_ptr(), grad_out.data_ptr(), gx.data_ptr(), _ptr(gw), _ptr(gb),
+          workspace.data_ptr() if nbytes else None, nbytes)
     return gx, gw, gb

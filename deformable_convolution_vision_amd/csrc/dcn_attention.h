@@ -29,24 +29,30 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_inff();
 
+// How the tiles of all batch elements and key heads fall to workgroups.
+struct Tiling {
+  int tiles;
+  int full;        // tiles below this one have a workgroup each; the inner loop of each of the others is
+  int splits;      // split over this many workgroups,
+  int per_split;   // of so many steps
+};
+
 struct Args {
   const void *q, *k, *v;
   const uint8_t* mask;         // [B][Lk] bytes, 0: the key is padding; or null
   void* out;                   // [B][Lq][Hq][D]
   float* lse;                  // [B][Hq][Lq] or null
-  float* part;                 // forward: partial outputs [split tile][split][row][DP], not yet divided by their sums
-  float* part_ml;              // ... with each row's maximum and sum, [split tile][split][row][2]
+  float* part;                 // split tiles' parts [tile][split][row][DP]: outputs not yet divided by their sums; dQ
+  float* part_ml;              // forward: each row's maximum and sum, [tile][split][row][2]
+  float* part_kv;              // parts of dK and dV [tile][split][2][key][DP]
   const void* dout;            // backward: [B][Lq][Hq][D]
-  const float* delta;          // backward: [B][Hkv][R][2]: lse in powers of two, and sum(dout * out)
+  const float* delta;          // backward: [B][Hkv][R] lse in powers of two, then as many sum(dout * out)
   void *dq, *dk, *dv;
   int64_t qs[3], ks[3], vs[3]; // strides in elements: batch, position, head
   int64_t ms;                  // the mask's batch stride
   int B, Lq, Lk, Hq, Hkv, g, D;
   int R;                       // query rows of one key head: g * Lq, row r = position r / g, head r % g
-  int tiles;                   // row tiles (dK, dV: key tiles) of all batch elements and key heads
-  int full;                    // tiles below this one have a workgroup each; the inner loop of each of the others
-  int splits;                  // is split over this many workgroups,
-  int per_split;               // of so many steps
+  Tiling y, ykv;               // of the forward or dQ; of dK and dV
   float c;                     // scale * log2(e): softmax runs in powers of two
   float scale;
 };
@@ -254,13 +260,16 @@ __device__ __forceinline__ void wait_loads() {
 // waits for this wave's LDS reads and writes, but not for its loads, and for the other waves
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// Rows 0 .. ROWS-1 of a tile into LDS by NT threads (thread `tid` of them): row r from base + r * stride (elements),
-// zeros where bit r of `live` is 0 and beyond D.  VEC: asynchronous, (ROWS * DP * sizeof(T)) /
-// (16 * NT) loads of each wave; otherwise element by element and done on return (but for a barrier).
-template <typename T, int DP, int ROWS, int NT, bool VEC>
-__device__ __forceinline__ void fetch_tile(T* lds, const T* base, int64_t stride, uint64_t live, int D, int tid) {
+// Rows 0 .. ROWS-1 of a tile into LDS by NT threads (thread `tid` of them): row r from element
+// offset(r) after base, zeros where bit r of `live` is 0 and beyond D.  VEC: asynchronous, the
+// same number of loads (tile_loads) of each wave; otherwise element by element and done on
+// return, but for a barrier.
+template <typename T, int DP, int ROWS, int NT>
+constexpr int tile_loads = ROWS * Tile<T, DP>::kVecs / NT;
+template <typename T, int DP, int ROWS, int NT, bool VEC, typename Offset>
+__device__ __forceinline__ void fetch_tile(T* lds, const T* base, Offset offset, uint64_t live, int D, int tid) {
   using L = Tile<T, DP>;
-  constexpr int N = ROWS * L::kVecs / NT, KV = Elem<T>::kVec;
+  constexpr int N = tile_loads<T, DP, ROWS, NT>, KV = Elem<T>::kVec;
   static_assert(ROWS * L::kVecs % NT == 0 && ROWS <= 64, "whole loads");
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   if constexpr (VEC) {
@@ -268,7 +277,7 @@ __device__ __forceinline__ void fetch_tile(T* lds, const T* base, int64_t stride
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int at = i * NT + tid, r = at / L::kVecs, d = ((at % L::kVecs) ^ L::swz(r)) * KV;
-      const uint32_t ofs = (static_cast<uint32_t>(r) * static_cast<uint32_t>(stride) + d) * static_cast<uint32_t>(sizeof(T));
+      const uint32_t ofs = (static_cast<uint32_t>(offset(r)) + d) * static_cast<uint32_t>(sizeof(T));
       const bool in = ((live >> r) & 1u) && d < D;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + (i * NT + wave * 64) * KV), 16,
                                                in ? ofs : kOutside, 0, 0, 0);
@@ -277,9 +286,49 @@ __device__ __forceinline__ void fetch_tile(T* lds, const T* base, int64_t stride
 #pragma unroll 1
     for (int i = 0; i < N; ++i) {
       const int at = i * NT + tid, r = at / L::kVecs, d = ((at % L::kVecs) ^ L::swz(r)) * KV;
-      const Vec16<T> v = load_vec<T, false>(base, r * stride, d, D, (live >> r) & 1u);
+      const Vec16<T> v = load_vec<T, false>(base, offset(r), d, D, (live >> r) & 1u);
       *reinterpret_cast<uint4*>(lds + at * KV) = v.u;
     }
+  }
+}
+
+// The key tiles of a row tile that hold attended keys, 64 keys each, in order: mask bits and
+// position.  32 tiles' bits are in the lanes at a time (the same in every wave).
+struct KeyTiles {
+  const uint8_t* mp;
+  int Lk, end, win, t;
+  uint32_t words;
+  __device__ __forceinline__ KeyTiles(const uint8_t* mask, int keys, int t0, int t1)
+      : mp(mask), Lk(keys), end(t1), win(t0), t(t0) {
+    fill();
+  }
+  __device__ __forceinline__ void fill() {
+    win = t;
+    words = key_words(mp, static_cast<int64_t>(t) * 64, 32, static_cast<int64_t>(end) * 64, Lk);
+  }
+  // bits of the next tile with an attended key, whose first key is k0; 0 when there is none
+  __device__ __forceinline__ uint64_t next(int64_t& k0) {
+    uint64_t word = 0;
+    for (; t < end && word == 0; ++t) {
+      if (t >= win + 32) fill();
+      const int i = 2 * (t - win);
+      word = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(words, i))) |
+             static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(words, i + 1))) << 32;
+    }
+    k0 = static_cast<int64_t>(t - 1) * 64;
+    return word;
+  }
+};
+
+// Scores of keys that do not count become -inf.  The word is the same for all lanes, so which
+// lanes keep register r are two runs of 32 lanes: bit acc_row(r, 0) and, for the upper half,
+// acc_row(r, 1), spread by the scalar unit.
+__device__ __forceinline__ void mask_scores(f32x16& s, uint32_t word) {
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const uint32_t lo = (word >> acc_row(r, 0)) & 1u ? 0xffffffffu : 0u, hi = (word >> acc_row(r, 1)) & 1u ? 0xffffffffu : 0u;
+    const uint64_t keep = (static_cast<uint64_t>(hi) << 32) | lo;
+    s[r] = __builtin_amdgcn_inverse_ballot_w64(keep) ? s[r] : kNegInf;
   }
 }
 
@@ -350,16 +399,57 @@ __device__ __forceinline__ Frag<float> row_frag(const float* tile, int r0, int i
   return f;
 }
 
+// One workgroup's part of the problem: a tile of rows (or, for dK and dV, of keys) of one (batch
+// element, key head), and steps s0 .. s1 - 1 of what it loops over.  Consecutive workgroups are consecutive pairs: the row tiles
+// that read the same keys then run on the same XCD when the pairs are a multiple of 8.
+struct Work {
+  int b, hk, row0, split, tail;   // tail: index of a split tile, or -1
+  int s0, s1;
+};
+__device__ __forceinline__ Work work_of(const Args& a, const Tiling& y, int at_tile, int rows, int steps) {
+  Work w;
+  int tile = at_tile;
+  w.tail = -1;
+  w.split = 0;
+  w.s0 = 0;
+  w.s1 = steps;
+  if (tile >= y.full) {
+    const int n = y.tiles - y.full, at = tile - y.full;
+    w.tail = at % n;
+    w.split = at / n;
+    tile = y.full + w.tail;
+    w.s0 = w.split * y.per_split;
+    w.s1 = min(steps, w.s0 + y.per_split);
+  }
+  const int nbh = a.B * a.Hkv, bh = tile % nbh;
+  w.b = bh / a.Hkv;
+  w.hk = bh % a.Hkv;
+  w.row0 = tile / nbh * rows;
+  return w;
+}
+
 // ---- host side
 
-struct Plan {
-  int dp;        // head size the kernel is built for: 32, 64 or 128
-  bool wide;     // waves of different rows share the key tiles (else waves of the same rows take different keys)
-  int waves;     // of a workgroup
-  int rows;      // rows of a tile
-  int step;      // keys of one step of the inner loop
-  int tiles, full, splits, per_split;
-};
+// Tiling for `tiles` tiles of `steps` steps each on a chip that holds `slots` workgroups at a
+// time: whole rounds of the chip go unsplit; the steps of each tile of the last, incomplete round
+// are split so that the round fills the chip, but not below `least` steps.
+inline Tiling tile_over(int64_t tiles, int64_t steps, int64_t slots, int64_t least) {
+  Tiling y{};
+  const int64_t tail = tiles % slots;
+  int64_t splits = tail == 0 ? 1 : slots / tail;
+  if (splits > steps / least) splits = steps / least > 1 ? steps / least : 1;
+  y.tiles = static_cast<int>(tiles);
+  y.per_split = static_cast<int>((steps + splits - 1) / splits);
+  y.splits = y.per_split > 0 ? static_cast<int>((steps + y.per_split - 1) / y.per_split) : 1;
+  if (y.splits < 1) y.splits = 1;
+  y.full = static_cast<int>(y.splits > 1 ? tiles - tail : tiles);
+  return y;
+}
+inline int64_t workgroups(const Tiling& y) { return y.full + static_cast<int64_t>(y.tiles - y.full) * y.splits; }
+inline int padded_head(int64_t D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
+// Tiles of a ring in the LDS: three where two workgroups of a CU then have room, else two.
+constexpr int stages_of(int row_bytes) { return row_bytes <= 128 ? 3 : 2; }
+constexpr int kCUs = 256;
 
 // Descriptor checks of every attention entry point: DCN_OK or a negative dcn_status.
 int check(const dcn_attn_desc* d);

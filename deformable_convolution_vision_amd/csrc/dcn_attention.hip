@@ -40,35 +40,6 @@ namespace dcn {
 namespace attn {
 namespace {
 
-// One workgroup's part of the problem: a tile of rows of one (batch element, key head), and
-// steps s0 .. s1 - 1 of its keys.  Consecutive workgroups are consecutive pairs: the row tiles
-// that read the same keys then run on the same XCD when the pairs are a multiple of 8.
-struct Work {
-  int b, hk, row0, split, tail;   // tail: index of a split tile, or -1
-  int s0, s1;
-};
-__device__ __forceinline__ Work work_of(const Args& a, int rows, int steps) {
-  Work w;
-  int tile = blockIdx.x;
-  w.tail = -1;
-  w.split = 0;
-  w.s0 = 0;
-  w.s1 = steps;
-  if (tile >= a.full) {
-    const int n = a.tiles - a.full, at = tile - a.full;
-    w.tail = at % n;
-    w.split = at / n;
-    tile = a.full + w.tail;
-    w.s0 = w.split * a.per_split;
-    w.s1 = min(steps, w.s0 + a.per_split);
-  }
-  const int nbh = a.B * a.Hkv, bh = tile % nbh;
-  w.b = bh / a.Hkv;
-  w.hk = bh % a.Hkv;
-  w.row0 = tile / nbh * rows;
-  return w;
-}
-
 // A lane's row in registers.
 template <typename T, int DP, bool VEC>
 __device__ __forceinline__ void load_row(const Args& a, const Work& w, int row, Frag<T> (&f)[DP / 16]) {
@@ -82,18 +53,6 @@ __device__ __forceinline__ void load_row(const Args& a, const Work& w, int row, 
 struct Running {
   float m = kNegInf, l = 0.f;
 };
-
-// Scores of keys that do not count become -inf.  The word is the same for all lanes, so which
-// lanes keep register r are two runs of 32 lanes: bit acc_row(r, 0) and, for the upper half,
-// acc_row(r, 1), spread by the scalar unit.
-__device__ __forceinline__ void mask_scores(f32x16& s, uint32_t word) {
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const uint32_t lo = (word >> acc_row(r, 0)) & 1u ? 0xffffffffu : 0u, hi = (word >> acc_row(r, 1)) & 1u ? 0xffffffffu : 0u;
-    const uint64_t keep = (static_cast<uint64_t>(hi) << 32) | lo;
-    s[r] = __builtin_amdgcn_inverse_ballot_w64(keep) ? s[r] : kNegInf;
-  }
-}
 
 // Takes N blocks of 32 scores in (raw products; word: the attended keys of each), gives the
 // weights as the second product's operands, and rescales the output accumulators when the
@@ -145,7 +104,7 @@ __device__ __forceinline__ void put4(const Args& a, const Work& w, int rows, int
   const int row = w.row0 + rr;
   if (row >= a.R) return;
   if (w.tail >= 0) {
-    const int64_t prow = (static_cast<int64_t>(w.tail) * a.splits + w.split) * rows + rr;
+    const int64_t prow = (static_cast<int64_t>(w.tail) * a.y.splits + w.split) * rows + rr;
     *reinterpret_cast<float4*>(a.part + prow * DP + d) = v;
     if (d == 0) *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(m, l);
     return;
@@ -225,11 +184,11 @@ constexpr size_t join_lds(int waves) { return static_cast<size_t>(waves) * 32 * 
 // The next block's rows are on their way while one is worked on.
 template <typename T, int DP, int W, bool VEC>
 __global__ __launch_bounds__(64 * W) void attn_few_rows_kernel(Args a) {
-  constexpr int DT = DP / 32, KL = DP * static_cast<int>(sizeof(T)) / 32, VL = 32 * Tile<T, DP>::kVecs / 64;
+  constexpr int DT = DP / 32, KL = DP * static_cast<int>(sizeof(T)) / 32, VL = tile_loads<T, DP, 32, 64>;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   T* const lds = reinterpret_cast<T*>(smem) + wave * 2 * 32 * DP;
-  const Work w = work_of(a, 32, (a.Lk + 32 * W - 1) / (32 * W));
+  const Work w = work_of(a, a.y, blockIdx.x, 32, (a.Lk + 32 * W - 1) / (32 * W));
   const T* kp = static_cast<const T*>(a.k) + w.b * a.ks[0] + w.hk * a.ks[2];
   const T* vp = static_cast<const T*>(a.v) + w.b * a.vs[0] + w.hk * a.vs[2];
   const uint8_t* mp = a.mask == nullptr ? nullptr : a.mask + w.b * a.ms;
@@ -263,7 +222,8 @@ __global__ __launch_bounds__(64 * W) void attn_few_rows_kernel(Args a) {
     }
   };
   const auto load_values = [&](int64_t k0, uint32_t word, int slot) {
-    fetch_tile<T, DP, 32, 64, VEC>(lds + slot * 32 * DP, vp + k0 * a.vs[1], a.vs[1], word, a.D, lane);
+    fetch_tile<T, DP, 32, 64, VEC>(lds + slot * 32 * DP, vp + k0 * a.vs[1], [&](int r) { return r * a.vs[1]; }, word, a.D,
+                                   lane);
   };
 
   const int64_t step = 32 * W, end = w.s1 * step;
@@ -313,11 +273,11 @@ constexpr int waves_per_simd(int row_bytes) { return row_bytes <= 64 ? 4 : row_b
 // is worked on, the next STAGES - 1 are on their way.
 template <typename T, int DP, int STAGES, bool VEC>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(waves_per_simd(sizeof(T) * DP)))) void attn_rows_kernel(Args a) {
-  constexpr int KT = 64, DT = DP / 32, BUF = 2 * KT * DP, LOADS = 2 * KT * Tile<T, DP>::kVecs / 256, AHEAD = STAGES - 1;
+  constexpr int KT = 64, DT = DP / 32, BUF = 2 * KT * DP, LOADS = 2 * tile_loads<T, DP, KT, 256>, AHEAD = STAGES - 1;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   T* const lds = reinterpret_cast<T*>(smem);              // [STAGES][keys, values][KT][DP]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Work w = work_of(a, 128, (a.Lk + KT - 1) / KT);
+  const Work w = work_of(a, a.y, blockIdx.x, 128, (a.Lk + KT - 1) / KT);
   const T* kp = static_cast<const T*>(a.k) + w.b * a.ks[0] + w.hk * a.ks[2];
   const T* vp = static_cast<const T*>(a.v) + w.b * a.vs[0] + w.hk * a.vs[2];
   const uint8_t* mp = a.mask == nullptr ? nullptr : a.mask + w.b * a.ms;
@@ -329,31 +289,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(waves_per_s
   Running run;
   const f32x16 zeros = zero_acc();
 
-  int win = w.s0;               // the 32 tiles whose mask words the lanes hold start here
-  uint32_t words = 0;
-  const auto fill = [&](int t) {
-    win = t;
-    words = key_words(mp, static_cast<int64_t>(t) * KT, 32, static_cast<int64_t>(w.s1) * KT, a.Lk);
-  };
-  int t = w.s0;                 // the next tile to look at
-  // the next tile that holds an attended key (the same for every wave) is sent for; its mask
-  // bits, or 0 when there is none
+  KeyTiles tiles(mp, a.Lk, w.s0, w.s1);
+  // sends for the next tile that holds an attended key; its mask bits, or 0 when there is none
   const auto send = [&](int slot) {
-    uint64_t word = 0;
-    for (; t < w.s1 && word == 0; ++t) {
-      if (t >= win + 32) fill(t);
-      const int i = 2 * (t - win);
-      word = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(words, i))) |
-             static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(words, i + 1))) << 32;
-    }
+    int64_t k0;
+    const uint64_t word = tiles.next(k0);
     if (word != 0) {
-      const int64_t k0 = static_cast<int64_t>(t - 1) * KT;
-      fetch_tile<T, DP, KT, 256, VEC>(lds + slot * BUF, kp + k0 * a.ks[1], a.ks[1], word, a.D, tid);
-      fetch_tile<T, DP, KT, 256, VEC>(lds + slot * BUF + KT * DP, vp + k0 * a.vs[1], a.vs[1], word, a.D, tid);
+      fetch_tile<T, DP, KT, 256, VEC>(lds + slot * BUF, kp + k0 * a.ks[1], [&](int r) { return r * a.ks[1]; }, word, a.D, tid);
+      fetch_tile<T, DP, KT, 256, VEC>(lds + slot * BUF + KT * DP, vp + k0 * a.vs[1], [&](int r) { return r * a.vs[1]; }, word,
+                                      a.D, tid);
     }
     return word;
   };
-  fill(w.s0);
   uint64_t word[AHEAD + 1];
 #pragma unroll
   for (int j = 0; j < AHEAD; ++j) word[j] = send(j);
@@ -397,24 +344,24 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Args a, int rows) {
   constexpr int V4 = DP / 4;
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, prow = at / V4;
   Work w;
-  const int tail = static_cast<int>(prow / rows), rr = static_cast<int>(prow % rows), tile = a.full + tail;
-  if (tile >= a.tiles) return;
+  const int tail = static_cast<int>(prow / rows), rr = static_cast<int>(prow % rows), tile = a.y.full + tail;
+  if (tile >= a.y.tiles) return;
   const int nbh = a.B * a.Hkv, bh = tile % nbh, d = static_cast<int>(at % V4) * 4;
   w.b = bh / a.Hkv;
   w.hk = bh % a.Hkv;
   w.row0 = tile / nbh * rows;
   w.tail = -1;
   if (w.row0 + rr >= a.R) return;
-  const int64_t p0 = static_cast<int64_t>(tail) * a.splits * rows + rr;
+  const int64_t p0 = static_cast<int64_t>(tail) * a.y.splits * rows + rr;
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + p0;
   const float* part = a.part + p0 * DP + d;
   float mm = kNegInf, ll = 0.f;
 #pragma unroll 4
-  for (int s = 0; s < a.splits; ++s) mm = fmaxf(mm, ml[static_cast<int64_t>(s) * rows].x);
+  for (int s = 0; s < a.y.splits; ++s) mm = fmaxf(mm, ml[static_cast<int64_t>(s) * rows].x);
   const float ms = mm == kNegInf ? 0.f : mm;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int s = 0; s < a.splits; ++s) {
+  for (int s = 0; s < a.y.splits; ++s) {
     const float2 x = ml[static_cast<int64_t>(s) * rows];
     const float f = exp2_fast(x.x - ms);
     const float4 v = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(s) * rows * DP);
@@ -427,54 +374,42 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Args a, int rows) {
   put4<T, DP>(a, w, rows, rr, d, mm, ll, acc);
 }
 
-constexpr int kCUs = 256;
-
 // Waves of the few-rows form: as many as the registers of a CU hold at this head size.
-template <typename T, int DP>
-constexpr int kWaves = sizeof(T) == 2 ? (DP == 32 ? 16 : 8) : (DP == 128 ? 4 : DP == 64 ? 8 : 16);
+constexpr int waves_of(int es, int dp) { return es == 2 ? (dp == 32 ? 16 : 8) : (dp == 128 ? 4 : dp == 64 ? 8 : 16); }
 
-int waves_of(int es, int dp) { return es == 2 ? (dp == 32 ? 16 : 8) : (dp == 128 ? 4 : dp == 64 ? 8 : 16); }
+struct Plan {
+  int dp;
+  bool wide;     // attn_rows_kernel (else attn_few_rows_kernel)
+  int waves;     // of a workgroup
+  int rows;      // of a tile
+  Tiling y;
+};
 
 Plan make_plan(const dcn_attn_desc* d) {
   Plan p{};
   const int es = d->dtype == DCN_BF16 ? 2 : 4;
-  p.dp = d->head_dim <= 32 ? 32 : d->head_dim <= 64 ? 64 : 128;
+  p.dp = padded_head(d->head_dim);
   const int64_t nbh = d->batch * d->key_heads, R = d->query_len * (d->query_heads / d->key_heads);
-  const int64_t few = nbh * ((R + 31) / 32);
-  p.wide = R > 96 && few > 2 * kCUs;
-  int64_t want = 0;
-  if (const char* f = std::getenv("DCN_ATTN_FORM")) {   // "rows" or "few", and a number of splits
+  p.wide = R > 96 && nbh * ((R + 31) / 32) > 2 * kCUs;
+  if (const char* f = std::getenv("DCN_ATTN_FORM")) {
     if (f[0] == 'r') p.wide = true;
     if (f[0] == 'f') p.wide = false;
-    while (*f != '\0' && (*f < '0' || *f > '9')) ++f;
-    want = std::atoi(f);
   }
   p.waves = p.wide ? 4 : waves_of(es, p.dp);
   p.rows = p.wide ? 128 : 32;
-  p.step = p.wide ? 64 : 32 * p.waves;
-  const int64_t tiles = nbh * ((R + p.rows - 1) / p.rows);
-  const int64_t steps = std::max<int64_t>(1, (d->key_len + p.step - 1) / p.step);
-  const int64_t slots = p.wide ? 2 * kCUs : 2 * kCUs * 8 / p.waves;
-  p.tiles = static_cast<int>(tiles);
-  int64_t full = tiles / slots * slots, tail = tiles - full;
-  int64_t splits = tail == 0 ? 1 : std::min<int64_t>(slots / tail, std::max<int64_t>(1, steps / 2));
-  if (want > 0) splits = std::min(want, steps);
-  p.per_split = static_cast<int>((steps + splits - 1) / splits);
-  p.splits = static_cast<int>((steps + p.per_split - 1) / p.per_split);
-  p.full = static_cast<int>(p.splits > 1 ? full : tiles);
+  const int64_t step = p.wide ? 64 : 32 * p.waves;
+  p.y = tile_over(nbh * ((R + p.rows - 1) / p.rows), (d->key_len + step - 1) / step,
+                  p.wide ? 2 * kCUs : 2 * kCUs * 8 / p.waves, 2);
   return p;
 }
 
-// Key tiles in the LDS of the rows form: three, where two workgroups of a CU have room for them.
-constexpr int stages_of(int es, int dp) { return es * dp <= 128 ? 3 : 2; }
-
 size_t lds_bytes(const Plan& p, int es) {
   const size_t row = static_cast<size_t>(p.dp) * es;
-  return std::max((p.wide ? stages_of(es, p.dp) * 2 * 64 : p.waves * 2 * 32) * row, join_lds(p.waves));
+  return std::max((p.wide ? stages_of(row) * 2 * 64 : p.waves * 2 * 32) * row, join_lds(p.waves));
 }
 
 size_t part_bytes(const Plan& p, size_t* ml_at) {
-  const size_t rows = static_cast<size_t>(p.tiles - p.full) * p.splits * p.rows;
+  const size_t rows = static_cast<size_t>(p.y.tiles - p.y.full) * p.y.splits * p.rows;
   *ml_at = rows * p.dp * 4;
   return (*ml_at + rows * 8 + 255) / 256 * 256;
 }
@@ -482,10 +417,10 @@ size_t part_bytes(const Plan& p, size_t* ml_at) {
 template <typename T, int DP>
 const void* fwd_kernel(bool wide, bool vec) {
   if (wide)
-    return vec ? reinterpret_cast<const void*>(&attn_rows_kernel<T, DP, stages_of(sizeof(T), DP), true>)
-               : reinterpret_cast<const void*>(&attn_rows_kernel<T, DP, stages_of(sizeof(T), DP), false>);
-  return vec ? reinterpret_cast<const void*>(&attn_few_rows_kernel<T, DP, kWaves<T, DP>, true>)
-             : reinterpret_cast<const void*>(&attn_few_rows_kernel<T, DP, kWaves<T, DP>, false>);
+    return vec ? reinterpret_cast<const void*>(&attn_rows_kernel<T, DP, stages_of(sizeof(T) * DP), true>)
+               : reinterpret_cast<const void*>(&attn_rows_kernel<T, DP, stages_of(sizeof(T) * DP), false>);
+  return vec ? reinterpret_cast<const void*>(&attn_few_rows_kernel<T, DP, waves_of(sizeof(T), DP), true>)
+             : reinterpret_cast<const void*>(&attn_few_rows_kernel<T, DP, waves_of(sizeof(T), DP), false>);
 }
 template <typename T>
 const void* fwd_kernel(int dp, bool wide, bool vec) {
@@ -577,10 +512,7 @@ extern "C" int dcn_cross_attention(const dcn_attn_desc* d, const void* q, const 
   a.mask = key_mask;
   a.out = out;
   a.lse = lse;
-  a.tiles = p.tiles;
-  a.full = p.full;
-  a.splits = p.splits;
-  a.per_split = p.per_split;
+  a.y = p.y;
   if (need > 0) {
     a.part = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + ml_at);
@@ -589,11 +521,10 @@ extern "C" int dcn_cross_attention(const dcn_attn_desc* d, const void* q, const 
   const int es = bf16 ? 2 : 4;
   const bool vec = vec_ok(q, d->q_stride, d->head_dim, es) && vec_ok(k, d->k_stride, d->head_dim, es) &&
                    vec_ok(v, d->v_stride, d->head_dim, es);
-  const int tail = p.tiles - p.full;
-  const int64_t grid = p.full + static_cast<int64_t>(tail) * p.splits;
+  const int tail = p.y.tiles - p.y.full;
   void* args[] = {&a};
   const void* fn = bf16 ? fwd_kernel<uint16_t>(p.dp, p.wide, vec) : fwd_kernel<float>(p.dp, p.wide, vec);
-  if (hipLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(64 * p.waves), args,
+  if (hipLaunchKernel(fn, dim3(static_cast<unsigned>(workgroups(p.y))), dim3(64 * p.waves), args,
                       lds_bytes(p, es), stream) !=
       hipSuccess)
     return DCN_E_HIP;

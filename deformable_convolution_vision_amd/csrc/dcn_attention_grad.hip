@@ -10,14 +10,15 @@
 // The weights are formed again from the scores and the forward's lse; nothing of size
 // Lq x Lk is stored.
 //
-// Launches: the row pass (delta, and lse in powers of two), then dQ (32 or 128 rows of a
-// workgroup, a loop over key tiles, as the forward), then dK and dV (32 or 128 keys of a
-// workgroup, a loop over row tiles).  Each sum is formed by one wave, or by waves and
-// workgroups whose parts are added in a fixed order: no atomics, the same bits each time.
-// The heads that share a key head are rows of one problem, so their gradients add up inside
-// the loop of dK and dV.
+// Launches: a pass over the rows (delta, and lse in powers of two); then dQ, and dK with dV, as
+// workgroups of one launch, since neither fills the chip alone where one side is short: 128 rows
+// and a loop over key tiles (as the forward), or 128 keys and a loop over row tiles, the tiles
+// in a ring that buffer -> LDS loads fill ahead of use.  Where there are fewer tiles than the
+// chip holds, their loops are split over workgroups, and a last launch adds the parts.  Each sum
+// is formed in a fixed order: no atomics, the same bits each time.  The heads that share a key
+// head are rows of one problem, so their gradients add up inside the loop of dK and dV.
 //
-// Both kernels form the scores so that the first products' result registers are an operand
+// Both form the scores so that the first products' result registers are an operand
 // of the second (see dcn_attention.h): dQ keeps a row per lane (S^T), dK/dV a key per lane
 // (S).  Rows with no key have lse = -inf; it enters as +inf, which makes every weight 0.
 //
@@ -37,56 +38,56 @@ namespace dcn {
 namespace attn {
 namespace {
 
-// One row of 16 lanes: delta and lse in powers of two.
-template <typename T>
-__global__ __launch_bounds__(256) void attn_rows_kernel(Args a) {
+// delta, and lse in powers of two, of each row: float arrays of B * Hq * Lq rows (in the order of
+// the pairs and their rows), one after the other.  16 bytes of a row (VEC) or one element a lane.
+template <typename T, int DP, bool VEC>
+__global__ __launch_bounds__(256) void attn_grad_rows_kernel(Args a) {
+  constexpr int LPR = VEC ? Tile<T, DP>::kVecs : 16, RPB = 256 / LPR;   // lanes of a row, rows of a workgroup
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv * a.R;
-  const int64_t prow = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  const int64_t prow = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / LPR;
   if (prow >= rows) return;
-  const int sub = threadIdx.x & 15;
+  const int sub = threadIdx.x % LPR;
   const int bh = static_cast<int>(prow / a.R), r = static_cast<int>(prow % a.R);
   const int b = bh / a.Hkv, pos = r / a.g, head = (bh % a.Hkv) * a.g + r % a.g;
   const int64_t at = ((static_cast<int64_t>(b) * a.Lq + pos) * a.Hq + head) * a.D;
   const T* o = static_cast<const T*>(a.out) + at;
   const T* go = static_cast<const T*>(a.dout) + at;
   float s = 0.f;
-  for (int d = sub; d < a.D; d += 16) s = fmaf(widen(o[d]), widen(go[d]), s);
+  if constexpr (VEC) {
+    const Vec16<T> x = load_vec<T, true>(o, 0, sub * Elem<T>::kVec, a.D, true);
+    const Vec16<T> y = load_vec<T, true>(go, 0, sub * Elem<T>::kVec, a.D, true);
 #pragma unroll
-  for (int w = 8; w > 0; w >>= 1) s += __shfl_xor(s, w, 16);
+    for (int j = 0; j < Elem<T>::kVec; ++j) s = fmaf(widen(x.e[j]), widen(y.e[j]), s);
+  } else {
+    for (int d = sub; d < a.D; d += LPR) s = fmaf(widen(o[d]), widen(go[d]), s);
+  }
+#pragma unroll
+  for (int w = LPR / 2; w > 0; w >>= 1) s += __shfl_xor(s, w, LPR);
   if (sub == 0) {
     const float lse = a.lse[(static_cast<int64_t>(b) * a.Hq + head) * a.Lq + pos];
-    float* out = const_cast<float*>(a.delta) + prow * 2;
-    out[0] = lse == kNegInf ? -kNegInf : lse * kLog2e;
-    out[1] = s;
+    float* out = const_cast<float*>(a.delta);
+    out[prow] = lse == kNegInf ? -kNegInf : lse * kLog2e;   // a row with no key: every weight becomes 0
+    out[rows + prow] = s;
   }
 }
 
-// Adds the waves' parts of a transposed sum (DP x 32 per wave) through LDS and hands each
-// row's 4 elements to store(row of the workgroup, element, values).
-template <int DP, int WC, int WS, int DT, typename Store>
-__device__ __forceinline__ void join_sum(const f32x16 (&o)[DT], float* os, Store store) {
-  constexpr int OST = DP + 4, V4 = DP / 4, NT = 64 * WC * WS;
-  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, wave = tid >> 6;
-  __syncthreads();
+// Turns a wave's transposed sum (DP x 32) into rows through its own part of the LDS, 32 elements
+// at a time, and hands 4 elements of row rr to store(rr, element, values).
+template <int DT, typename Store>
+__device__ __forceinline__ void rows_out(const f32x16 (&o)[DT], float* os, Store store) {
+  constexpr int OST = 36;
+  const int lane = threadIdx.x & 63, half = lane >> 5;
 #pragma unroll
-  for (int i = 0; i < DT; ++i)
+  for (int i = 0; i < DT; ++i) {
 #pragma unroll
     for (int r4 = 0; r4 < 4; ++r4)
-      *reinterpret_cast<float4*>(os + (wave * 32 + (lane & 31)) * OST + 32 * i + acc_row(4 * r4, half)) =
+      *reinterpret_cast<float4*>(os + (lane & 31) * OST + acc_row(4 * r4, half)) =
           make_float4(o[i][4 * r4], o[i][4 * r4 + 1], o[i][4 * r4 + 2], o[i][4 * r4 + 3]);
-  __syncthreads();
-  for (int at = tid; at < WC * 32 * V4; at += NT) {
-    const int rr = at / V4, d = (at % V4) * 4, grp = rr / 32, ri = rr % 32;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < WS; ++w) {
-      const float4 v = *reinterpret_cast<const float4*>(os + ((grp * WS + w) * 32 + ri) * OST + d);
-      acc.x += v.x;
-      acc.y += v.y;
-      acc.z += v.z;
-      acc.w += v.w;
+    for (int n = 0; n < 4; ++n) {
+      const int rr = n * 8 + lane / 8, d = (lane % 8) * 4;
+      store(rr, 32 * i + d, *reinterpret_cast<const float4*>(os + rr * OST + d));
     }
-    store(rr, d, acc);
   }
 }
 
@@ -98,343 +99,350 @@ __device__ __forceinline__ void store4(T* p, int d, int D, float4 v, float f) {
     if (d + j < D) p[d + j] = narrow<T>(vals[j]);
 }
 
-template <typename T, int DP, int WQ, int WK, bool VEC>
-__global__ __launch_bounds__(64 * WQ * WK) void attn_dq_kernel(Args a) {
-  constexpr int NT = 64 * WQ * WK, KV = Elem<T>::kVec, ST = DP;
-  constexpr int SUB = WK == 1 ? 2 : 1, KT = 32 * SUB * WK, VPR = DP / KV, NV = KT * VPR / NT, DT = DP / 32;
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  T* ks = reinterpret_cast<T*>(smem);
-  T* vs = ks + KT * ST;
-  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, wave = tid >> 6;
-  const int wq = wave / WK, wk = wave % WK;
-  const int nbh = a.B * a.Hkv;
-  int id = blockIdx.x;
-  const int bh = id % nbh;
-  id /= nbh;
-  const int split = id % a.splits, rt = id / a.splits;
-  const int b = bh / a.Hkv, hk = bh % a.Hkv;
-  const T* kp = static_cast<const T*>(a.k) + b * a.ks[0] + hk * a.ks[2];
-  const T* vp = static_cast<const T*>(a.v) + b * a.vs[0] + hk * a.vs[2];
-  const uint8_t* mp = a.mask == nullptr ? nullptr : a.mask + b * a.ms;
+template <typename T>
+__device__ __forceinline__ T* dq_row(const Args& a, const Work& w, int row) {
+  return static_cast<T*>(a.dq) +
+         ((static_cast<int64_t>(w.b) * a.Lq + row / a.g) * a.Hq + w.hk * a.g + row % a.g) * a.D;
+}
+template <typename T>
+__device__ __forceinline__ T* dkv_row(const Args& a, const Work& w, int key, int which) {
+  T* p = static_cast<T*>(which ? a.dv : a.dk);
+  return p == nullptr ? p : p + ((static_cast<int64_t>(w.b) * a.Lk + key) * a.Hkv + w.hk) * a.D;
+}
 
-  const int row = rt * 32 * WQ + wq * 32 + (lane & 31);
+constexpr int kT = 64;           // rows of a tile in the LDS
+constexpr int kRowVals = 2 * kT; // lse and delta of a row tile
+
+template <typename T, int DP, int STAGES, bool VEC>
+__device__ __forceinline__ void dq_part(const Args& a, int tile, T* lds) {
+  constexpr int DT = DP / 32, BUF = 2 * kT * DP, AHEAD = STAGES - 1, LOADS = VEC ? 2 * tile_loads<T, DP, kT, 256> : 0;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const Work w = work_of(a, a.y, tile, 128, (a.Lk + kT - 1) / kT);
+  const T* kp = static_cast<const T*>(a.k) + w.b * a.ks[0] + w.hk * a.ks[2];
+  const T* vp = static_cast<const T*>(a.v) + w.b * a.vs[0] + w.hk * a.vs[2];
+  const int row = w.row0 + wave * 32 + (lane & 31);
+  const bool busy = w.row0 + wave * 32 < a.R;   // some of the wave's rows exist
   Frag<T> qf[DP / 16], gf[DP / 16];
   float lse2 = -kNegInf, delta = 0.f;
   {
     const bool live = row < a.R;
-    const int pos = live ? row / a.g : 0, head = hk * a.g + (live ? row % a.g : 0);
-    const T* qp = static_cast<const T*>(a.q) + b * a.qs[0] + pos * a.qs[1] + head * a.qs[2];
-    const T* gp = static_cast<const T*>(a.dout) + ((static_cast<int64_t>(b) * a.Lq + pos) * a.Hq + head) * a.D;
-    load_frags<T, DP, VEC>(qp, 0, a.D, live, qf);
-    load_frags<T, DP, VEC>(gp, 0, a.D, live, gf);
+    const int pos = live ? row / a.g : 0, head = w.hk * a.g + (live ? row % a.g : 0);
+    load_frags<T, DP, VEC>(static_cast<const T*>(a.q) + w.b * a.qs[0] + pos * a.qs[1] + head * a.qs[2], 0, a.D, live, qf);
+    load_frags<T, DP, VEC>(static_cast<const T*>(a.dout) + ((static_cast<int64_t>(w.b) * a.Lq + pos) * a.Hq + head) * a.D,
+                           0, a.D, live, gf);
     if (live) {
-      const int64_t prow = static_cast<int64_t>(bh) * a.R + row;
-      lse2 = a.delta[prow * 2];
-      delta = a.delta[prow * 2 + 1];
+      const int64_t prow = static_cast<int64_t>(w.b * a.Hkv + w.hk) * a.R + row;
+      lse2 = a.delta[prow];
+      delta = a.delta[static_cast<int64_t>(a.B) * a.Hkv * a.R + prow];
     }
   }
   f32x16 o[DT];
 #pragma unroll
   for (int i = 0; i < DT; ++i) o[i] = zero_acc();
+  const f32x16 zeros = zero_acc();
 
-  const int tiles = (a.Lk + KT - 1) / KT;
-  const int t0 = split * a.per_split, t1 = min(tiles, t0 + a.per_split);
-  Vec16<T> kr[NV], vr[NV];
-  const auto load_tile = [&](int t) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int at = tid + i * NT, key = t * KT + at / VPR, d = (at % VPR) * KV;
-      // rows of padded keys are taken as zeros: their weight is 0, and 0 times a NaN is none
-      bool live = key < a.Lk;
-      if (mp != nullptr && live) live = mp[key] != 0;
-      kr[i] = load_vec<T, VEC>(kp + key * a.ks[1], 0, d, a.D, live);
-      vr[i] = load_vec<T, VEC>(vp + key * a.vs[1], 0, d, a.D, live);
+  KeyTiles tiles(a.mask == nullptr ? nullptr : a.mask + w.b * a.ms, a.Lk, w.s0, w.s1);
+  // rows of padded keys are not read and taken as zeros: their weight is 0, and 0 times a NaN is none
+  const auto send = [&](int slot) {
+    int64_t k0;
+    const uint64_t word = tiles.next(k0);
+    if (word != 0) {
+      fetch_tile<T, DP, kT, 256, VEC>(lds + slot * BUF, kp + k0 * a.ks[1], [&](int r) { return r * a.ks[1]; }, word, a.D, tid);
+      fetch_tile<T, DP, kT, 256, VEC>(lds + slot * BUF + kT * DP, vp + k0 * a.vs[1], [&](int r) { return r * a.vs[1]; }, word,
+                                      a.D, tid);
     }
+    return word;
   };
-  if (t0 < t1) load_tile(t0);
-  for (int t = t0; t < t1; ++t) {
-    __syncthreads();
+  uint64_t word[AHEAD + 1];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int at = tid + i * NT, key = at / VPR, d = (at % VPR) * KV;
-      *reinterpret_cast<uint4*>(ks + Tile<T, DP>::at(key, d)) = kr[i].u;
-      *reinterpret_cast<uint4*>(vs + Tile<T, DP>::at(key, d)) = vr[i].u;
-    }
-    __syncthreads();
-    if (t + 1 < t1) load_tile(t + 1);
-    const int k0 = t * KT + wk * 32 * SUB;
-    uint64_t word;
-    {
-      const int key = k0 + lane;
-      bool live = lane < 32 * SUB && key < a.Lk;
-      if (mp != nullptr && live) live = mp[key] != 0;
-      word = __ballot(live);
-    }
+  for (int j = 0; j < AHEAD; ++j) word[j] = send(j);
+  int slot = 0;
+  while (word[0] != 0) {
+    if (AHEAD == 2 && word[1] != 0) wait_loads<LOADS>();
+    else wait_loads<0>();
+    lds_barrier();
+    word[AHEAD] = send(slot == 0 ? STAGES - 1 : slot - 1);
+    const T* ks = lds + slot * BUF;
+    const T* vs = ks + kT * DP;
 #pragma unroll
-    for (int s = 0; s < SUB; ++s) {
-      const uint32_t w = static_cast<uint32_t>(word >> (32 * s));
-      if (w == 0) continue;
-      const int r0 = wk * 32 * SUB + s * 32;
-      f32x16 sa = zero_acc(), pa = zero_acc();
+    for (int n = 0; n < 2; ++n) {
+      const uint32_t keep = static_cast<uint32_t>(word[0] >> (32 * n));
+      if (keep == 0 || !busy) continue;
+      f32x16 s = zeros, p = zeros;
 #pragma unroll
       for (int i = 0; i < DP / 16; ++i) {
-        sa = mma(row_frag<DP>(ks, r0, i), qf[i], sa);
-        pa = mma(row_frag<DP>(vs, r0, i), gf[i], pa);
+        s = mma(row_frag<DP>(ks, 32 * n, i), qf[i], s);
+        p = mma(row_frag<DP>(vs, 32 * n, i), gf[i], p);
       }
+      if (keep != 0xffffffffu) mask_scores(s, keep);
       float ds[16];
-      const uint32_t wh = w >> (4 * half);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const float p = exp2_fast(fmaf(sa[r], a.c, -lse2));
-        ds[r] = ((wh >> acc_row(r, 0)) & 1u) ? p * (pa[r] - delta) : 0.f;
-      }
+      for (int r = 0; r < 16; ++r) ds[r] = exp2_fast(fmaf(s[r], a.c, -lse2)) * (p[r] - delta);
       typename POperand<T>::type pf;
       to_operand(ds, pf);
 #pragma unroll
-      for (int i = 0; i < DT; ++i) o[i] = mma_rows<DP>(ks, r0, 32 * i, pf, o[i]);
+      for (int i = 0; i < DT; ++i) o[i] = mma_rows<DP>(ks, 32 * n, 32 * i, pf, o[i]);
     }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) word[j] = word[j + 1];
+    slot = slot == STAGES - 1 ? 0 : slot + 1;
   }
-  join_sum<DP, WQ, WK>(o, reinterpret_cast<float*>(smem), [&](int rr, int d, float4 v) {
-    const int orow = rt * 32 * WQ + rr;
+  __syncthreads();
+  rows_out(o, reinterpret_cast<float*>(lds) + wave * 32 * 36, [&](int rr, int d, float4 v) {
+    const int at = wave * 32 + rr, orow = w.row0 + at;
     if (orow >= a.R) return;
-    if (a.splits > 1) {
-      const int64_t prow = (static_cast<int64_t>(split) * nbh + bh) * a.R + orow;
-      *reinterpret_cast<float4*>(a.part + prow * DP + d) = v;
-      return;
-    }
-    const int pos = orow / a.g, head = hk * a.g + orow % a.g;
-    store4<T>(static_cast<T*>(a.dq) + ((static_cast<int64_t>(b) * a.Lq + pos) * a.Hq + head) * a.D, d, a.D, v,
-              a.scale);
+    if (w.tail >= 0)
+      *reinterpret_cast<float4*>(a.part + ((static_cast<int64_t>(w.tail) * a.y.splits + w.split) * 128 + at) * DP + d) = v;
+    else
+      store4<T>(dq_row<T>(a, w, orow), d, a.D, v, a.scale);
   });
 }
 
-// WC waves of 32 keys each share the row tiles; with WS > 1 the waves take 32 rows each of a
-// tile and the same keys.
-template <typename T, int DP, int WC, int WS, bool VEC>
-__global__ __launch_bounds__(64 * WC * WS) void attn_dkv_kernel(Args a) {
-  constexpr int NT = 64 * WC * WS, KV = Elem<T>::kVec, ST = DP;
-  constexpr int SUB = WS == 1 ? 2 : 1, RT = 32 * SUB * WS, VPR = DP / KV, NV = RT * VPR / NT, DT = DP / 32;
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  T* qs = reinterpret_cast<T*>(smem);
-  T* gs = qs + RT * ST;
-  float* ls = reinterpret_cast<float*>(gs + RT * ST);   // [RT] lse, [RT] delta
-  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, wave = tid >> 6;
-  const int wc = wave / WS, wr = wave % WS;
-  const int nbh = a.B * a.Hkv;
-  int id = blockIdx.x;
-  const int bh = id % nbh;
-  id /= nbh;
-  const int split = id % a.splits, kt = id / a.splits;
-  const int b = bh / a.Hkv, hk = bh % a.Hkv;
-  const T* qp = static_cast<const T*>(a.q) + b * a.qs[0];
-  const T* gp = static_cast<const T*>(a.dout) + static_cast<int64_t>(b) * a.Lq * a.Hq * a.D;
-
-  const int key = kt * 32 * WC + wc * 32 + (lane & 31);
+template <typename T, int DP, int STAGES, bool VEC>
+__device__ __forceinline__ void dkv_part(const Args& a, int tile, T* lds) {
+  constexpr int DT = DP / 32, BUF = 2 * kT * DP, AHEAD = STAGES - 1, LOADS = VEC ? 2 * tile_loads<T, DP, kT, 256> + 1 : 1;
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  float* const vals = reinterpret_cast<float*>(lds + STAGES * BUF);   // [STAGES][lse, delta][kT]
+  const Work w = work_of(a, a.ykv, tile, 128, (a.R + kT - 1) / kT);
+  const int key = w.row0 + wave * 32 + (lane & 31);
   bool live = key < a.Lk;
-  if (a.mask != nullptr && live) live = a.mask[b * a.ms + key] != 0;
+  if (a.mask != nullptr && live) live = a.mask[w.b * a.ms + key] != 0;
   Frag<T> kf[DP / 16], vf[DP / 16];
-  {
-    const T* kp = static_cast<const T*>(a.k) + b * a.ks[0] + hk * a.ks[2] + (live ? key : 0) * a.ks[1];
-    const T* vp = static_cast<const T*>(a.v) + b * a.vs[0] + hk * a.vs[2] + (live ? key : 0) * a.vs[1];
-    load_frags<T, DP, VEC>(kp, 0, a.D, live, kf);
-    load_frags<T, DP, VEC>(vp, 0, a.D, live, vf);
-  }
+  load_frags<T, DP, VEC>(static_cast<const T*>(a.k) + w.b * a.ks[0] + w.hk * a.ks[2] + (live ? key : 0) * a.ks[1], 0, a.D,
+                         live, kf);
+  load_frags<T, DP, VEC>(static_cast<const T*>(a.v) + w.b * a.vs[0] + w.hk * a.vs[2] + (live ? key : 0) * a.vs[1], 0, a.D,
+                         live, vf);
   f32x16 ok[DT], ov[DT];
 #pragma unroll
   for (int i = 0; i < DT; ++i) {
     ok[i] = zero_acc();
     ov[i] = zero_acc();
   }
+  const f32x16 zeros = zero_acc();
   const bool any = __any(live);
-  const int tiles = (a.R + RT - 1) / RT;
-  const int t0 = split * a.per_split;
-  // keys that are all padding have no gradient and read no rows
-  const int t1 = __syncthreads_or(any) ? min(tiles, t0 + a.per_split) : t0;
-  Vec16<T> qr[NV], gr[NV];
-  float lr = 0.f;
-  const auto load_tile = [&](int t) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int at = tid + i * NT, row = t * RT + at / VPR, d = (at % VPR) * KV;
-      const bool in = row < a.R;
-      const int pos = in ? row / a.g : 0, head = hk * a.g + (in ? row % a.g : 0);
-      qr[i] = load_vec<T, VEC>(qp + pos * a.qs[1] + head * a.qs[2], 0, d, a.D, in);
-      gr[i] = load_vec<T, VEC>(gp + (static_cast<int64_t>(pos) * a.Hq + head) * a.D, 0, d, a.D, in);
-    }
-    if (tid < 2 * RT) {
-      const int row = t * RT + (tid >> 1);
-      lr = row < a.R ? a.delta[(static_cast<int64_t>(bh) * a.R + row) * 2 + (tid & 1)]
-                     : ((tid & 1) ? 0.f : -kNegInf);
-    }
-  };
-  static_assert(2 * RT <= NT, "one thread per row value");
-  if (t0 < t1) load_tile(t0);
-  for (int t = t0; t < t1; ++t) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int at = tid + i * NT, row = at / VPR, d = (at % VPR) * KV;
-      *reinterpret_cast<uint4*>(qs + Tile<T, DP>::at(row, d)) = qr[i].u;
-      *reinterpret_cast<uint4*>(gs + Tile<T, DP>::at(row, d)) = gr[i].u;
-    }
-    if (tid < 2 * RT) ls[(tid & 1) * RT + (tid >> 1)] = lr;
-    __syncthreads();
-    if (t + 1 < t1) load_tile(t + 1);
-    if (!any) continue;
-#pragma unroll
-    for (int s = 0; s < SUB; ++s) {
-      const int r0 = wr * 32 * SUB + s * 32;
-      f32x16 sa = zero_acc(), pa = zero_acc();
-#pragma unroll
-      for (int i = 0; i < DP / 16; ++i) {
-        sa = mma(row_frag<DP>(qs, r0, i), kf[i], sa);
-        pa = mma(row_frag<DP>(gs, r0, i), vf[i], pa);
+  // keys that are all padding have no gradient, and no rows are read for them
+  const int s1 = __syncthreads_or(any) ? w.s1 : w.s0;
+  const T* qb = static_cast<const T*>(a.q) + w.b * a.qs[0] + w.hk * a.g * a.qs[2];
+  const T* gb = static_cast<const T*>(a.dout) + (static_cast<int64_t>(w.b) * a.Lq * a.Hq + w.hk * a.g) * a.D;
+  const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv * a.R, row_base = static_cast<int64_t>(w.b * a.Hkv + w.hk) * a.R;
+  const auto send = [&](int t, int slot) {
+    const int r0 = t * kT, n = min(kT, a.R - r0);
+    const uint64_t in = n == 64 ? ~uint64_t{0} : (uint64_t{1} << n) - 1;
+    // rows run over the heads that share the key head, then over positions
+    const int pos0 = r0 / a.g, h0 = r0 - pos0 * a.g;
+    const auto split = [&](int r, int& pos, int& h) {
+      pos = r;
+      h = 0;
+      if (a.g > 1) {
+        const unsigned x = static_cast<unsigned>(h0 + r);
+        pos = static_cast<int>(x / static_cast<unsigned>(a.g));
+        h = static_cast<int>(x) - pos * a.g;
       }
-      float p[16], ds[16];
+    };
+    fetch_tile<T, DP, kT, 256, VEC>(lds + slot * BUF, qb + pos0 * a.qs[1], [&](int r) {
+      int pos, h;
+      split(r, pos, h);
+      return pos * a.qs[1] + h * a.qs[2];
+    }, in, a.D, tid);
+    fetch_tile<T, DP, kT, 256, VEC>(lds + slot * BUF + kT * DP, gb + static_cast<int64_t>(pos0) * a.Hq * a.D, [&](int r) {
+      int pos, h;
+      split(r, pos, h);
+      return (static_cast<int64_t>(pos) * a.Hq + h) * a.D;
+    }, in, a.D, tid);
+    // lse by waves 0 and 2, delta by 1 and 3 (a pair writes the same values, and every wave has as many loads
+    // under way); rows beyond the last give zeros, and their zero query and gradient rows add nothing
+    const int which = wave & 1;
+    const __amdgpu_buffer_rsrc_t rs = rsrc_of(a.delta + which * rows + row_base + r0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(vals + slot * kRowVals + which * kT), 4,
+                                             lane < n ? lane * 4 : kOutside, 0, 0, 0);
+  };
 #pragma unroll
-      for (int r4 = 0; r4 < 4; ++r4) {
-        const float4 lse = *reinterpret_cast<const float4*>(ls + r0 + acc_row(4 * r4, half));
-        const float4 del = *reinterpret_cast<const float4*>(ls + RT + r0 + acc_row(4 * r4, half));
-        const float le[4] = {lse.x, lse.y, lse.z, lse.w}, de[4] = {del.x, del.y, del.z, del.w};
+  for (int j = 0; j < AHEAD; ++j)
+    if (w.s0 + j < s1) send(w.s0 + j, j);
+  int slot = 0;
+  for (int t = w.s0; t < s1; ++t) {
+    if (AHEAD == 2 && t + 1 < s1) wait_loads<LOADS>();
+    else wait_loads<0>();
+    lds_barrier();
+    if (t + AHEAD < s1) send(t + AHEAD, slot == 0 ? STAGES - 1 : slot - 1);
+    const T* qs = lds + slot * BUF;
+    const T* gs = qs + kT * DP;
+    const float* ls = vals + slot * kRowVals;
+    if (any) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = 4 * r4 + j;
-          p[r] = live ? exp2_fast(fmaf(sa[r], a.c, -le[j])) : 0.f;
-          ds[r] = p[r] * (pa[r] - de[j]);
+      for (int n = 0; n < 2; ++n) {
+        const int r0 = 32 * n;
+        f32x16 s = zeros, dp = zeros;
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i) {
+          s = mma(row_frag<DP>(qs, r0, i), kf[i], s);
+          dp = mma(row_frag<DP>(gs, r0, i), vf[i], dp);
+        }
+        float p[16], ds[16];
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+          const float4 lse = *reinterpret_cast<const float4*>(ls + r0 + acc_row(4 * r4, half));
+          const float4 del = *reinterpret_cast<const float4*>(ls + kT + r0 + acc_row(4 * r4, half));
+          const float le[4] = {lse.x, lse.y, lse.z, lse.w}, de[4] = {del.x, del.y, del.z, del.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = 4 * r4 + j;
+            p[r] = exp2_fast(fmaf(s[r], a.c, -le[j]));
+            ds[r] = p[r] * (dp[r] - de[j]);
+          }
+        }
+        typename POperand<T>::type pf, df;
+        to_operand(p, pf);
+        to_operand(ds, df);
+#pragma unroll
+        for (int i = 0; i < DT; ++i) {
+          ov[i] = mma_rows<DP>(gs, r0, 32 * i, pf, ov[i]);
+          ok[i] = mma_rows<DP>(qs, r0, 32 * i, df, ok[i]);
         }
       }
-      typename POperand<T>::type pf, df;
-      to_operand(p, pf);
-      to_operand(ds, df);
-#pragma unroll
-      for (int i = 0; i < DT; ++i) {
-        ov[i] = mma_rows<DP>(gs, r0, 32 * i, pf, ov[i]);
-        ok[i] = mma_rows<DP>(qs, r0, 32 * i, df, ok[i]);
-      }
     }
+    slot = slot == STAGES - 1 ? 0 : slot + 1;
   }
-  const int64_t keys = static_cast<int64_t>(nbh) * a.Lk;
+  // a lane whose key is padding has summed the weights of a zero key row: its gradients are 0
+  if (!live) {
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) ok[i][r] = ov[i][r] = 0.f;
+  }
+  __syncthreads();
   const auto store = [&](int rr, int d, float4 v, int which) {
-    const int okey = kt * 32 * WC + rr;
+    const int at = wave * 32 + rr, okey = w.row0 + at;
     if (okey >= a.Lk) return;
-    if (a.splits > 1) {
-      const int64_t prow = (static_cast<int64_t>(split) * 2 + which) * keys + static_cast<int64_t>(bh) * a.Lk + okey;
-      *reinterpret_cast<float4*>(a.part + prow * DP + d) = v;
+    if (w.tail >= 0) {
+      const int64_t part = (static_cast<int64_t>(w.tail) * a.ykv.splits + w.split) * 2 + which;
+      *reinterpret_cast<float4*>(a.part_kv + (part * 128 + at) * DP + d) = v;
       return;
     }
-    T* out = static_cast<T*>(which ? a.dv : a.dk);
-    if (out == nullptr) return;
-    store4<T>(out + ((static_cast<int64_t>(b) * a.Lk + okey) * a.Hkv + hk) * a.D, d, a.D, v, which ? 1.f : a.scale);
+    T* out = dkv_row<T>(a, w, okey, which);
+    if (out != nullptr) store4<T>(out, d, a.D, v, which ? 1.f : a.scale);
   };
-  join_sum<DP, WC, WS>(ok, reinterpret_cast<float*>(smem), [&](int rr, int d, float4 v) { store(rr, d, v, 0); });
-  join_sum<DP, WC, WS>(ov, reinterpret_cast<float*>(smem), [&](int rr, int d, float4 v) { store(rr, d, v, 1); });
+  float* os = reinterpret_cast<float*>(lds) + wave * 32 * 36;
+  rows_out(ok, os, [&](int rr, int d, float4 v) { store(rr, d, v, 0); });
+  rows_out(ov, os, [&](int rr, int d, float4 v) { store(rr, d, v, 1); });
 }
 
-// Adds up split parts: one thread for 4 elements of a row; rows of dQ, or keys of dK, dV.
-template <typename T, int DP, bool KEYS>
-__global__ __launch_bounds__(256) void attn_add_kernel(Args a) {
+// Workgroups 0 .. kv - 1: dK and dV; the others: dQ.
+template <typename T, int DP, int STAGES, bool VEC>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DP * sizeof(T) <= 128 ? 2 : 1)))
+void attn_grad_kernel(Args a, int kv) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  T* lds = reinterpret_cast<T*>(smem);
+  if (static_cast<int>(blockIdx.x) < kv) dkv_part<T, DP, STAGES, VEC>(a, blockIdx.x, lds);
+  else dq_part<T, DP, STAGES, VEC>(a, blockIdx.x - kv, lds);
+}
+
+// Adds up the parts of split tiles: one thread for 4 elements of a row of dQ, or a key of dK or
+// dV (vectors `q4` and beyond).
+template <typename T, int DP>
+__global__ __launch_bounds__(256) void attn_grad_add_kernel(Args a, int64_t q4, int64_t n4) {
   constexpr int V4 = DP / 4;
-  const int nbh = a.B * a.Hkv, len = KEYS ? a.Lk : a.R;
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t rows = static_cast<int64_t>(nbh) * len * (KEYS ? 2 : 1), prow = at / V4;
-  const int d = static_cast<int>(at % V4) * 4;
-  if (prow >= rows) return;
+  int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= n4) return;
+  const bool kv = at >= q4;
+  if (kv) at -= q4;
+  const Tiling& y = kv ? a.ykv : a.y;
+  const int d = static_cast<int>(at % V4) * 4, rr = static_cast<int>(at / V4 % 128);
+  const int64_t unit = at / V4 / 128;
+  const int which = kv ? static_cast<int>(unit % 2) : 0, tail = static_cast<int>(kv ? unit / 2 : unit);
+  const int nbh = a.B * a.Hkv, tile = y.full + tail, bh = tile % nbh;
+  Work w;
+  w.b = bh / a.Hkv;
+  w.hk = bh % a.Hkv;
+  w.row0 = tile / nbh * 128;
+  if (w.row0 + rr >= (kv ? a.Lk : a.R)) return;
+  const int64_t step = static_cast<int64_t>(kv ? 2 : 1) * 128 * DP;
+  const float* p = (kv ? a.part_kv : a.part) + (static_cast<int64_t>(tail) * y.splits * (kv ? 2 : 1) + which) * 128 * DP +
+                   static_cast<int64_t>(rr) * DP + d;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < a.splits; ++s) {
-    const float4 v = *reinterpret_cast<const float4*>(a.part + (s * rows + prow) * DP + d);
+#pragma unroll 4
+  for (int s = 0; s < y.splits; ++s) {
+    const float4 v = *reinterpret_cast<const float4*>(p + s * step);
     acc.x += v.x;
     acc.y += v.y;
     acc.z += v.z;
     acc.w += v.w;
   }
-  const int which = KEYS && prow >= rows / 2;
-  const int64_t one = prow - (which ? rows / 2 : 0);
-  const int bh = static_cast<int>(one / len), r = static_cast<int>(one % len), b = bh / a.Hkv, hk = bh % a.Hkv;
-  if (KEYS) {
-    T* out = static_cast<T*>(which ? a.dv : a.dk);
-    if (out == nullptr) return;
-    store4<T>(out + ((static_cast<int64_t>(b) * a.Lk + r) * a.Hkv + hk) * a.D, d, a.D, acc, which ? 1.f : a.scale);
-  } else {
-    store4<T>(static_cast<T*>(a.dq) + ((static_cast<int64_t>(b) * a.Lq + r / a.g) * a.Hq + hk * a.g + r % a.g) * a.D,
-              d, a.D, acc, a.scale);
-  }
-}
-
-constexpr int kCUs = 256;
-
-struct GradPlan {
-  int dp, wide, splits, per_split, tile;
-};
-// `outer` rows (or keys) held by the waves, `inner` looped over.
-GradPlan make_plan(int64_t nbh, int64_t outer, int64_t inner, int64_t D) {
-  GradPlan p{};
-  p.dp = D <= 32 ? 32 : D <= 64 ? 64 : 128;
-  p.wide = outer > 96 && nbh * ((outer + 127) / 128) >= 2 * kCUs;
-  p.tile = p.wide ? 64 : 128;
-  const int64_t tiles = std::max<int64_t>(1, (inner + p.tile - 1) / p.tile);
-  int64_t splits = 1;
-  if (!p.wide) {
-    const int64_t groups = std::max<int64_t>(1, nbh * ((outer + 31) / 32));
-    splits = std::min<int64_t>(std::max<int64_t>(1, 2 * kCUs / groups), std::max<int64_t>(1, tiles / 2));
-  }
-  p.per_split = static_cast<int>((tiles + splits - 1) / splits);
-  p.splits = static_cast<int>((tiles + p.per_split - 1) / p.per_split);
-  return p;
-}
-
-size_t lds_bytes(const GradPlan& p, int es) {
-  const size_t tile = static_cast<size_t>(2) * p.tile * p.dp * es + static_cast<size_t>(p.tile) * 8;
-  return std::max(tile, static_cast<size_t>(4) * 32 * (p.dp + 4) * 4);
+  T* out = kv ? dkv_row<T>(a, w, w.row0 + rr, which) : dq_row<T>(a, w, w.row0 + rr);
+  if (out != nullptr) store4<T>(out, d, a.D, acc, which ? 1.f : a.scale);
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Layout {
-  GradPlan q, kv;
-  size_t part_at, bytes;   // row values first, then the parts of whichever kernel runs
+  int dp;
+  Tiling q, kv;
+  size_t part_at, part_kv_at, bytes;   // the row values come first
 };
 
 Layout make_layout(const dcn_attn_desc* d) {
   Layout y{};
+  y.dp = padded_head(d->head_dim);
   const int64_t nbh = d->batch * d->key_heads, R = d->query_len * (d->query_heads / d->key_heads);
-  y.q = make_plan(nbh, R, d->key_len, d->head_dim);
-  y.kv = make_plan(nbh, d->key_len, R, d->head_dim);
+  const int64_t rows = (R + kT - 1) / kT, keys = (d->key_len + kT - 1) / kT;
+  y.q = tile_over(nbh * ((R + 127) / 128), keys, 2 * kCUs, 2);
+  y.kv = tile_over(nbh * ((d->key_len + 127) / 128), rows, 2 * kCUs, 2);
   y.part_at = up256(static_cast<size_t>(nbh) * R * 8);
-  size_t part = 0;
-  if (y.q.splits > 1) part = static_cast<size_t>(y.q.splits) * nbh * R * y.q.dp * 4;
-  if (y.kv.splits > 1) part = std::max(part, static_cast<size_t>(y.kv.splits) * 2 * nbh * d->key_len * y.kv.dp * 4);
-  y.bytes = y.part_at + up256(part);
+  const size_t tile = static_cast<size_t>(128) * y.dp * 4;
+  y.part_kv_at = y.part_at + static_cast<size_t>(y.q.tiles - y.q.full) * y.q.splits * tile;
+  y.bytes = y.part_kv_at + static_cast<size_t>(y.kv.tiles - y.kv.full) * y.kv.splits * 2 * tile;
   return y;
 }
 
-enum Which { DQ, DKV };
-template <typename T, int DP, int A, int B, bool VEC>
-const void* grad_kernel(Which w) {
-  return w == DQ ? reinterpret_cast<const void*>(&attn_dq_kernel<T, DP, A, B, VEC>)
-                 : reinterpret_cast<const void*>(&attn_dkv_kernel<T, DP, A, B, VEC>);
-}
-template <typename T, int DP>
-const void* grad_kernel(Which w, bool wide, bool vec) {
-  if (wide) return vec ? grad_kernel<T, DP, 4, 1, true>(w) : grad_kernel<T, DP, 4, 1, false>(w);
-  return vec ? grad_kernel<T, DP, 1, 4, true>(w) : grad_kernel<T, DP, 1, 4, false>(w);
-}
-template <typename T>
-const void* grad_kernel(Which w, int dp, bool wide, bool vec) {
-  return dp == 32   ? grad_kernel<T, 32>(w, wide, vec)
-         : dp == 64 ? grad_kernel<T, 64>(w, wide, vec)
-                    : grad_kernel<T, 128>(w, wide, vec);
-}
-template <typename T, bool KEYS>
-const void* add_kernel(int dp) {
-  return dp == 32   ? reinterpret_cast<const void*>(&attn_add_kernel<T, 32, KEYS>)
-         : dp == 64 ? reinterpret_cast<const void*>(&attn_add_kernel<T, 64, KEYS>)
-                    : reinterpret_cast<const void*>(&attn_add_kernel<T, 128, KEYS>);
+size_t grad_lds(int row_bytes) {
+  const size_t ring = static_cast<size_t>(stages_of(row_bytes)) * (2 * kT * row_bytes + kRowVals * 4);
+  return std::max<size_t>(ring, 4 * 32 * 36 * 4);
 }
 
-bool launch(const void* fn, int64_t grid, size_t lds, Args* a, hipStream_t stream) {
-  void* args[] = {a};
-  return grid == 0 ||
-         hipLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(256), args, lds, stream) == hipSuccess;
+template <typename T, int DP>
+const void* grad_kernel(bool vec) {
+  constexpr int S = stages_of(DP * sizeof(T));
+  return vec ? reinterpret_cast<const void*>(&attn_grad_kernel<T, DP, S, true>)
+             : reinterpret_cast<const void*>(&attn_grad_kernel<T, DP, S, false>);
+}
+template <typename T, int DP>
+const void* rows_kernel(bool vec) {
+  return vec ? reinterpret_cast<const void*>(&attn_grad_rows_kernel<T, DP, true>)
+             : reinterpret_cast<const void*>(&attn_grad_rows_kernel<T, DP, false>);
+}
+
+template <typename T, int DP>
+int run_grad(Args& a, const Layout& y, bool vec, hipStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv * a.R;
+  void* args[] = {&a};
+  if (rows > 0) {
+    const int per = vec ? 256 / Tile<T, DP>::kVecs : 16;
+    if (hipLaunchKernel(rows_kernel<T, DP>(vec), dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(256), args, 0,
+                        stream) != hipSuccess)
+      return DCN_E_HIP;
+  }
+  const bool q = a.dq != nullptr && rows > 0, keys = (a.dk != nullptr || a.dv != nullptr) && a.Lk > 0;
+  const int64_t kv = keys ? workgroups(y.kv) : 0, grid = kv + (q ? workgroups(y.q) : 0);
+  if (grid == 0) return DCN_OK;
+  int kv32 = static_cast<int>(kv);
+  void* grad_args[] = {&a, &kv32};
+  if (hipLaunchKernel(grad_kernel<T, DP>(vec), dim3(static_cast<unsigned>(grid)), dim3(256), grad_args,
+                      grad_lds(DP * sizeof(T)), stream) != hipSuccess)
+    return DCN_E_HIP;
+  int64_t q4 = q ? static_cast<int64_t>(y.q.tiles - y.q.full) * 128 * (DP / 4) : 0;
+  int64_t n4 = q4 + (keys ? static_cast<int64_t>(y.kv.tiles - y.kv.full) * 2 * 128 * (DP / 4) : 0);
+  if (n4 == 0) return DCN_OK;
+  void* add_args[] = {&a, &q4, &n4};
+  return hipLaunchKernel(reinterpret_cast<const void*>(&attn_grad_add_kernel<T, DP>),
+                         dim3(static_cast<unsigned>((n4 + 255) / 256)), dim3(256), add_args, 0, stream) == hipSuccess
+             ? DCN_OK
+             : DCN_E_HIP;
+}
+template <typename T>
+int run_grad(Args& a, const Layout& y, bool vec, hipStream_t stream) {
+  return y.dp == 32   ? run_grad<T, 32>(a, y, vec, stream)
+         : y.dp == 64 ? run_grad<T, 64>(a, y, vec, stream)
+                      : run_grad<T, 128>(a, y, vec, stream);
 }
 
 }  // namespace
@@ -476,42 +484,18 @@ extern "C" int dcn_cross_attention_backward(const dcn_attn_desc* d, const void* 
   a.dout = grad_out;
   a.delta = static_cast<const float*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + y.part_at);
+  a.part_kv = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + y.part_kv_at);
   a.dq = grad_q;
   a.dk = grad_k;
   a.dv = grad_v;
+  a.y = y.q;
+  a.ykv = y.kv;
   const bool bf16 = d->dtype == DCN_BF16;
   const int es = bf16 ? 2 : 4;
-  const int64_t dense[3] = {0, 0, d->head_dim};
+  // out and grad_out are dense; a row tile's positions have to lie within 32 bits of each other too
+  const int64_t dense[3] = {0, d->query_heads * d->head_dim, d->head_dim};
   const bool vec = vec_ok(q, d->q_stride, d->head_dim, es) && vec_ok(k, d->k_stride, d->head_dim, es) &&
-                   vec_ok(v, d->v_stride, d->head_dim, es) && vec_ok(grad_out, dense, d->head_dim, es);
-  const int64_t nbh = d->batch * d->key_heads, R = a.R;
-  if (rows) {
-    const void* fn = bf16 ? reinterpret_cast<const void*>(&attn_rows_kernel<uint16_t>)
-                          : reinterpret_cast<const void*>(&attn_rows_kernel<float>);
-    if (!launch(fn, (nbh * R + 15) / 16, 0, &a, stream)) return DCN_E_HIP;
-  }
-  if (grad_q != nullptr && rows) {
-    a.splits = y.q.splits;
-    a.per_split = y.q.per_split;
-    const int64_t tiles = (R + (y.q.wide ? 127 : 31)) / (y.q.wide ? 128 : 32);
-    const void* fn = bf16 ? grad_kernel<uint16_t>(DQ, y.q.dp, y.q.wide, vec) : grad_kernel<float>(DQ, y.q.dp, y.q.wide, vec);
-    if (!launch(fn, nbh * tiles * a.splits, lds_bytes(y.q, es), &a, stream)) return DCN_E_HIP;
-    if (a.splits > 1) {
-      fn = bf16 ? add_kernel<uint16_t, false>(y.q.dp) : add_kernel<float, false>(y.q.dp);
-      if (!launch(fn, (nbh * R * (y.q.dp / 4) + 255) / 256, 0, &a, stream)) return DCN_E_HIP;
-    }
-  }
-  if ((grad_k != nullptr || grad_v != nullptr) && keys) {
-    a.splits = y.kv.splits;
-    a.per_split = y.kv.per_split;
-    const int64_t tiles = (d->key_len + (y.kv.wide ? 127 : 31)) / (y.kv.wide ? 128 : 32);
-    const void* fn =
-        bf16 ? grad_kernel<uint16_t>(DKV, y.kv.dp, y.kv.wide, vec) : grad_kernel<float>(DKV, y.kv.dp, y.kv.wide, vec);
-    if (!launch(fn, nbh * tiles * a.splits, lds_bytes(y.kv, es), &a, stream)) return DCN_E_HIP;
-    if (a.splits > 1) {
-      fn = bf16 ? add_kernel<uint16_t, true>(y.kv.dp) : add_kernel<float, true>(y.kv.dp);
-      if (!launch(fn, (2 * nbh * d->key_len * (y.kv.dp / 4) + 255) / 256, 0, &a, stream)) return DCN_E_HIP;
-    }
-  }
-  return DCN_OK;
+                   vec_ok(v, d->v_stride, d->head_dim, es) && vec_ok(grad_out, dense, d->head_dim, es) &&
+                   vec_ok(out, dense, d->head_dim, es) && 64 * d->q_stride[1] + (a.g - 1) * d->q_stride[2] <= int64_t{1} << 28;
+  return bf16 ? run_grad<uint16_t>(a, y, vec, stream) : run_grad<float>(a, y, vec, stream);
 }

@@ -142,7 +142,7 @@ def test_empty_batch_and_only_the_gradients_asked_for():
         x, G, w, b, go = make(name, "bf16", "silu")
         _, mean, rstd = dcn.group_norm_act(x, G, w, b, return_stats=True)
         full = dcn.group_norm_act_backward(go, x, mean, rstd, G, w, b, activation="silu")
-        desc = dcn._norm_desc(x, G, w, b, 0.0, "silu")
+        desc = dcn.norm_desc(x, G, w, b, activation="silu")
         nb = dcn.dcn_group_norm_backward_workspace_bytes(desc)
         ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
         for wanted in ((0,), (1,), (2,), (0, 2)):
