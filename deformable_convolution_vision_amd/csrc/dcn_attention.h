@@ -292,6 +292,16 @@ __device__ __forceinline__ void fetch_tile(T* lds, const T* base, Offset offset,
   }
 }
 
+// Has what a fragment's loads bring awaited here, and not again in every turn of a loop that
+// follows (where the wait would take in all that is on its way to the LDS).
+template <typename T, int N>
+__device__ __forceinline__ void arrived(Frag<T> (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < static_cast<int>(sizeof(T)) * 2; ++j) asm volatile("" : "+v"(reinterpret_cast<uint32_t*>(&f[i])[j]));
+}
+
 // The key tiles of a row tile that hold attended keys, 64 keys each, in order: mask bits and
 // position.  32 tiles' bits are in the lanes at a time (the same in every wave).
 struct KeyTiles {
@@ -310,6 +320,10 @@ struct KeyTiles {
   __device__ __forceinline__ uint64_t next(int64_t& k0) {
     uint64_t word = 0;
     for (; t < end && word == 0; ++t) {
+      if (mp == nullptr && (t + 1) * 64 <= Lk) {
+        word = ~uint64_t{0};
+        continue;
+      }
       if (t >= win + 32) fill();
       const int i = 2 * (t - win);
       word = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(words, i))) |
@@ -361,18 +375,21 @@ struct POperand<uint16_t> { using type = PFrag16; };
 template <>
 struct POperand<float> { using type = PFrag32; };
 
-// r0: the first of the 32 rows, a multiple of 32
+// The transposed operand of 16 rows (h: the first or second 16 of the 32 that start at r0, a
+// multiple of 32).
 template <int DP>
-__device__ __forceinline__ f32x16 mma_rows(const uint16_t* tile, int r0, int d0, const PFrag16& p, f32x16 acc) {
+__device__ __forceinline__ Frag<uint16_t> col_frag(const uint16_t* tile, int r0, int d0, int h) {
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
   const int l = threadIdx.x & 63, i = l & 15, r = r0 + 4 * (l >> 5) + (i >> 2), d = d0 + 16 * ((l >> 4) & 1) + 4 * (i & 3);
+  Frag<uint16_t> a;
+  a.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + Tile<uint16_t, DP>::at(r + 16 * h, d)));
+  a.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + Tile<uint16_t, DP>::at(r + 16 * h + 8, d)));
+  return a;
+}
+template <int DP>
+__device__ __forceinline__ f32x16 mma_rows(const uint16_t* tile, int r0, int d0, const PFrag16& p, f32x16 acc) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    Frag<uint16_t> a;
-    a.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + Tile<uint16_t, DP>::at(r + 16 * h, d)));
-    a.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + Tile<uint16_t, DP>::at(r + 16 * h + 8, d)));
-    acc = mma(a, p.f[h], acc);
-  }
+  for (int h = 0; h < 2; ++h) acc = mma(col_frag<DP>(tile, r0, d0, h), p.f[h], acc);
   return acc;
 }
 template <int DP>

@@ -54,9 +54,26 @@ struct Running {
   float m = kNegInf, l = 0.f;
 };
 
+// Takes the maximum of a lane's new scores into account.  Any m serves the formulas: it is only
+// to keep the weights within range.  So it is raised, and what is summed is rescaled, only when
+// scores exceed it by more than 2^8 (and at the first ones), which is seldom after a few tiles;
+// the weights then reach up to 2^8.
+template <int DT>
+__device__ __forceinline__ void raise_max(float mt, Running& run, f32x16 (&o)[DT]) {
+  if (__any(mt > run.m + 8.f)) {
+    const float mn = fmaxf(run.m, mt), alpha = run.m == kNegInf ? 0.f : exp2_fast(run.m - mn);
+    run.m = mn;
+    run.l *= alpha;
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[i][r] *= alpha;
+  }
+}
+
 // Takes N blocks of 32 scores in (raw products; word: the attended keys of each), gives the
-// weights as the second product's operands, and rescales the output accumulators when the
-// maximum rises.  Maximum and sum run in four strands each: one would wait for itself.
+// weights as the second product's operands.  Maximum and sum run in four strands each: one would
+// wait for itself.
 template <typename T, int N, int DT>
 __device__ __forceinline__ void softmax_step(f32x16 (&s)[N], const uint32_t (&word)[N], float c, Running& run,
                                              f32x16 (&o)[DT], typename POperand<T>::type (&pf)[N]) {
@@ -73,16 +90,7 @@ __device__ __forceinline__ void softmax_step(f32x16 (&s)[N], const uint32_t (&wo
       if (n > 0) mt[j] = max3(mt[j], s[n][4 * j], s[n][4 * j + 1]);
       mt[j] = max3(mt[j], s[n][4 * j + 2], s[n][4 * j + 3]);
     }
-  const float mn = fmaxf(run.m, max_halves(fmaxf(max3(mt[0], mt[1], mt[2]), mt[3])) * c);
-  if (__any(mn != run.m)) {
-    const float alpha = run.m == kNegInf ? 0.f : exp2_fast(run.m - mn);
-    run.m = mn;
-    run.l *= alpha;
-#pragma unroll
-    for (int i = 0; i < DT; ++i)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) o[i][r] *= alpha;
-  }
+  raise_max(max_halves(fmaxf(max3(mt[0], mt[1], mt[2]), mt[3])) * c, run, o);
   const float ms = run.m == kNegInf ? 0.f : run.m;   // no key counted yet: exp2(-inf) = 0
   float sum[4] = {run.l, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -184,10 +192,11 @@ constexpr size_t join_lds(int waves) { return static_cast<size_t>(waves) * 32 * 
 // The next block's rows are on their way while one is worked on.
 template <typename T, int DP, int W, bool VEC>
 __global__ __launch_bounds__(64 * W) void attn_few_rows_kernel(Args a) {
+  constexpr int AHEAD = 1;   // blocks on their way while one is worked on
   constexpr int DT = DP / 32, KL = DP * static_cast<int>(sizeof(T)) / 32, VL = tile_loads<T, DP, 32, 64>;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  T* const lds = reinterpret_cast<T*>(smem) + wave * 2 * 32 * DP;
+  T* const lds = reinterpret_cast<T*>(smem) + wave * (AHEAD + 1) * 32 * DP;
   const Work w = work_of(a, a.y, blockIdx.x, 32, (a.Lk + 32 * W - 1) / (32 * W));
   const T* kp = static_cast<const T*>(a.k) + w.b * a.ks[0] + w.hk * a.ks[2];
   const T* vp = static_cast<const T*>(a.v) + w.b * a.vs[0] + w.hk * a.vs[2];
@@ -199,7 +208,7 @@ __global__ __launch_bounds__(64 * W) void attn_few_rows_kernel(Args a) {
   for (int i = 0; i < DT; ++i) o[i] = zero_acc();
   Running run;
 
-  Frag<T> kf[DP / 16], kn[DP / 16];
+  Frag<T> kf[AHEAD + 1][DP / 16];
   // Rows of padded keys are taken as zeros and not read: a padded key's weight is exactly 0,
   // but 0 times an infinity or NaN in its value row would not be.
   const auto load_keys = [&](int64_t k0, uint32_t word, Frag<T> (&f)[DP / 16]) {
@@ -221,58 +230,71 @@ __global__ __launch_bounds__(64 * W) void attn_few_rows_kernel(Args a) {
       load_frags<T, DP, false>(kp + k0 * a.ks[1], (lane & 31) * a.ks[1], a.D, in, f);
     }
   };
-  const auto load_values = [&](int64_t k0, uint32_t word, int slot) {
-    fetch_tile<T, DP, 32, 64, VEC>(lds + slot * 32 * DP, vp + k0 * a.vs[1], [&](int r) { return r * a.vs[1]; }, word, a.D,
+  const auto load_values = [&](int64_t k0, uint32_t word, T* __restrict__ to) {
+    fetch_tile<T, DP, 32, 64, VEC>(to, vp + k0 * a.vs[1], [&](int r) { return r * a.vs[1]; }, word, a.D,
                                    lane);
   };
 
   const int64_t step = 32 * W, end = w.s1 * step;
   for (int64_t win = w.s0 * step + 32 * wave; win < end && win < a.Lk; win += 64 * step) {
     const uint32_t words = key_words(mp, win, step, end, a.Lk);
-    uint64_t live = __ballot(words != 0);
-    int at = live ? __builtin_ctzll(live) : 0, slot = 0;
-    uint32_t word[1] = {static_cast<uint32_t>(__builtin_amdgcn_readlane(words, at))};
-    if (live) {
-      load_keys(win + at * step, word[0], kf);
-      load_values(win + at * step, word[0], 0);
-    }
-    while (live) {
+    uint64_t live = __ballot(words != 0);   // the blocks of the window not sent for yet
+    // Sends for the next block that holds an attended key; its mask bits, or 0 when there is none
+    // (the loads then all lie outside and fetch nothing: as many are under way either way, so
+    // that a wait for the block before can leave them alone).
+    const auto send = [&](Frag<T> (&f)[DP / 16], T* __restrict__ to) {
+      const int at = live != 0 ? __builtin_ctzll(live) : 0;
+      const uint32_t word = live != 0 ? __builtin_amdgcn_readlane(words, at) : 0u;
       live &= live - 1;
-      at = live ? __builtin_ctzll(live) : 0;
-      const uint32_t word_next = __builtin_amdgcn_readlane(words, at);
-      if (live) {
-        load_keys(win + at * step, word_next, kn);
-        load_values(win + at * step, word_next, slot ^ 1);
-      }
+      load_keys(win + at * step, word, f);
+      load_values(win + at * step, word, to);
+      return word;
+    };
+    constexpr int N = AHEAD + 1;
+    uint32_t word[N];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) word[j] = send(kf[j], lds + j * 32 * DP);
+    if (win == w.s0 * step + 32 * wave) arrived(qf);
+    // One block: its values in `cur` while a later block's are sent to `to` (two places, and the
+    // compiler is told so: see attn_rows_kernel).
+    const auto turn = [&](Frag<T> (&k)[DP / 16], uint32_t mine, Frag<T> (&kn)[DP / 16], uint32_t& sent,
+                          const T* __restrict__ cur, T* __restrict__ to) {
+      sent = send(kn, to);
       f32x16 s[1] = {zero_acc()};   // (registers for standing zeros are not to spare here)
 #pragma unroll
-      for (int i = 0; i < DP / 16; ++i) s[0] = mma(kf[i], qf[i], s[0]);
+      for (int i = 0; i < DP / 16; ++i) s[0] = mma(k[i], qf[i], s[0]);
+      const uint32_t m1[1] = {mine};
       typename POperand<T>::type pf[1];
-      softmax_step<T>(s, word, a.c, run, o, pf);
-      // this block's values are there when only the next block's loads are under way
-      if constexpr (VEC) {
-        if (live) wait_loads<KL + VL>();
-        else wait_loads<0>();
+      softmax_step<T>(s, m1, a.c, run, o, pf);
+      if constexpr (VEC) wait_loads<AHEAD * (KL + VL)>();   // this block's values are there
+#pragma unroll
+      for (int i = 0; i < DT; ++i) o[i] = mma_rows<DP>(cur, 0, 32 * i, pf[0], o[i]);
+    };
+    bool more = true;
+    while (more) {
+      // one turn for each place, so that registers under way are named and never moved
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        if (word[j] == 0) {
+          more = false;
+          break;
+        }
+        turn(kf[j], word[j], kf[(j + AHEAD) % N], word[(j + AHEAD) % N], lds + j * 32 * DP, lds + (j + AHEAD) % N * 32 * DP);
       }
-#pragma unroll
-      for (int i = 0; i < DT; ++i) o[i] = mma_rows<DP>(lds + slot * 32 * DP, 0, 32 * i, pf[0], o[i]);
-#pragma unroll
-      for (int i = 0; i < DP / 16; ++i) kf[i] = kn[i];
-      word[0] = word_next;
-      slot ^= 1;
     }
+    wait_loads<0>();   // what was sent for last must not land on what the LDS is used for next
   }
   join_waves<T, DP, W, 1>(a, w, 32, run.m, sum_halves(run.l), o, smem);
 }
 
 // Waves of a SIMD that the rows form leaves registers for (accumulators then stay in the ordinary
 // registers: with more of them than needed the compiler moves them to the others and back).
-constexpr int waves_per_simd(int row_bytes) { return row_bytes <= 64 ? 4 : row_bytes <= 128 ? 3 : row_bytes <= 256 ? 2 : 1; }
+constexpr int waves_per_simd(int row_bytes) { return row_bytes <= 256 ? 2 : 1; }
 
 // Rows of 128 in four waves, which share a ring of STAGES key tiles of 64 in the LDS: while one
 // is worked on, the next STAGES - 1 are on their way.
 template <typename T, int DP, int STAGES, bool VEC>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(waves_per_simd(sizeof(T) * DP)))) void attn_rows_kernel(Args a) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(waves_per_simd(sizeof(T) * DP), waves_per_simd(sizeof(T) * DP)))) void attn_rows_kernel(Args a) {
   constexpr int KT = 64, DT = DP / 32, BUF = 2 * KT * DP, LOADS = 2 * tile_loads<T, DP, KT, 256>, AHEAD = STAGES - 1;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   T* const lds = reinterpret_cast<T*>(smem);              // [STAGES][keys, values][KT][DP]
@@ -291,46 +313,67 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(waves_per_s
 
   KeyTiles tiles(mp, a.Lk, w.s0, w.s1);
   // sends for the next tile that holds an attended key; its mask bits, or 0 when there is none
-  const auto send = [&](int slot) {
+  const auto send = [&](T* __restrict__ to) {
     int64_t k0;
     const uint64_t word = tiles.next(k0);
     if (word != 0) {
-      fetch_tile<T, DP, KT, 256, VEC>(lds + slot * BUF, kp + k0 * a.ks[1], [&](int r) { return r * a.ks[1]; }, word, a.D, tid);
-      fetch_tile<T, DP, KT, 256, VEC>(lds + slot * BUF + KT * DP, vp + k0 * a.vs[1], [&](int r) { return r * a.vs[1]; }, word,
+      fetch_tile<T, DP, KT, 256, VEC>(to, kp + k0 * a.ks[1], [&](int r) { return r * a.ks[1]; }, word, a.D, tid);
+      fetch_tile<T, DP, KT, 256, VEC>(to + KT * DP, vp + k0 * a.vs[1], [&](int r) { return r * a.vs[1]; }, word,
                                       a.D, tid);
     }
     return word;
   };
   uint64_t word[AHEAD + 1];
 #pragma unroll
-  for (int j = 0; j < AHEAD; ++j) word[j] = send(j);
-  int slot = 0;
-  while (word[0] != 0) {
-    // this wave's share of the tile is there when only the later tiles' loads are under way
-    if constexpr (AHEAD == 2) {
-      if (word[1] != 0) wait_loads<LOADS>();
-      else wait_loads<0>();
-    } else {
-      wait_loads<0>();
-    }
-    lds_barrier();              // the other waves' shares too; and the tile before is no longer read
-    word[AHEAD] = send(slot == 0 ? STAGES - 1 : slot - 1);
-    const T* ks = lds + slot * BUF;
-    const T* vs = ks + KT * DP;
+  for (int j = 0; j < AHEAD; ++j) word[j] = send(lds + j * BUF);
+  arrived(qf);
+  // One tile: `cur` is worked on while a later one is sent to `to`.  The two are different
+  // places, and the compiler is told so (restrict): it would otherwise wait for everything that
+  // is on its way to the LDS before it reads from it.
+  const auto turn = [&](const T* __restrict__ cur, T* __restrict__ to) {
+    word[AHEAD] = send(to);
+    const T* ks = cur;
+    const T* vs = cur + KT * DP;
     f32x16 s[2];
+    Frag<T> kf[2][DP / 16];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      s[n] = zeros;
+    for (int i = 0; i < DP / 16; ++i)
 #pragma unroll
-      for (int i = 0; i < DP / 16; ++i) s[n] = mma(row_frag<DP>(ks, 32 * n, i), qf[i], s[n]);
-    }
+      for (int n = 0; n < 2; ++n) kf[n][i] = row_frag<DP>(ks, 32 * n, i);
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) s[n] = mma(kf[n][i], qf[i], i == 0 ? zeros : s[n]);
     const uint32_t both[2] = {static_cast<uint32_t>(word[0]), static_cast<uint32_t>(word[0] >> 32)};
     typename POperand<T>::type pf[2];
     softmax_step<T>(s, both, a.c, run, o, pf);
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < 2; ++n) {
+        Frag<T> vf[DT][2];
 #pragma unroll
-      for (int i = 0; i < DT; ++i) o[i] = mma_rows<DP>(vs, 32 * n, 32 * i, pf[n], o[i]);
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) vf[i][h] = col_frag<DP>(vs, 32 * n, 32 * i, h);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < DT; ++i) o[i] = mma(vf[i][h], pf[n].f[h], o[i]);
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < DT; ++i) o[i] = mma_rows<DP>(vs, 32 * n, 32 * i, pf[n], o[i]);
+    }
+  };
+  int slot = 0;
+  while (word[0] != 0) {
+    // this wave's share of the tile is there when only the later tiles' loads are under way
+    if (AHEAD == 2 && word[1] != 0) wait_loads<LOADS>();
+    else wait_loads<0>();
+    lds_barrier();              // the other waves' shares too; and the tile before is no longer read
+    turn(lds + slot * BUF, lds + (slot == 0 ? STAGES - 1 : slot - 1) * BUF);
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) word[j] = word[j + 1];
     slot = slot == STAGES - 1 ? 0 : slot + 1;
@@ -399,7 +442,7 @@ Plan make_plan(const dcn_attn_desc* d) {
   p.rows = p.wide ? 128 : 32;
   const int64_t step = p.wide ? 64 : 32 * p.waves;
   p.y = tile_over(nbh * ((R + p.rows - 1) / p.rows), (d->key_len + step - 1) / step,
-                  p.wide ? 2 * kCUs : 2 * kCUs * 8 / p.waves, 2);
+                  p.wide ? 2 * kCUs : kCUs, p.wide ? 2 : 4);
   return p;
 }
 

@@ -385,8 +385,9 @@ Layout make_layout(const dcn_attn_desc* d) {
   y.dp = padded_head(d->head_dim);
   const int64_t nbh = d->batch * d->key_heads, R = d->query_len * (d->query_heads / d->key_heads);
   const int64_t rows = (R + kT - 1) / kT, keys = (d->key_len + kT - 1) / kT;
-  y.q = tile_over(nbh * ((R + 127) / 128), keys, 2 * kCUs, 2);
-  y.kv = tile_over(nbh * ((d->key_len + 127) / 128), rows, 2 * kCUs, 2);
+  const int least = d->dtype == DCN_BF16 ? 2 : 1;
+  y.q = tile_over(nbh * ((R + 127) / 128), keys, 2 * kCUs, least);
+  y.kv = tile_over(nbh * ((d->key_len + 127) / 128), rows, 2 * kCUs, least);
   y.part_at = up256(static_cast<size_t>(nbh) * R * 8);
   const size_t tile = static_cast<size_t>(128) * y.dp * 4;
   y.part_kv_at = y.part_at + static_cast<size_t>(y.q.tiles - y.q.full) * y.q.splits * tile;
