@@ -143,36 +143,42 @@ __device__ __forceinline__ void dq_part(const Args& a, int tile, T* lds) {
 
   KeyTiles tiles(a.mask == nullptr ? nullptr : a.mask + w.b * a.ms, a.Lk, w.s0, w.s1);
   // rows of padded keys are not read and taken as zeros: their weight is 0, and 0 times a NaN is none
-  const auto send = [&](int slot) {
+  const auto send = [&](T* __restrict__ to) {
     int64_t k0;
     const uint64_t word = tiles.next(k0);
     if (word != 0) {
-      fetch_tile<T, DP, kT, 256, VEC>(lds + slot * BUF, kp + k0 * a.ks[1], [&](int r) { return r * a.ks[1]; }, word, a.D, tid);
-      fetch_tile<T, DP, kT, 256, VEC>(lds + slot * BUF + kT * DP, vp + k0 * a.vs[1], [&](int r) { return r * a.vs[1]; }, word,
+      fetch_tile<T, DP, kT, 256, VEC>(to, kp + k0 * a.ks[1], [&](int r) { return r * a.ks[1]; }, word, a.D, tid);
+      fetch_tile<T, DP, kT, 256, VEC>(to + kT * DP, vp + k0 * a.vs[1], [&](int r) { return r * a.vs[1]; }, word,
                                       a.D, tid);
     }
     return word;
   };
   uint64_t word[AHEAD + 1];
 #pragma unroll
-  for (int j = 0; j < AHEAD; ++j) word[j] = send(j);
-  int slot = 0;
-  while (word[0] != 0) {
-    if (AHEAD == 2 && word[1] != 0) wait_loads<LOADS>();
-    else wait_loads<0>();
-    lds_barrier();
-    word[AHEAD] = send(slot == 0 ? STAGES - 1 : slot - 1);
-    const T* ks = lds + slot * BUF;
-    const T* vs = ks + kT * DP;
+  for (int j = 0; j < AHEAD; ++j) word[j] = send(lds + j * BUF);
+  arrived(qf);
+  arrived(gf);
+  // one tile: `cur` is worked on while a later one is sent to `to`, another place (restrict: no
+  // wait for what is on its way before `cur` is read)
+  const auto turn = [&](const T* __restrict__ cur, T* __restrict__ to) {
+    word[AHEAD] = send(to);
+    const T* ks = cur;
+    const T* vs = cur + kT * DP;
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const uint32_t keep = static_cast<uint32_t>(word[0] >> (32 * n));
       if (keep == 0 || !busy) continue;
       f32x16 s = zeros, p = zeros;
+      Frag<T> kf[DP / 16], vf[DP / 16];
 #pragma unroll
       for (int i = 0; i < DP / 16; ++i) {
-        s = mma(row_frag<DP>(ks, 32 * n, i), qf[i], s);
-        p = mma(row_frag<DP>(vs, 32 * n, i), gf[i], p);
+        kf[i] = row_frag<DP>(ks, 32 * n, i);
+        vf[i] = row_frag<DP>(vs, 32 * n, i);
+      }
+#pragma unroll
+      for (int i = 0; i < DP / 16; ++i) {
+        s = mma(kf[i], qf[i], s);
+        p = mma(vf[i], gf[i], p);
       }
       if (keep != 0xffffffffu) mask_scores(s, keep);
       float ds[16];
@@ -183,6 +189,13 @@ __device__ __forceinline__ void dq_part(const Args& a, int tile, T* lds) {
 #pragma unroll
       for (int i = 0; i < DT; ++i) o[i] = mma_rows<DP>(ks, 32 * n, 32 * i, pf, o[i]);
     }
+  };
+  int slot = 0;
+  while (word[0] != 0) {
+    if (AHEAD == 2 && word[1] != 0) wait_loads<LOADS>();
+    else wait_loads<0>();
+    lds_barrier();
+    turn(lds + slot * BUF, lds + (slot == 0 ? STAGES - 1 : slot - 1) * BUF);
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) word[j] = word[j + 1];
     slot = slot == STAGES - 1 ? 0 : slot + 1;
@@ -200,9 +213,10 @@ __device__ __forceinline__ void dq_part(const Args& a, int tile, T* lds) {
 
 template <typename T, int DP, int STAGES, bool VEC>
 __device__ __forceinline__ void dkv_part(const Args& a, int tile, T* lds) {
-  constexpr int DT = DP / 32, BUF = 2 * kT * DP, AHEAD = STAGES - 1, LOADS = VEC ? 2 * tile_loads<T, DP, kT, 256> + 1 : 1;
+  // a place in the ring: query rows, gradient rows, and lse and delta of each
+  constexpr int DT = DP / 32, BUF = 2 * kT * DP + kRowVals * 4 / static_cast<int>(sizeof(T)), AHEAD = STAGES - 1;
+  constexpr int LOADS = VEC ? 2 * tile_loads<T, DP, kT, 256> + 1 : 1;
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  float* const vals = reinterpret_cast<float*>(lds + STAGES * BUF);   // [STAGES][lse, delta][kT]
   const Work w = work_of(a, a.ykv, tile, 128, (a.R + kT - 1) / kT);
   const int key = w.row0 + wave * 32 + (lane & 31);
   bool live = key < a.Lk;
@@ -225,7 +239,7 @@ __device__ __forceinline__ void dkv_part(const Args& a, int tile, T* lds) {
   const T* qb = static_cast<const T*>(a.q) + w.b * a.qs[0] + w.hk * a.g * a.qs[2];
   const T* gb = static_cast<const T*>(a.dout) + (static_cast<int64_t>(w.b) * a.Lq * a.Hq + w.hk * a.g) * a.D;
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv * a.R, row_base = static_cast<int64_t>(w.b * a.Hkv + w.hk) * a.R;
-  const auto send = [&](int t, int slot) {
+  const auto send = [&](int t, T* __restrict__ to) {
     const int r0 = t * kT, n = min(kT, a.R - r0);
     const uint64_t in = n == 64 ? ~uint64_t{0} : (uint64_t{1} << n) - 1;
     // rows run over the heads that share the key head, then over positions
@@ -239,12 +253,12 @@ __device__ __forceinline__ void dkv_part(const Args& a, int tile, T* lds) {
         h = static_cast<int>(x) - pos * a.g;
       }
     };
-    fetch_tile<T, DP, kT, 256, VEC>(lds + slot * BUF, qb + pos0 * a.qs[1], [&](int r) {
+    fetch_tile<T, DP, kT, 256, VEC>(to, qb + pos0 * a.qs[1], [&](int r) {
       int pos, h;
       split(r, pos, h);
       return pos * a.qs[1] + h * a.qs[2];
     }, in, a.D, tid);
-    fetch_tile<T, DP, kT, 256, VEC>(lds + slot * BUF + kT * DP, gb + static_cast<int64_t>(pos0) * a.Hq * a.D, [&](int r) {
+    fetch_tile<T, DP, kT, 256, VEC>(to + kT * DP, gb + static_cast<int64_t>(pos0) * a.Hq * a.D, [&](int r) {
       int pos, h;
       split(r, pos, h);
       return (static_cast<int64_t>(pos) * a.Hq + h) * a.D;
@@ -253,54 +267,64 @@ __device__ __forceinline__ void dkv_part(const Args& a, int tile, T* lds) {
     // under way); rows beyond the last give zeros, and their zero query and gradient rows add nothing
     const int which = wave & 1;
     const __amdgpu_buffer_rsrc_t rs = rsrc_of(a.delta + which * rows + row_base + r0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(vals + slot * kRowVals + which * kT), 4,
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(reinterpret_cast<float*>(to + 2 * kT * DP) + which * kT), 4,
                                              lane < n ? lane * 4 : kOutside, 0, 0, 0);
   };
 #pragma unroll
   for (int j = 0; j < AHEAD; ++j)
-    if (w.s0 + j < s1) send(w.s0 + j, j);
+    if (w.s0 + j < s1) send(w.s0 + j, lds + j * BUF);
+  arrived(kf);
+  arrived(vf);
+  const auto turn = [&](int t, const T* __restrict__ cur, T* __restrict__ to) {
+    if (t + AHEAD < s1) send(t + AHEAD, to);
+    if (!any) return;
+    const T* qs = cur;
+    const T* gs = cur + kT * DP;
+    const float* ls = reinterpret_cast<const float*>(cur + 2 * kT * DP);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int r0 = 32 * n;
+      f32x16 s = zeros, dp = zeros;
+      Frag<T> qf[DP / 16], gf[DP / 16];
+#pragma unroll
+      for (int i = 0; i < DP / 16; ++i) {
+        qf[i] = row_frag<DP>(qs, r0, i);
+        gf[i] = row_frag<DP>(gs, r0, i);
+      }
+#pragma unroll
+      for (int i = 0; i < DP / 16; ++i) {
+        s = mma(qf[i], kf[i], s);
+        dp = mma(gf[i], vf[i], dp);
+      }
+      float p[16], ds[16];
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4) {
+        const float4 lse = *reinterpret_cast<const float4*>(ls + r0 + acc_row(4 * r4, half));
+        const float4 del = *reinterpret_cast<const float4*>(ls + kT + r0 + acc_row(4 * r4, half));
+        const float le[4] = {lse.x, lse.y, lse.z, lse.w}, de[4] = {del.x, del.y, del.z, del.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = 4 * r4 + j;
+          p[r] = exp2_fast(fmaf(s[r], a.c, -le[j]));
+          ds[r] = p[r] * (dp[r] - de[j]);
+        }
+      }
+      typename POperand<T>::type pf, df;
+      to_operand(p, pf);
+      to_operand(ds, df);
+#pragma unroll
+      for (int i = 0; i < DT; ++i) {
+        ov[i] = mma_rows<DP>(gs, r0, 32 * i, pf, ov[i]);
+        ok[i] = mma_rows<DP>(qs, r0, 32 * i, df, ok[i]);
+      }
+    }
+  };
   int slot = 0;
   for (int t = w.s0; t < s1; ++t) {
     if (AHEAD == 2 && t + 1 < s1) wait_loads<LOADS>();
     else wait_loads<0>();
     lds_barrier();
-    if (t + AHEAD < s1) send(t + AHEAD, slot == 0 ? STAGES - 1 : slot - 1);
-    const T* qs = lds + slot * BUF;
-    const T* gs = qs + kT * DP;
-    const float* ls = vals + slot * kRowVals;
-    if (any) {
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int r0 = 32 * n;
-        f32x16 s = zeros, dp = zeros;
-#pragma unroll
-        for (int i = 0; i < DP / 16; ++i) {
-          s = mma(row_frag<DP>(qs, r0, i), kf[i], s);
-          dp = mma(row_frag<DP>(gs, r0, i), vf[i], dp);
-        }
-        float p[16], ds[16];
-#pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4) {
-          const float4 lse = *reinterpret_cast<const float4*>(ls + r0 + acc_row(4 * r4, half));
-          const float4 del = *reinterpret_cast<const float4*>(ls + kT + r0 + acc_row(4 * r4, half));
-          const float le[4] = {lse.x, lse.y, lse.z, lse.w}, de[4] = {del.x, del.y, del.z, del.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int r = 4 * r4 + j;
-            p[r] = exp2_fast(fmaf(s[r], a.c, -le[j]));
-            ds[r] = p[r] * (dp[r] - de[j]);
-          }
-        }
-        typename POperand<T>::type pf, df;
-        to_operand(p, pf);
-        to_operand(ds, df);
-#pragma unroll
-        for (int i = 0; i < DT; ++i) {
-          ov[i] = mma_rows<DP>(gs, r0, 32 * i, pf, ov[i]);
-          ok[i] = mma_rows<DP>(qs, r0, 32 * i, df, ok[i]);
-        }
-      }
-    }
+    turn(t, lds + slot * BUF, lds + (slot == 0 ? STAGES - 1 : slot - 1) * BUF);
     slot = slot == STAGES - 1 ? 0 : slot + 1;
   }
   // a lane whose key is padding has summed the weights of a zero key row: its gradients are 0
@@ -327,9 +351,12 @@ __device__ __forceinline__ void dkv_part(const Args& a, int tile, T* lds) {
   rows_out(ov, os, [&](int rr, int d, float4 v) { store(rr, d, v, 1); });
 }
 
+// Waves of a SIMD (workgroups of a CU) that the registers allow.
+constexpr int waves_per_simd(int row_bytes) { return row_bytes <= 64 ? 3 : row_bytes <= 128 ? 2 : 1; }
+
 // Workgroups 0 .. kv - 1: dK and dV; the others: dQ.
 template <typename T, int DP, int STAGES, bool VEC>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DP * sizeof(T) <= 128 ? 2 : 1)))
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(waves_per_simd(DP * sizeof(T)), waves_per_simd(DP * sizeof(T)))))
 void attn_grad_kernel(Args a, int kv) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   T* lds = reinterpret_cast<T*>(smem);
@@ -385,9 +412,18 @@ Layout make_layout(const dcn_attn_desc* d) {
   y.dp = padded_head(d->head_dim);
   const int64_t nbh = d->batch * d->key_heads, R = d->query_len * (d->query_heads / d->key_heads);
   const int64_t rows = (R + kT - 1) / kT, keys = (d->key_len + kT - 1) / kT;
-  const int least = d->dtype == DCN_BF16 ? 2 : 1;
-  y.q = tile_over(nbh * ((R + 127) / 128), keys, 2 * kCUs, least);
-  y.kv = tile_over(nbh * ((d->key_len + 127) / 128), rows, 2 * kCUs, least);
+  // One launch holds both kinds of workgroups.  dK and dV are split to fill the chip by
+  // themselves; dQ, where its tiles alone do not fill it, into what the last round has left.  A
+  // step of fp32 is 16 times as many matrix cycles as one of bf16: there a single step is a part.
+  const int es = d->dtype == DCN_BF16 ? 2 : 4, least = es == 2 ? 2 : 1;
+  const int64_t slots = static_cast<int64_t>(kCUs) * waves_per_simd(y.dp * es), nq = nbh * ((R + 127) / 128);
+  y.kv = tile_over(nbh * ((d->key_len + 127) / 128), rows, slots, least);
+  int64_t left = slots;
+  if (nq < slots) {
+    left = slots - workgroups(y.kv) % slots;
+    if (left < nq) left += slots;
+  }
+  y.q = tile_over(nq, keys, left, least);
   y.part_at = up256(static_cast<size_t>(nbh) * R * 8);
   const size_t tile = static_cast<size_t>(128) * y.dp * 4;
   y.part_kv_at = y.part_at + static_cast<size_t>(y.q.tiles - y.q.full) * y.q.splits * tile;
