@@ -186,8 +186,28 @@ __device__ __forceinline__ void dq_part(const Args& a, int tile, T* lds) {
       for (int r = 0; r < 16; ++r) ds[r] = exp2_fast(fmaf(s[r], a.c, -lse2)) * (p[r] - delta);
       typename POperand<T>::type pf;
       to_operand(ds, pf);
+      if constexpr (sizeof(T) == 2) {
+        typename POperand<T>::type rest;
 #pragma unroll
-      for (int i = 0; i < DT; ++i) o[i] = mma_rows<DP>(ks, 32 * n, 32 * i, pf, o[i]);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t w2 = pf.f[h].w[j];
+            rest.f[h].w[j] = pack_bf16(ds[8 * h + 2 * j] - __uint_as_float(w2 << 16),
+                                       ds[8 * h + 2 * j + 1] - __uint_as_float(w2 & 0xffff0000u));
+          }
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const Frag<T> c = col_frag<DP>(ks, 32 * n, 32 * i, h);
+            o[i] = mma(c, pf.f[h], o[i]);
+            o[i] = mma(c, rest.f[h], o[i]);
+          }
+      } else {
+#pragma unroll
+        for (int i = 0; i < DT; ++i) o[i] = mma_rows<DP>(ks, 32 * n, 32 * i, pf, o[i]);
+      }
     }
   };
   int slot = 0;
@@ -352,11 +372,13 @@ __device__ __forceinline__ void dkv_part(const Args& a, int tile, T* lds) {
 }
 
 // Waves of a SIMD (workgroups of a CU) that the registers allow.
-constexpr int waves_per_simd(int row_bytes) { return row_bytes <= 64 ? 3 : row_bytes <= 128 ? 2 : 1; }
+// (fp32 rows of 64: 107 us with one, 74 with two and a few registers spilled, at B 4, Lq 55, Lk 1736, 8 heads on
+// 2; bf16 rows of 128: 225 with one, 585 with two, at B 2, Lq = Lk = 2100, 8 heads.)
+constexpr int waves_per_simd(int es, int dp) { return es * dp <= 64 ? 3 : es * dp <= 128 || (es == 4 && dp == 64) ? 2 : 1; }
 
 // Workgroups 0 .. kv - 1: dK and dV; the others: dQ.
 template <typename T, int DP, int STAGES, bool VEC>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(waves_per_simd(DP * sizeof(T)), waves_per_simd(DP * sizeof(T)))))
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(waves_per_simd(sizeof(T), DP), waves_per_simd(sizeof(T), DP))))
 void attn_grad_kernel(Args a, int kv) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   T* lds = reinterpret_cast<T*>(smem);
@@ -416,7 +438,7 @@ Layout make_layout(const dcn_attn_desc* d) {
   // themselves; dQ, where its tiles alone do not fill it, into what the last round has left.  A
   // step of fp32 is 16 times as many matrix cycles as one of bf16: there a single step is a part.
   const int es = d->dtype == DCN_BF16 ? 2 : 4, least = es == 2 ? 2 : 1;
-  const int64_t slots = static_cast<int64_t>(kCUs) * waves_per_simd(y.dp * es), nq = nbh * ((R + 127) / 128);
+  const int64_t slots = static_cast<int64_t>(kCUs) * waves_per_simd(es, y.dp), nq = nbh * ((R + 127) / 128);
   y.kv = tile_over(nbh * ((d->key_len + 127) / 128), rows, slots, least);
   int64_t left = slots;
   if (nq < slots) {
