@@ -31,7 +31,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstdlib>
 
 #include "dcn.h"
 #include "dcn_attention.h"
@@ -235,9 +234,11 @@ __global__ __launch_bounds__(64 * W) void attn_few_rows_kernel(Args a) {
                                    lane);
   };
 
-  const int64_t step = 32 * W, end = w.s1 * step;
-  for (int64_t win = w.s0 * step + 32 * wave; win < end && win < a.Lk; win += 64 * step) {
-    const uint32_t words = key_words(mp, win, step, end, a.Lk);
+  // the waves of all workgroups that share the tile take the blocks in turn: what a mask leaves
+  // out is then missing from each alike
+  const int64_t step = static_cast<int64_t>(32 * W) * (w.tail >= 0 ? a.y.splits : 1), first = 32 * (w.split * W + wave);
+  for (int64_t win = first; win < a.Lk; win += 64 * step) {
+    const uint32_t words = key_words(mp, win, step, a.Lk, a.Lk);
     uint64_t live = __ballot(words != 0);   // the blocks of the window not sent for yet
     // Sends for the next block that holds an attended key; its mask bits, or 0 when there is none
     // (the loads then all lie outside and fetch nothing: as many are under way either way, so
@@ -254,7 +255,7 @@ __global__ __launch_bounds__(64 * W) void attn_few_rows_kernel(Args a) {
     uint32_t word[N];
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) word[j] = send(kf[j], lds + j * 32 * DP);
-    if (win == w.s0 * step + 32 * wave) arrived(qf);
+    if (win == first) arrived(qf);
     // One block: its values in `cur` while a later block's are sent to `to` (two places, and the
     // compiler is told so: see attn_rows_kernel).
     const auto turn = [&](Frag<T> (&k)[DP / 16], uint32_t mine, Frag<T> (&kn)[DP / 16], uint32_t& sent,
@@ -428,21 +429,24 @@ struct Plan {
   Tiling y;
 };
 
+// The rows form where its tiles of 128 rows are filled and the few-rows form, of which a CU holds
+// one workgroup, would need nearly more than one round of the chip.  Measured (bf16, few / rows):
+// 160 tiles of 32 rows (2 x 300 rows of 8 heads of 32, 4200 keys) 20.1 / 23.3 us, 198 (fp32, 3 x
+// 333 of 6 of 40, 1051 keys) 25.2 / 31.2, 232 (900 of 8 of 32, 16800 keys) 54.3 / 46.1, 320 (4 x
+// 300 of 8 of 32, 4200 keys) 37.1 / 25.5.
+// Splits: the few-rows form down to four steps (with fewer, the launch that joins them costs more
+// than they save: one row, 8 heads of 64, 1050 keys 14.4 us in two parts, 10.6 unsplit).
 Plan make_plan(const dcn_attn_desc* d) {
   Plan p{};
   const int es = d->dtype == DCN_BF16 ? 2 : 4;
   p.dp = padded_head(d->head_dim);
   const int64_t nbh = d->batch * d->key_heads, R = d->query_len * (d->query_heads / d->key_heads);
-  p.wide = R > 96 && nbh * ((R + 31) / 32) > 2 * kCUs;
-  if (const char* f = std::getenv("DCN_ATTN_FORM")) {
-    if (f[0] == 'r') p.wide = true;
-    if (f[0] == 'f') p.wide = false;
-  }
+  p.wide = R > 96 && nbh * ((R + 31) / 32) * 8 > 7 * kCUs;
   p.waves = p.wide ? 4 : waves_of(es, p.dp);
   p.rows = p.wide ? 128 : 32;
   const int64_t step = p.wide ? 64 : 32 * p.waves;
-  p.y = tile_over(nbh * ((R + p.rows - 1) / p.rows), (d->key_len + step - 1) / step,
-                  p.wide ? 2 * kCUs : kCUs, p.wide ? 2 : 4);
+  p.y = tile_over(nbh * ((R + p.rows - 1) / p.rows), (d->key_len + step - 1) / step, p.wide ? 2 * kCUs : kCUs,
+                  p.wide ? 2 : 4);
   return p;
 }
 
