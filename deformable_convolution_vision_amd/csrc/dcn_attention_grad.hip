@@ -22,8 +22,16 @@
 // of the second (see dcn_attention.h): dQ keeps a row per lane (S^T), dK/dV a key per lane
 // (S).  Rows with no key have lse = -inf; it enters as +inf, which makes every weight 0.
 //
-// Arithmetic: fp32 sums; for bf16, P and dS are rounded to bf16 as operands of the second
-// products, and the gradients once.
+// Arithmetic: fp32 sums; for bf16, P is rounded to bf16 as an operand of dV, dS enters dQ and dK as
+// two bf16 operands (its rounded value and what that leaves: 16 bits of it), and the gradients
+// are rounded once.  delta already carries the rounding of out; with a rounded dS on top of it dQ
+// and dK were 1.4 to 1.6 times one rounding away from the exact gradients, with both parts 1.1.
+// That costs a product more: 4200 queries over 1050 keys, 8 heads of 64, batch 2, 99 us without,
+// 107 with both parts of dQ, 112 of dK too.
+//
+// What bounds it: the matrix products (14 Lq Lk D of the formulas' 10, and 4 for the second parts)
+// and the vector instructions for the weights hardly overlap within a SIMD; at that size they are
+// 33 and 31 us of the 112, and the parts of split tiles are 28 MB written and read again.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -113,6 +121,20 @@ __device__ __forceinline__ T* dkv_row(const Args& a, const Work& w, int key, int
 constexpr int kT = 64;           // rows of a tile in the LDS
 constexpr int kRowVals = 2 * kT; // lse and delta of a row tile
 
+// What an operand of score gradients leaves of them by its rounding to bf16, as a second operand.
+__device__ __forceinline__ POperand<uint16_t>::type rest_of(const float (&ds)[16], const POperand<uint16_t>::type& pf) {
+  POperand<uint16_t>::type rest;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t w2 = pf.f[h].w[j];
+      rest.f[h].w[j] = pack_bf16(ds[8 * h + 2 * j] - __uint_as_float(w2 << 16),
+                                 ds[8 * h + 2 * j + 1] - __uint_as_float(w2 & 0xffff0000u));
+    }
+  return rest;
+}
+
 template <typename T, int DP, int STAGES, bool VEC>
 __device__ __forceinline__ void dq_part(const Args& a, int tile, T* lds) {
   constexpr int DT = DP / 32, BUF = 2 * kT * DP, AHEAD = STAGES - 1, LOADS = VEC ? 2 * tile_loads<T, DP, kT, 256> : 0;
@@ -187,15 +209,7 @@ __device__ __forceinline__ void dq_part(const Args& a, int tile, T* lds) {
       typename POperand<T>::type pf;
       to_operand(ds, pf);
       if constexpr (sizeof(T) == 2) {
-        typename POperand<T>::type rest;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t w2 = pf.f[h].w[j];
-            rest.f[h].w[j] = pack_bf16(ds[8 * h + 2 * j] - __uint_as_float(w2 << 16),
-                                       ds[8 * h + 2 * j + 1] - __uint_as_float(w2 & 0xffff0000u));
-          }
+        const auto rest = rest_of(ds, pf);
 #pragma unroll
         for (int i = 0; i < DT; ++i)
 #pragma unroll
@@ -332,10 +346,24 @@ __device__ __forceinline__ void dkv_part(const Args& a, int tile, T* lds) {
       typename POperand<T>::type pf, df;
       to_operand(p, pf);
       to_operand(ds, df);
+      if constexpr (sizeof(T) == 2) {
+        const auto rest = rest_of(ds, df);
 #pragma unroll
-      for (int i = 0; i < DT; ++i) {
-        ov[i] = mma_rows<DP>(gs, r0, 32 * i, pf, ov[i]);
-        ok[i] = mma_rows<DP>(qs, r0, 32 * i, df, ok[i]);
+        for (int i = 0; i < DT; ++i) {
+          ov[i] = mma_rows<DP>(gs, r0, 32 * i, pf, ov[i]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const Frag<T> c = col_frag<DP>(qs, r0, 32 * i, h);
+            ok[i] = mma(c, df.f[h], ok[i]);
+            ok[i] = mma(c, rest.f[h], ok[i]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < DT; ++i) {
+          ov[i] = mma_rows<DP>(gs, r0, 32 * i, pf, ov[i]);
+          ok[i] = mma_rows<DP>(qs, r0, 32 * i, df, ok[i]);
+        }
       }
     }
   };
