@@ -341,7 +341,8 @@ int dcn_cross_attention(const dcn_attn_desc* desc, const void* q, const void* k,
  * every repetition.  Masked positions get zeros, and so do rows with no key.  Arithmetic: the
  * weights are formed again from the scores and lse in fp32; for bf16 the weights are rounded to
  * bf16 as an operand of the second product, the score gradients enter theirs as two bf16
- * operands (the rounded value and what it leaves); sums in fp32 in a fixed order (no atomics).  Workspace and errors as for dcn_cross_attention. */
+ * operands (the rounded value and what it leaves); sums in fp32 in a fixed order (no atomics).
+ * Workspace and errors as for dcn_cross_attention. */
 int dcn_cross_attention_backward_workspace_bytes(const dcn_attn_desc* desc, size_t* bytes);
 int dcn_cross_attention_backward(const dcn_attn_desc* desc, const void* q, const void* k, const void* v,
                                  const uint8_t* key_mask, const void* out, const float* lse,
