@@ -20,9 +20,9 @@
 // pass that first joins the chunks' parts and then writes.  Sums are joined in a fixed order;
 // there are no atomics.
 //
-// In the second way the variance is formed from sums of d and d^2, d = x - r with r the chunk's first value of
-// the channel, and chunks and channels are joined as (count, mean, sum of squares about the
-// mean): nothing large cancels where the mean is far from 0.
+// In the second way the variance is formed from sums of d and d^2, d = x - r with r the middle one of three
+// values of the channel in the chunk (a single one may lie far out), and chunks and channels are joined as
+// (count, mean, sum of squares about the mean): nothing large cancels where the mean is far from 0.
 //
 // Arithmetic: fp32 throughout, every output rounded to its type once.
 
@@ -215,6 +215,8 @@ __device__ __forceinline__ void join_rows(float (&s1)[V], float (&s2)[V], bool m
 // has been used).
 constexpr int kAhead = 4, kGradAhead = 2;
 
+__device__ __forceinline__ float middle(float a, float b, float c) { return __builtin_amdgcn_fmed3f(a, b, c); }
+
 template <typename T, int V>
 __global__ __launch_bounds__(kNT) void norm_stats_kernel(Args a) {
   extern __shared__ float2 lds[];            // [cb] mean and squares of a channel, then the row threads' sums
@@ -222,7 +224,7 @@ __global__ __launch_bounds__(kNT) void norm_stats_kernel(Args a) {
   float2* red = lds + a.sum.cb;
   const Share sh = share_of(a, a.sum);
   const int chunk = blockIdx.x;
-  const int64_t r0 = chunk * a.sum.rows, r1 = min(a.P, r0 + a.sum.rows);
+  const int64_t r0 = chunk * a.sum.rows, r1 = min(a.P, r0 + a.sum.rows), rm = (r0 + r1) / 2;
   const float n = static_cast<float>(r1 - r0);
   const int tc = threadIdx.x % a.sum.tc, tr = threadIdx.x / a.sum.tc, VR = sh.width / V;
   const T* base = static_cast<const T*>(a.x) + static_cast<int64_t>(sh.b) * a.P * a.C + sh.c0;
@@ -234,11 +236,14 @@ __global__ __launch_bounds__(kNT) void norm_stats_kernel(Args a) {
     for (int j = 0; j < V; ++j) s1[j] = s2[j] = 0.f;
     if (mine) {
       const T* p = base + (v0 + tc) * V;
-      const Vec<T, V> ref = load<T, V>(p + r0 * a.C);
+      const Vec<T, V> x0 = load<T, V>(p + r0 * a.C), xm = load<T, V>(p + rm * a.C), x1 = load<T, V>(p + (r1 - 1) * a.C);
       Vec<T, V> v[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k)
         if (r0 + tr + k * a.sum.tr < r1) v[k] = load<T, V>(p + (r0 + tr + k * a.sum.tr) * a.C);
+      float ref[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) ref[j] = middle(widen(x0.e[j]), widen(xm.e[j]), widen(x1.e[j]));
       for (int64_t r = r0 + tr; r < r1; r += kAhead * a.sum.tr) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
@@ -246,7 +251,7 @@ __global__ __launch_bounds__(kNT) void norm_stats_kernel(Args a) {
           if (row >= r1) break;
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            const float d = widen(v[k].e[j]) - widen(ref.e[j]);
+            const float d = widen(v[k].e[j]) - ref[j];
             s1[j] += d;
             s2[j] = fmaf(d, d, s2[j]);
           }
@@ -255,7 +260,8 @@ __global__ __launch_bounds__(kNT) void norm_stats_kernel(Args a) {
       }
     }
     join_rows<V>(s1, s2, mine, a, width, red, [&](int c, float2 s) {
-      const float ref = widen(base[r0 * a.C + v0 * V + c]), m = s.x / n;
+      const T* p = base + v0 * V + c;
+      const float ref = middle(widen(p[r0 * a.C]), widen(p[rm * a.C]), widen(p[(r1 - 1) * a.C])), m = s.x / n;
       chan[v0 * V + c] = make_float2(ref + m, not_below_0(s.y - s.x * m));
     });
   }
@@ -578,7 +584,7 @@ __global__ __launch_bounds__(kST) void norm_slice_kernel(Args a) {
     bias[j] = a.b == nullptr ? 0.f : widen(static_cast<const T*>(a.b)[c]);
   }
   const float inv = 1.f / (static_cast<float>(a.P) * a.Cg);
-  // sums about a value near the mean (of the first position's first channels), as in norm_stats_kernel
+  // sums about a value that is taken to be near the mean (of the first position's first channels)
   const Vec<T, V> first = load<T, V>(static_cast<const T*>(a.x) + static_cast<int64_t>(b) * a.P * a.C + g * a.Cg);
   float ref = 0.f;
 #pragma unroll
@@ -594,9 +600,23 @@ __global__ __launch_bounds__(kST) void norm_slice_kernel(Args a) {
         s += d;
         q = fmaf(d, d, q);
       }
-  const float2 t = block_sum(s, q, lds);
+  float2 t = block_sum(s, q, lds);
   const float shift = t.x * inv, m = ref + shift;
-  const float rstd = 1.f / sqrtf(not_below_0(t.y * inv - shift * shift) + a.eps);
+  float var = not_below_0(t.y * inv - shift * shift);
+  if (shift * shift > 16.f * var) {   // the value near the mean was not near it: its squares once more, about the mean
+    q = 0.f;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (mine && row + k * rows < P)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float d = widen(v[k].e[j]) - m;
+          q = fmaf(d, d, q);
+        }
+    t = block_sum(q, 0.f, lds);
+    var = t.x * inv;
+  }
+  const float rstd = 1.f / sqrtf(var + a.eps);
   if (threadIdx.x == 0) {
     if (a.mean != nullptr) a.mean[unit] = m;
     if (a.rstd != nullptr) a.rstd[unit] = rstd;

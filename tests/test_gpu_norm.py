@@ -77,6 +77,25 @@ def test_norm_and_gradients(name, dtype):
         assert all(s is None or torch.equal(s, t) for s, t in zip(grads, again)), "the same call gave other bits"
 
 
+@pytest.mark.parametrize("hw", [(25, 42), (70, 90)])   # in a workgroup's registers, and in two passes
+@pytest.mark.parametrize("where", ["first", "last", "first channel"])
+def test_a_position_far_out(hw, where):
+    """One position 1e4 standard deviations out, wherever a sum about a sample could take it as its
+    sample: squares are still summed about something near the mean, to ACC of the variance; the
+    mean's error, ACC of the mean of |x|, is small against the standard deviation."""
+    rng = np.random.default_rng(5)
+    x = rng.standard_normal((2, *hw, 32)).astype(np.float32)
+    if where == "first channel":
+        x[:, 0, 0, ::8] = 1e4
+    else:
+        x[(slice(None), 0, 0) if where == "first" else (slice(None), -1, -1)] = 1e4
+    out = dcn.group_norm_act(torch.from_numpy(x).cuda(), 4).double().cpu().numpy()
+    g = x.astype(np.float64).reshape(2, -1, 4, 8)
+    dev = g - g.mean((1, 3), keepdims=True)
+    want = (dev / np.sqrt((dev ** 2).mean((1, 3), keepdims=True) + 1e-5)).reshape(x.shape)
+    assert (np.abs(out - want) <= norm_oracle.ACC * (1 + np.abs(want))).all()
+
+
 @pytest.mark.parametrize("act", ["none", "silu", "gelu"])
 def test_gradients_against_differences(act):
     """<gradient, direction> against central differences of the definition in 64 bits."""
