@@ -464,7 +464,8 @@ inline Tiling tile_over(int64_t tiles, int64_t steps, int64_t slots, int64_t lea
 }
 inline int64_t workgroups(const Tiling& y) { return y.full + static_cast<int64_t>(y.tiles - y.full) * y.splits; }
 inline int padded_head(int64_t D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
-// Tiles of a ring in the LDS: three where two workgroups of a CU then have room, else two.
+// Tiles of a ring in the LDS: three where two workgroups of a CU then have room (rows of 128 bytes:
+// 48 KB a workgroup), else two (rows of 256 or 512 bytes: 64 or 128 KB).
 constexpr int stages_of(int row_bytes) { return row_bytes <= 128 ? 3 : 2; }
 constexpr int kCUs = 256;
 

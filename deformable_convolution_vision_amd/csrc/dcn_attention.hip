@@ -24,7 +24,24 @@
 //
 // Arithmetic: products of bf16 (exact) or fp32 added in fp32; the softmax in fp32; for bf16
 // the weights exp(s - m) are rounded to bf16 as the second product's operand (their sum is
-// not), and the output is rounded once.
+// not), and the output is rounded once.  (That rounding is what the matrix units' bf16 rate costs:
+// the output is 1.4 times one rounding away from the exact one.  The sum by a product with ones,
+// 16 additions fewer a lane, would be the rounded weights' and put lse off by 1e-4: not done.)
+//
+// What bounds it, measured (copies reach 5.0 TB/s on this card, products 1253 TFLOP/s of bf16):
+//  - Single tokens: the keys' and values' bytes.  8 batch elements of 16 heads of 128 on 4 key heads,
+//    16800 keys, 203 MB attended: 58 us in all, of which the join of the parts is 4.5 and about 5 the
+//    start of each workgroup's first loads, which nothing hides; 1.1 GB take 215 us, the rate of a
+//    copy.  One row of 8 heads of 64 over 1050 keys: 10.3 us, a launch and one workgroup's chain of
+//    five steps.
+//  - 300 queries of 8 heads of 32 over 4200 keys, batch 2: 19.6 us, one round of 160 workgroups; each
+//    wave's chain of load, product, softmax, product over its 9 blocks, and the join of 16 waves.
+//  - 4200 queries over 16800 keys, 8 heads of 64, batch 2: 383 us, 755 TFLOP/s.  A tile of 64 keys and
+//    32 rows is 512 cycles of products and 842 of vector instructions (at the rates a loop of each
+//    alone reaches, four waves on a SIMD); 1638 are measured: the two overlap little.  Eight waves on
+//    two halves of the keys (390 against 371 us then) and the products of one tile among the
+//    exponentials of another (398 against 396) did not change that.
+//  - fp32: the matrix units, 16 times as many cycles as for bf16.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -186,7 +203,11 @@ __device__ __forceinline__ void join_waves(const Args& a, const Work& w, int row
 constexpr size_t join_lds(int waves) { return static_cast<size_t>(waves) * 32 * (36 + 2) * 4; }
 
 // 32 rows; the W waves of a workgroup take every W-th block of 32 keys and join at the end, so
-// no wave waits for another inside the loop.  A lane's key row comes straight from memory as
+// no wave waits for another inside the loop (the single-token case above: 137 us with tiles shared by
+// the waves and a mask byte waited for at each row, 65 with these and the mask in bits, 54 since no
+// LDS read waits for loads under way).  Two blocks on their
+// way instead of one need registers that a wave has not: 11.4 against 10.5 us for one token over
+// 1050 keys, 25.5 against 24.9 for 333 queries in fp32.  A lane's key row comes straight from memory as
 // the first product's operand; values go through two places in the LDS that are the wave's own.
 // The next block's rows are on their way while one is worked on.
 template <typename T, int DP, int W, bool VEC>
@@ -293,7 +314,9 @@ __global__ __launch_bounds__(64 * W) void attn_few_rows_kernel(Args a) {
 constexpr int waves_per_simd(int row_bytes) { return row_bytes <= 256 ? 2 : 1; }
 
 // Rows of 128 in four waves, which share a ring of STAGES key tiles of 64 in the LDS: while one
-// is worked on, the next STAGES - 1 are on their way.
+// is worked on, the next STAGES - 1 are on their way.  (4200 queries over 16800 keys, batch 2, 8 heads
+// of 64: 453 us with loads through registers into one tile, 387 with the ring, 383 with the maximum
+// raised lazily.)
 template <typename T, int DP, int STAGES, bool VEC>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(waves_per_simd(sizeof(T) * DP), waves_per_simd(sizeof(T) * DP)))) void attn_rows_kernel(Args a) {
   constexpr int KT = 64, DT = DP / 32, BUF = 2 * KT * DP, LOADS = 2 * tile_loads<T, DP, KT, 256>, AHEAD = STAGES - 1;
@@ -418,7 +441,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Args a, int rows) {
   put4<T, DP>(a, w, rows, rr, d, mm, ll, acc);
 }
 
-// Waves of the few-rows form: as many as the registers of a CU hold at this head size.
+// Waves of the few-rows form: as many as the registers of a CU hold at this head size (one workgroup
+// a CU: with the splits sized for two or three, the parts of a second round only add to the join).
 constexpr int waves_of(int es, int dp) { return es == 2 ? (dp == 32 ? 16 : 8) : (dp == 128 ? 4 : dp == 64 ? 8 : 16); }
 
 struct Plan {

@@ -29,9 +29,13 @@
 // That costs a product more: 4200 queries over 1050 keys, 8 heads of 64, batch 2, 99 us without,
 // 107 with both parts of dQ, 112 of dK too.
 //
-// What bounds it: the matrix products (14 Lq Lk D of the formulas' 10, and 4 for the second parts)
-// and the vector instructions for the weights hardly overlap within a SIMD; at that size they are
-// 33 and 31 us of the 112, and the parts of split tiles are 28 MB written and read again.
+// What bounds it, measured: at that size the matrix units are busy 39 % of the time (the products are
+// 14 Lq Lk D and 4 more for the second parts, of the formulas' 10), with the vector instructions for
+// the weights beside them, which hardly overlap with the products of the same SIMD; the pass over
+// the rows is 5 us, and adding the parts of split tiles (37 MB written, 28 read again) 8.  Two
+// batches of 300 queries of 8 heads of 32 over 4200 keys, 32.3 us: 27 of the one round of loops,
+// 3 and 4 the launches before and after it.  fp32 (129 queries of 4 heads on 2 of 64 over 515 keys,
+// batch 2, 25.6 us): 19 us are loops of one step each, the two other launches the rest.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
