@@ -36,9 +36,9 @@
 //    five steps.
 //  - 300 queries of 8 heads of 32 over 4200 keys, batch 2: 19.6 us, one round of 160 workgroups; each
 //    wave's chain of load, product, softmax, product over its 9 blocks, and the join of 16 waves.
-//  - 4200 queries over 16800 keys, 8 heads of 64, batch 2: 383 us, 755 TFLOP/s.  A tile of 64 keys and
+//  - 4200 queries over 16800 keys, 8 heads of 64, batch 2: 365 us, 792 TFLOP/s.  A tile of 64 keys and
 //    32 rows is 512 cycles of products and 842 of vector instructions (at the rates a loop of each
-//    alone reaches, four waves on a SIMD); 1638 are measured: the two overlap little.  Eight waves on
+//    alone reaches, four waves on a SIMD); 1560 are measured: the two overlap little.  Eight waves on
 //    two halves of the keys (390 against 371 us then) and the products of one tile among the
 //    exponentials of another (398 against 396) did not change that.
 //  - fp32: the matrix units, 16 times as many cycles as for bf16.
@@ -316,7 +316,9 @@ constexpr int waves_per_simd(int row_bytes) { return row_bytes <= 256 ? 2 : 1; }
 // Rows of 128 in four waves, which share a ring of STAGES key tiles of 64 in the LDS: while one
 // is worked on, the next STAGES - 1 are on their way.  (4200 queries over 16800 keys, batch 2, 8 heads
 // of 64: 453 us with loads through registers into one tile, 387 with the ring, 383 with the maximum
-// raised lazily.)
+// raised lazily.)  A wave goes first on its SIMD from its second products to its next loads, so that
+// its matrix instructions are not held up among the other wave's vector instructions: 381 -> 365 us
+// there, 46 -> 41 for 900 queries over 16800 keys, 8 heads of 32.  (The few-rows form gains nothing.)
 template <typename T, int DP, int STAGES, bool VEC>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(waves_per_simd(sizeof(T) * DP), waves_per_simd(sizeof(T) * DP)))) void attn_rows_kernel(Args a) {
   constexpr int KT = 64, DT = DP / 32, BUF = 2 * KT * DP, LOADS = 2 * tile_loads<T, DP, KT, 256>, AHEAD = STAGES - 1;
@@ -356,6 +358,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(waves_per_s
   // is on its way to the LDS before it reads from it.
   const auto turn = [&](const T* __restrict__ cur, T* __restrict__ to) {
     word[AHEAD] = send(to);
+    __builtin_amdgcn_s_setprio(0);
     const T* ks = cur;
     const T* vs = cur + KT * DP;
     f32x16 s[2];
@@ -371,6 +374,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(waves_per_s
     const uint32_t both[2] = {static_cast<uint32_t>(word[0]), static_cast<uint32_t>(word[0] >> 32)};
     typename POperand<T>::type pf[2];
     softmax_step<T>(s, both, a.c, run, o, pf);
+    __builtin_amdgcn_s_setprio(1);
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
       for (int n = 0; n < 2; ++n) {

@@ -125,6 +125,22 @@ __device__ __forceinline__ T* dkv_row(const Args& a, const Work& w, int key, int
 constexpr int kT = 64;           // rows of a tile in the LDS
 constexpr int kRowVals = 2 * kT; // lse and delta of a row tile
 
+// Waves of a SIMD (workgroups of a CU) that the registers allow.
+// (fp32 rows of 64: 107 us with one, 74 with two and a few registers spilled, at B 4, Lq 55, Lk 1736, 8 heads on
+// 2; bf16 rows of 128: 225 with one, 585 with two, at B 2, Lq = Lk = 2100, 8 heads.)
+constexpr int waves_per_simd(int es, int dp) { return es * dp <= 64 ? 3 : es * dp <= 128 || (es == 4 && dp == 64) ? 2 : 1; }
+
+// A wave's priority on its SIMD: first in its second products, so that they are not held up among
+// the other wave's vector instructions.  (B 2, Lq 4200, Lk 1050, 8 heads of 64: 114.5 -> 112 us; Lq = Lk
+// = 2100, 8 heads of 128: 241 -> 229; with three waves to a SIMD 32.6 -> 34 us, so not there.)
+template <typename T, int DP>
+__device__ __forceinline__ void go_first(bool first) {
+  if constexpr (sizeof(T) == 2 && waves_per_simd(sizeof(T), DP) < 3) {
+    if (first) __builtin_amdgcn_s_setprio(1);
+    else __builtin_amdgcn_s_setprio(0);
+  }
+}
+
 // What an operand of score gradients leaves of them by its rounding to bf16, as a second operand.
 __device__ __forceinline__ POperand<uint16_t>::type rest_of(const float (&ds)[16], const POperand<uint16_t>::type& pf) {
   POperand<uint16_t>::type rest;
@@ -206,6 +222,7 @@ __device__ __forceinline__ void dq_part(const Args& a, int tile, T* lds) {
         s = mma(kf[i], qf[i], s);
         p = mma(vf[i], gf[i], p);
       }
+      go_first<T, DP>(false);
       if (keep != 0xffffffffu) mask_scores(s, keep);
       float ds[16];
 #pragma unroll
@@ -214,6 +231,7 @@ __device__ __forceinline__ void dq_part(const Args& a, int tile, T* lds) {
       to_operand(ds, pf);
       if constexpr (sizeof(T) == 2) {
         const auto rest = rest_of(ds, pf);
+        go_first<T, DP>(true);
 #pragma unroll
         for (int i = 0; i < DT; ++i)
 #pragma unroll
@@ -334,6 +352,7 @@ __device__ __forceinline__ void dkv_part(const Args& a, int tile, T* lds) {
         s = mma(qf[i], kf[i], s);
         dp = mma(gf[i], vf[i], dp);
       }
+      go_first<T, DP>(false);
       float p[16], ds[16];
 #pragma unroll
       for (int r4 = 0; r4 < 4; ++r4) {
@@ -352,6 +371,7 @@ __device__ __forceinline__ void dkv_part(const Args& a, int tile, T* lds) {
       to_operand(ds, df);
       if constexpr (sizeof(T) == 2) {
         const auto rest = rest_of(ds, df);
+        go_first<T, DP>(true);
 #pragma unroll
         for (int i = 0; i < DT; ++i) {
           ov[i] = mma_rows<DP>(gs, r0, 32 * i, pf, ov[i]);
@@ -402,11 +422,6 @@ __device__ __forceinline__ void dkv_part(const Args& a, int tile, T* lds) {
   rows_out(ok, os, [&](int rr, int d, float4 v) { store(rr, d, v, 0); });
   rows_out(ov, os, [&](int rr, int d, float4 v) { store(rr, d, v, 1); });
 }
-
-// Waves of a SIMD (workgroups of a CU) that the registers allow.
-// (fp32 rows of 64: 107 us with one, 74 with two and a few registers spilled, at B 4, Lq 55, Lk 1736, 8 heads on
-// 2; bf16 rows of 128: 225 with one, 585 with two, at B 2, Lq = Lk = 2100, 8 heads.)
-constexpr int waves_per_simd(int es, int dp) { return es * dp <= 64 ? 3 : es * dp <= 128 || (es == 4 && dp == 64) ? 2 : 1; }
 
 // Workgroups kv0 .. kv1 - 1: dK and dV; the others (from q0 on): dQ.  Those with the longer loops
 // come first (dQ first: 38 -> 32 us at B 2, Lq 300, Lk 4200, 8 heads of 32).
