@@ -36,9 +36,9 @@
 //    five steps.
 //  - 300 queries of 8 heads of 32 over 4200 keys, batch 2: 19.6 us, one round of 160 workgroups; each
 //    wave's chain of load, product, softmax, product over its 9 blocks, and the join of 16 waves.
-//  - 4200 queries over 16800 keys, 8 heads of 64, batch 2: 365 us, 792 TFLOP/s.  A tile of 64 keys and
-//    32 rows is 512 cycles of products and 842 of vector instructions (at the rates a loop of each
-//    alone reaches, four waves on a SIMD); 1560 are measured: the two overlap little.  Eight waves on
+//  - 4200 queries over 16800 keys, 8 heads of 64, batch 2: 362 to 378 us, 765 to 798
+//    TFLOP/s.  A tile of 64 keys and 32 rows is 512 cycles of products and 842 of vector instructions (at the rates a loop of each
+//    alone reaches, four waves on a SIMD); about 1580 are measured: the two overlap little.  Eight waves on
 //    two halves of the keys (390 against 371 us then) and the products of one tile among the
 //    exponentials of another (398 against 396) did not change that.
 //  - fp32: the matrix units, 16 times as many cycles as for bf16.
