@@ -616,7 +616,8 @@ def _call(name: str, device, *args) -> None:
 
 def _attention_key(query, key, value, key_mask, scale):
     """The fields of a descriptor after checks of the tensors' shapes, types, devices and strides
-    (elements of a head adjacent; the other strides free)."""
+    (elements of a head adjacent; the other strides free).  All are plain numbers: a scale that is
+    handed in as a tensor or an array of one value is read now, for each call."""
     dtype = _DTYPES.get(query.dtype)
     if dtype is None:
         raise TypeError(f"unsupported dtype {query.dtype}; use float32 or bfloat16")
@@ -648,7 +649,8 @@ def _attention_key(query, key, value, key_mask, scale):
         ms, inner = key_mask.stride()
         if Lk > 1 and inner != 1:
             raise ValueError("the positions of key_mask must be adjacent")
-    return B, Lq, Lk, Hq, Hkv, D, qs[:3], ks[:3], vs[:3], ms, scale if scale is not None else (D or 1) ** -0.5, dtype
+    scale = (D or 1) ** -0.5 if scale is None else float(scale)
+    return B, Lq, Lk, Hq, Hkv, D, qs[:3], ks[:3], vs[:3], ms, scale, dtype
 
 
 def attention_desc(query, key, value, key_mask=None, scale=None) -> AttnDesc:
@@ -765,7 +767,7 @@ def _norm_key(input, num_groups, weight, bias, eps, activation):
     P = 1
     for n in shape[1:-1]:
         P *= n
-    return shape[0], P, C, int(num_groups), eps, act, dtype, 0
+    return shape[0], P, C, int(num_groups), float(eps), act, dtype, 0   # plain numbers, as in _attention_key
 
 
 def norm_desc(input, num_groups, weight=None, bias=None, eps=1e-5, activation="none") -> NormDesc:
