@@ -904,6 +904,7 @@ template <typename T, int V>
 int backward(const dcn_norm_desc* d, Args* a, hipStream_t stream) {
   plan(d, V, sizeof(T), a);
   const bool params = a->gw != nullptr || a->gb != nullptr;
+  if (a->B == 0 && !params) return DCN_OK;   // grad_x is empty: a grid of no batch element is no launch
   const bool whole = fits_slice(d, V, grad_held(sizeof(T)));
   if (a->B > 0 && (whole || fits_slice(d, 1, grad_held(sizeof(T))))) {
     if (!params) a->cpart = nullptr;

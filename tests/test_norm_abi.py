@@ -88,3 +88,9 @@ def test_binding_refuses_what_is_not_on_a_gpu(lib):
         dcn.group_norm_act(torch.zeros(1, 4, 8), 2)
     with pytest.raises(TypeError):
         dcn.group_norm_act(torch.zeros(1, 4, 8).half(), 2)
+
+
+def test_an_empty_batch_with_only_grad_x_launches_nothing(lib):
+    d = desc(batch=0)
+    r = ctypes.byref(d)
+    assert lib.dcn_group_norm_backward(r, FAKE, None, None, FAKE, FAKE, FAKE, FAKE, None, None, None, 0, None) == dcn.OK
