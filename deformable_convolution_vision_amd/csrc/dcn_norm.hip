@@ -877,10 +877,11 @@ const void* grad_slice_kernel(int act) {
 }
 
 // Whether a group's positions fit `held` vectors (of V elements, within the group) of each thread of
-// a slice.
+// a slice, and one launch takes a slice for each group and batch element: a dispatch counts its
+// threads in 32 bits.
 bool fits_slice(const dcn_norm_desc* d, int V, int held) {
-  const int64_t Cg = d->channels / d->groups;
-  return Cg % V == 0 && Cg / V <= kST && d->positions <= held * (kST / (Cg / V));
+  const int64_t Cg = d->channels / d->groups, most = (int64_t{1} << 32) / kST - 8;
+  return Cg % V == 0 && Cg / V <= kST && d->positions <= held * (kST / (Cg / V)) && d->batch * d->groups <= most;
 }
 
 template <typename T, int V>

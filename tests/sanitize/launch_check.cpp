@@ -1,0 +1,89 @@
+// launch_check.cpp -- records the launches of the attention and group norm entry points (no GPU:
+// hipLaunchKernel is this file's) and checks that each can be made: a dispatch counts the
+// threads of each dimension of its grid in 32 bits, and none may be 0.
+// Test infrastructure: built and run by tests/test_launch_shapes.py on the CPU.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <cstdio>
+#include <cstring>
+
+#include "dcn.h"
+
+namespace {
+
+int fails = 0, launches = 0;
+int64_t groups = 0;   // workgroups along x of the calls since reset()
+const char* now = "";
+
+void reset(const char* what) {
+  now = what;
+  launches = 0;
+  groups = 0;
+}
+void expect(bool ok, const char* what) {
+  if (!ok) {
+    std::printf("FAIL %s: %s (%d launches, %lld workgroups)\n", now, what, launches, static_cast<long long>(groups));
+    ++fails;
+  }
+}
+
+}  // namespace
+
+extern "C" hipError_t hipLaunchKernel(const void*, dim3 grid, dim3 block, void**, size_t lds, hipStream_t) {
+  const uint64_t g[3] = {grid.x, grid.y, grid.z}, b[3] = {block.x, block.y, block.z};
+  for (int i = 0; i < 3; ++i) {
+    expect(g[i] > 0 && b[i] > 0, "a grid of nothing");
+    expect(g[i] * b[i] < uint64_t{1} << 32, "more threads than a dispatch counts");
+  }
+  expect(grid.y < 65536 && grid.z < 65536, "more workgroups along y or z than a launch takes");
+  expect(block.x * block.y * block.z <= 1024, "too many threads a workgroup");
+  expect(lds <= 160 * 1024, "more LDS than a CU has");
+  ++launches;
+  groups += grid.x;
+  return hipSuccess;
+}
+
+namespace {
+
+alignas(256) char mem[512];
+void* const p = mem;   // no call reads or writes it: nothing is launched
+
+dcn_norm_desc norm(int64_t B, int64_t P, int64_t C, int64_t G, int32_t dt) {
+  dcn_norm_desc d;
+  std::memset(&d, 0, sizeof(d));
+  d.batch = B;
+  d.positions = P;
+  d.channels = C;
+  d.groups = G;
+  d.eps = 1e-5f;
+  d.activation = DCN_ACT_GELU;
+  d.dtype = dt;
+  return d;
+}
+
+void run_norm(const dcn_norm_desc& d, bool slice, const char* what) {
+  float* const f = reinterpret_cast<float*>(mem);
+  reset(what);
+  expect(dcn_group_norm(&d, p, p, p, p, f, f, p, SIZE_MAX, nullptr) == DCN_OK, "status");
+  if (slice) expect(groups >= d.batch * d.groups, "a workgroup for each group");
+  reset(what);
+  expect(dcn_group_norm_backward(&d, p, p, p, f, f, p, p, p, p, p, SIZE_MAX, nullptr) == DCN_OK, "gradients' status");
+  if (slice) expect(groups >= d.batch * d.groups, "a workgroup for each group of the gradients");
+}
+
+}  // namespace
+
+int main() {
+  for (int32_t dt : {static_cast<int32_t>(DCN_F32), static_cast<int32_t>(DCN_BF16)}) {
+    run_norm(norm(2, 1050, 256, 32, dt), true, "norm of a small map");
+    run_norm(norm(8, 16800, 256, 32, dt), false, "norm of large maps");
+    run_norm(norm(65528, 49, 64, 64, dt), true, "norm of many small maps, nearly 2^22 groups");
+    run_norm(norm(32768, 49, 128, 128, dt), false, "norm of many small maps, 2^22 groups");
+    run_norm(norm(65534, 7, 8192, 8192, dt), false, "norm of the most groups");
+    run_norm(norm(65534, 3000, 8192, 64, dt), false, "norm of the most batch elements");
+    run_norm(norm(1, 2147483647, 1, 1, dt), false, "norm of the most positions");
+  }
+  if (fails == 0) std::printf("LAUNCHES OK\n");
+  return fails == 0 ? 0 : 1;
+}
