@@ -53,6 +53,7 @@ struct Args {
   int B, Lq, Lk, Hq, Hkv, g, D;
   int R;                       // query rows of one key head: g * Lq, row r = position r / g, head r % g
   Tiling y, ykv;               // of the forward or dQ; of dK and dV
+  int first;                   // workgroups of this kernel in launches before this one
   float c;                     // scale * log2(e): softmax runs in powers of two
   float scale;
 };
@@ -468,6 +469,18 @@ inline int padded_head(int64_t D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
 // 48 KB a workgroup), else two (rows of 256 or 512 bytes: 64 or 128 KB).
 constexpr int stages_of(int row_bytes) { return row_bytes <= 128 ? 3 : 2; }
 constexpr int kCUs = 256;
+
+// Launches n workgroups of `threads` threads.  A dispatch counts its threads in 32 bits: beyond that
+// they go in several launches, each of which is told (Args::first) how many went before it.
+inline bool launch_groups(const void* fn, int64_t n, int threads, void** args, Args* a, size_t lds, hipStream_t stream) {
+  constexpr int64_t kMost = int64_t{1} << 21;   // of up to 1024 threads
+  for (int64_t first = 0; first < n; first += kMost) {
+    a->first = static_cast<int>(first);
+    const int64_t now = n - first < kMost ? n - first : kMost;
+    if (hipLaunchKernel(fn, dim3(static_cast<unsigned>(now)), dim3(threads), args, lds, stream) != hipSuccess) return false;
+  }
+  return true;
+}
 
 // Descriptor checks of every attention entry point: DCN_OK or a negative dcn_status.
 int check(const dcn_attn_desc* d);

@@ -217,7 +217,7 @@ __global__ __launch_bounds__(64 * W) void attn_few_rows_kernel(Args a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   T* const lds = reinterpret_cast<T*>(smem) + wave * (AHEAD + 1) * 32 * DP;
-  const Work w = work_of(a, a.y, blockIdx.x, 32, (a.Lk + 32 * W - 1) / (32 * W));
+  const Work w = work_of(a, a.y, a.first + blockIdx.x, 32, (a.Lk + 32 * W - 1) / (32 * W));
   const T* kp = static_cast<const T*>(a.k) + w.b * a.ks[0] + w.hk * a.ks[2];
   const T* vp = static_cast<const T*>(a.v) + w.b * a.vs[0] + w.hk * a.vs[2];
   const uint8_t* mp = a.mask == nullptr ? nullptr : a.mask + w.b * a.ms;
@@ -327,7 +327,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(waves_per_s
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   T* const lds = reinterpret_cast<T*>(smem);              // [STAGES][keys, values][KT][DP]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Work w = work_of(a, a.y, blockIdx.x, 128, (a.Lk + KT - 1) / KT);
+  const Work w = work_of(a, a.y, a.first + blockIdx.x, 128, (a.Lk + KT - 1) / KT);
   const T* kp = static_cast<const T*>(a.k) + w.b * a.ks[0] + w.hk * a.ks[2];
   const T* vp = static_cast<const T*>(a.v) + w.b * a.vs[0] + w.hk * a.vs[2];
   const uint8_t* mp = a.mask == nullptr ? nullptr : a.mask + w.b * a.ms;
@@ -601,10 +601,7 @@ extern "C" int dcn_cross_attention(const dcn_attn_desc* d, const void* q, const 
   const int tail = p.y.tiles - p.y.full;
   void* args[] = {&a};
   const void* fn = bf16 ? fwd_kernel<uint16_t>(p.dp, p.wide, vec) : fwd_kernel<float>(p.dp, p.wide, vec);
-  if (hipLaunchKernel(fn, dim3(static_cast<unsigned>(workgroups(p.y))), dim3(64 * p.waves), args,
-                      lds_bytes(p, es), stream) !=
-      hipSuccess)
-    return DCN_E_HIP;
+  if (!launch_groups(fn, workgroups(p.y), 64 * p.waves, args, &a, lds_bytes(p, es), stream)) return DCN_E_HIP;
   if (tail > 0) {
     const int64_t n = static_cast<int64_t>(tail) * p.rows * (p.dp / 4);
     int rows = p.rows;

@@ -72,6 +72,33 @@ void run_norm(const dcn_norm_desc& d, bool slice, const char* what) {
   if (slice) expect(groups >= d.batch * d.groups, "a workgroup for each group of the gradients");
 }
 
+dcn_attn_desc attn(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int64_t D, int32_t dt) {
+  dcn_attn_desc d;
+  std::memset(&d, 0, sizeof(d));
+  d.batch = B;
+  d.query_len = Lq;
+  d.key_len = Lk;
+  d.query_heads = Hq;
+  d.key_heads = Hkv;
+  d.head_dim = D;
+  const int64_t row[3] = {0, 1 << 10, 128};
+  std::memcpy(d.q_stride, row, sizeof(row));
+  std::memcpy(d.k_stride, row, sizeof(row));
+  std::memcpy(d.v_stride, row, sizeof(row));
+  d.scale = 0.125f;
+  d.dtype = dt;
+  return d;
+}
+
+// rows: of a tile of the forward
+void run_attn(const dcn_attn_desc& d, int rows, const char* what) {
+  float* const f = reinterpret_cast<float*>(mem);
+  const int64_t pairs = d.batch * d.key_heads, r = d.query_len * (d.query_heads / d.key_heads);
+  reset(what);
+  expect(dcn_cross_attention(&d, p, p, p, nullptr, p, f, p, SIZE_MAX, nullptr) == DCN_OK, "status");
+  expect(groups >= pairs * ((r + rows - 1) / rows), "a workgroup for each tile");
+}
+
 }  // namespace
 
 int main() {
@@ -84,6 +111,15 @@ int main() {
     run_norm(norm(65534, 3000, 8192, 64, dt), false, "norm of the most batch elements");
     run_norm(norm(1, 2147483647, 1, 1, dt), false, "norm of the most positions");
   }
+  for (int32_t dt : {static_cast<int32_t>(DCN_F32), static_cast<int32_t>(DCN_BF16)})
+    for (int64_t D : {8, 20, 64, 128}) {
+      run_attn(attn(2, 300, 4200, 8, 8, D, dt), 32, "attention of queries");
+      run_attn(attn(2, 4200, 16800, 8, 8, D, dt), 128, "attention of a map");
+      run_attn(attn(1 << 20, 1, 9, 16, 8, D, dt), 32, "attention of 2^23 pairs of one token");
+      run_attn(attn(1 << 20, 49, 49, 4, 4, D, dt), 32, "attention of 2^22 windows");
+      run_attn(attn(2000000, 97, 97, 4, 4, D, dt), 128, "attention of 8000000 windows in the rows form");
+      run_attn(attn(1, 2000000000, 5, 1, 1, D, dt), 128, "attention of 2000000000 rows");
+    }
   if (fails == 0) std::printf("LAUNCHES OK\n");
   return fails == 0 ? 0 : 1;
 }

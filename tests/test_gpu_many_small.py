@@ -1,5 +1,5 @@
-"""More small problems than one dispatch counts threads for (2^32): group norm of many small maps,
-against the definition in 64 bits."""
+"""More small problems than one dispatch counts threads for (2^32): group norm of many small maps
+and attention of many pairs of a batch element and a key head, against the definition in 64 bits."""
 
 import numpy as np
 import pytest
@@ -7,7 +7,7 @@ import torch
 
 import deformable_convolution_vision_amd as dcn
 import norm_oracle
-from attention_oracle import check
+from attention_oracle import attention, check
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +37,32 @@ def test_norm_of_many_small_maps(dtype):
     ref = norm_oracle.backward(f64(go), f64(x), f64(mean), f64(rstd), C, f64(w), f64(b), "silu", kind)
     for n, t in zip(("gx", "gw", "gb"), grads):
         check(f64(t), ref[n], ref[n + "_tol"], n)
+
+
+def make_pairs(dtype):
+    """One token of 16 heads of 8 on 8 key heads over 3 states, for 2^19 + 3 batch elements: more than
+    2^22 pairs."""
+    B, g = (1 << 19) + 3, torch.Generator().manual_seed(12)
+    q, dout = (torch.randn((B, 1, 16, 8), generator=g).to(dtype).cuda() for _ in range(2))
+    k, v = (torch.randn((B, 3, 8, 8), generator=g).to(dtype).cuda() for _ in range(2))
+    mask = torch.rand((B, 3), generator=g).cuda() < 0.7
+    return q, k, v, mask, dout
+
+
+# the elements that are compared with 64 bits: the ends, and about those where a launch may end
+SOME = [i + j for i in (0, 1 << 17, 1 << 18, 3 << 17, (1 << 19) - 1) for j in (0, 1, 2, 3)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_attention_of_many_small_pairs(dtype):
+    q, k, v, mask, _ = make_pairs(dtype)
+    out, lse = dcn.cross_attention(q, k, v, key_mask=mask, return_lse=True)
+    torch.cuda.synchronize()
+    ref = attention(*(f64(t[SOME]) for t in (q, k, v)), mask[SOME].cpu().numpy(), 8 ** -0.5,
+                    "f32" if dtype == torch.float32 else "bf16")
+    check(f64(out[SOME]), ref["out"], ref["out_tol"], "out")
+    check(f64(lse[SOME]), ref["lse"], ref["lse_tol"], "lse")
+    for at in range(0, q.shape[0], 1 << 17):     # every element, in calls of one launch
+        piece = slice(at, at + (1 << 17))
+        got = dcn.cross_attention(q[piece], k[piece], v[piece], key_mask=mask[piece], return_lse=True)
+        assert torch.equal(got[0], out[piece]) and torch.equal(got[1], lse[piece]), at
