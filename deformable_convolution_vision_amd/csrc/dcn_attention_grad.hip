@@ -56,7 +56,7 @@ template <typename T, int DP, bool VEC>
 __global__ __launch_bounds__(256) void attn_grad_rows_kernel(Args a) {
   constexpr int LPR = VEC ? Tile<T, DP>::kVecs : 16, RPB = 256 / LPR;   // lanes of a row, rows of a workgroup
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv * a.R;
-  const int64_t prow = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / LPR;
+  const int64_t prow = (static_cast<int64_t>(a.first) + blockIdx.x) * RPB + threadIdx.x / LPR;
   if (prow >= rows) return;
   const int sub = threadIdx.x % LPR;
   const int bh = static_cast<int>(prow / a.R), r = static_cast<int>(prow % a.R);
@@ -430,7 +430,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(waves_per_s
 void attn_grad_kernel(Args a, int kv0, int kv1, int q0) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   T* lds = reinterpret_cast<T*>(smem);
-  const int id = blockIdx.x;
+  const int id = a.first + blockIdx.x;
   if (id < kv0 || id >= kv1) dq_part<T, DP, STAGES, VEC>(a, id - q0, lds);
   else dkv_part<T, DP, STAGES, VEC>(a, id - kv0, lds);
 }
@@ -527,9 +527,7 @@ int run_grad(Args& a, const Layout& y, bool vec, hipStream_t stream) {
   void* args[] = {&a};
   if (rows > 0) {
     const int per = vec ? 256 / Tile<T, DP>::kVecs : 16;
-    if (hipLaunchKernel(rows_kernel<T, DP>(vec), dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(256), args, 0,
-                        stream) != hipSuccess)
-      return DCN_E_HIP;
+    if (!launch_groups(rows_kernel<T, DP>(vec), (rows + per - 1) / per, 256, args, &a, 0, stream)) return DCN_E_HIP;
   }
   const bool q = a.dq != nullptr && rows > 0, keys = (a.dk != nullptr || a.dv != nullptr) && a.Lk > 0;
   const int64_t kv = keys ? workgroups(y.kv) : 0, nq = q ? workgroups(y.q) : 0, grid = kv + nq;
@@ -537,9 +535,7 @@ int run_grad(Args& a, const Layout& y, bool vec, hipStream_t stream) {
   const bool q_first = y.q.per_split > y.kv.per_split;
   int kv0 = q_first ? static_cast<int>(nq) : 0, kv1 = kv0 + static_cast<int>(kv), q0 = q_first ? 0 : kv1;
   void* grad_args[] = {&a, &kv0, &kv1, &q0};
-  if (hipLaunchKernel(grad_kernel<T, DP>(vec), dim3(static_cast<unsigned>(grid)), dim3(256), grad_args,
-                      grad_lds(DP * sizeof(T)), stream) != hipSuccess)
-    return DCN_E_HIP;
+  if (!launch_groups(grad_kernel<T, DP>(vec), grid, 256, grad_args, &a, grad_lds(DP * sizeof(T)), stream)) return DCN_E_HIP;
   int64_t q4 = q ? static_cast<int64_t>(y.q.tiles - y.q.full) * 128 * (DP / 4) : 0;
   int64_t n4 = q4 + (keys ? static_cast<int64_t>(y.kv.tiles - y.kv.full) * 2 * 128 * (DP / 4) : 0);
   if (n4 == 0) return DCN_OK;

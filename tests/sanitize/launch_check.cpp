@@ -97,6 +97,10 @@ void run_attn(const dcn_attn_desc& d, int rows, const char* what) {
   reset(what);
   expect(dcn_cross_attention(&d, p, p, p, nullptr, p, f, p, SIZE_MAX, nullptr) == DCN_OK, "status");
   expect(groups >= pairs * ((r + rows - 1) / rows), "a workgroup for each tile");
+  reset(what);
+  expect(dcn_cross_attention_backward(&d, p, p, p, nullptr, p, f, p, p, p, p, p, SIZE_MAX, nullptr) == DCN_OK,
+         "gradients' status");
+  expect(groups >= pairs * ((r + 127) / 128 + (d.key_len + 127) / 128), "a workgroup for each tile of the gradients");
 }
 
 }  // namespace

@@ -66,3 +66,21 @@ def test_attention_of_many_small_pairs(dtype):
         piece = slice(at, at + (1 << 17))
         got = dcn.cross_attention(q[piece], k[piece], v[piece], key_mask=mask[piece], return_lse=True)
         assert torch.equal(got[0], out[piece]) and torch.equal(got[1], lse[piece]), at
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_attention_gradients_of_many_small_pairs(dtype):
+    """Over 2^24 workgroups of the gradients' launch: 2 for each of 2^23 pairs."""
+    q, k, v, mask, dout = (torch.cat([t, t]) for t in make_pairs(dtype))
+    out, lse = dcn.cross_attention(q, k, v, key_mask=mask, return_lse=True)
+    grads = dcn.cross_attention_backward(dout, q, k, v, out, lse, key_mask=mask)
+    torch.cuda.synchronize()
+    last = [-1, -2, -3]
+    ref = attention(*(f64(t[SOME + last]) for t in (q, k, v)), mask[SOME + last].cpu().numpy(), 8 ** -0.5,
+                    "f32" if dtype == torch.float32 else "bf16", f64(dout[SOME + last]))
+    for n, t in zip(("gq", "gk", "gv"), grads):
+        check(f64(t[SOME + last]), ref[n], ref[n + "_tol"], n)
+    for at in range(0, q.shape[0], 1 << 17):
+        p = slice(at, at + (1 << 17))
+        for x, y in zip(grads, dcn.cross_attention_backward(dout[p], q[p], k[p], v[p], out[p], lse[p], key_mask=mask[p])):
+            assert torch.equal(x[p], y), at
