@@ -812,12 +812,31 @@ int columns(const Args& a, const Cut& c) { return (a.C + c.cb - 1) / c.cb; }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// one upper bound for both vector widths (16-byte rows or single elements, known at the call)
-size_t group_bytes(const dcn_norm_desc* d) {
-  return up256(static_cast<size_t>(d->batch) * kMaxChunks * d->groups * 8);
+// Whether a group's positions fit `held` vectors (of V elements, within the group) of each thread of
+// a slice, and one launch takes a slice for each group and batch element: a dispatch counts its
+// threads in 32 bits.
+bool fits_slice(const dcn_norm_desc* d, int V, int held) {
+  const int64_t Cg = d->channels / d->groups, most = (int64_t{1} << 32) / kST - 8;
+  return Cg % V == 0 && Cg / V <= kST && d->positions <= held * (kST / (Cg / V)) && d->batch * d->groups <= most;
 }
-size_t chan_bytes(const dcn_norm_desc* d) {
-  return up256(static_cast<size_t>(d->batch) * kMaxChunks * d->channels * 8);
+
+// What the parts of a call take, for either vector width (16-byte rows or single elements, known at
+// the call): `group` bytes of the groups' parts, then `chan` of the channels'.  A pass of sums has
+// max(B, 256) chunks at most over all batch elements (cut_of); a slice has no parts but the channels'
+// sums of each batch element, and is certain where single elements fit it.
+struct Parts {
+  size_t group, chan;
+};
+Parts forward_parts(const dcn_norm_desc* d) {
+  if (d->batch == 0 || fits_slice(d, 1, kHeld)) return {0, 0};
+  return {up256(static_cast<size_t>(std::max<int64_t>(d->batch, kMaxChunks)) * d->groups * 8), 0};
+}
+Parts backward_parts(const dcn_norm_desc* d) {
+  if (d->batch == 0) return {0, 0};
+  if (fits_slice(d, 1, grad_held(d->dtype == DCN_BF16 ? 2 : 4)))
+    return {0, d->batch > 1 ? up256(static_cast<size_t>(d->batch) * d->channels * 8) : 0};
+  const size_t chunks = static_cast<size_t>(std::max<int64_t>(d->batch, kMaxChunks));
+  return {up256(chunks * d->groups * 8), up256(chunks * d->channels * 8)};
 }
 
 size_t sums_lds(const Args& a, int V) {
@@ -874,14 +893,6 @@ const void* grad_slice_kernel(int act) {
     case DCN_ACT_GELU: return reinterpret_cast<const void*>(&norm_grad_slice_kernel<T, V, DCN_ACT_GELU>);
     default: return reinterpret_cast<const void*>(&norm_grad_slice_kernel<T, V, DCN_ACT_NONE>);
   }
-}
-
-// Whether a group's positions fit `held` vectors (of V elements, within the group) of each thread of
-// a slice, and one launch takes a slice for each group and batch element: a dispatch counts its
-// threads in 32 bits.
-bool fits_slice(const dcn_norm_desc* d, int V, int held) {
-  const int64_t Cg = d->channels / d->groups, most = (int64_t{1} << 32) / kST - 8;
-  return Cg % V == 0 && Cg / V <= kST && d->positions <= held * (kST / (Cg / V)) && d->batch * d->groups <= most;
 }
 
 template <typename T, int V>
@@ -945,7 +956,7 @@ int workspace_status(const void* ws, size_t have, size_t need) {
 extern "C" int dcn_group_norm_workspace_bytes(const dcn_norm_desc* d, size_t* bytes) {
   if (bytes == nullptr) return DCN_E_ARG;
   const int rc = dcn::norm::check(d);
-  if (rc == DCN_OK) *bytes = dcn::norm::group_bytes(d);
+  if (rc == DCN_OK) *bytes = dcn::norm::forward_parts(d).group;
   return rc;
 }
 
@@ -957,7 +968,7 @@ extern "C" int dcn_group_norm(const dcn_norm_desc* d, const void* x, const void*
   if (rc != DCN_OK) return rc;
   if (d->batch == 0) return DCN_OK;
   if (x == nullptr || out == nullptr) return DCN_E_ARG;
-  rc = workspace_status(workspace, workspace_bytes, group_bytes(d));
+  rc = workspace_status(workspace, workspace_bytes, forward_parts(d).group);
   if (rc != DCN_OK) return rc;
   Args a{};
   a.x = x;
@@ -975,8 +986,10 @@ extern "C" int dcn_group_norm(const dcn_norm_desc* d, const void* x, const void*
 extern "C" int dcn_group_norm_backward_workspace_bytes(const dcn_norm_desc* d, size_t* bytes) {
   if (bytes == nullptr) return DCN_E_ARG;
   const int rc = dcn::norm::check(d);
-  if (rc == DCN_OK) *bytes = dcn::norm::group_bytes(d) + dcn::norm::chan_bytes(d);
-  return rc;
+  if (rc != DCN_OK) return rc;
+  const dcn::norm::Parts need = dcn::norm::backward_parts(d);
+  *bytes = need.group + need.chan;
+  return DCN_OK;
 }
 
 extern "C" int dcn_group_norm_backward(const dcn_norm_desc* d, const void* x, const void* weight, const void* bias,
@@ -987,7 +1000,8 @@ extern "C" int dcn_group_norm_backward(const dcn_norm_desc* d, const void* x, co
   int rc = check(d);
   if (rc != DCN_OK) return rc;
   if (d->batch > 0 && (x == nullptr || mean == nullptr || rstd == nullptr || grad_out == nullptr)) return DCN_E_ARG;
-  rc = workspace_status(workspace, workspace_bytes, group_bytes(d) + chan_bytes(d));
+  const Parts need = backward_parts(d);
+  rc = workspace_status(workspace, workspace_bytes, need.group + need.chan);
   if (rc != DCN_OK) return rc;
   Args a{};
   a.x = x;
@@ -1000,7 +1014,7 @@ extern "C" int dcn_group_norm_backward(const dcn_norm_desc* d, const void* x, co
   a.gw = grad_weight;
   a.gb = grad_bias;
   a.gpart = static_cast<float*>(workspace);
-  a.cpart = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + group_bytes(d));
+  a.cpart = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + need.group);
   const bool bf16 = d->dtype == DCN_BF16;
   const bool vec = aligned(x) && aligned(grad_out) && aligned(grad_x) && d->channels % (bf16 ? 8 : 4) == 0;
   if (bf16) return vec ? backward<uint16_t, 8>(d, &a, stream) : backward<uint16_t, 1>(d, &a, stream);

@@ -14,6 +14,7 @@ namespace {
 
 int fails = 0, launches = 0;
 int64_t groups = 0;   // workgroups along x of the calls since reset()
+int64_t chunks = 0;   // chunks of all batch elements, of the first launch since then
 const char* now = "";
 
 void reset(const char* what) {
@@ -39,6 +40,7 @@ extern "C" hipError_t hipLaunchKernel(const void*, dim3 grid, dim3 block, void**
   expect(grid.y < 65536 && grid.z < 65536, "more workgroups along y or z than a launch takes");
   expect(block.x * block.y * block.z <= 1024, "too many threads a workgroup");
   expect(lds <= 160 * 1024, "more LDS than a CU has");
+  if (launches == 0) chunks = static_cast<int64_t>(grid.x) * grid.z;
   ++launches;
   groups += grid.x;
   return hipSuccess;
@@ -62,14 +64,22 @@ dcn_norm_desc norm(int64_t B, int64_t P, int64_t C, int64_t G, int32_t dt) {
   return d;
 }
 
-void run_norm(const dcn_norm_desc& d, bool slice, const char* what) {
+// at: an address in `mem` (of another alignment than 16 bytes: rows are read element by element)
+void run_norm(const dcn_norm_desc& d, bool slice, const char* what, void* at = p) {
   float* const f = reinterpret_cast<float*>(mem);
+  size_t nf = 0, nb = 0;
+  expect(dcn_group_norm_workspace_bytes(&d, &nf) == DCN_OK && dcn_group_norm_backward_workspace_bytes(&d, &nb) == DCN_OK,
+         "workspace status");
+  const int64_t part = d.groups * 8, chan = d.channels * 8, ws = nf, wb = nb;
   reset(what);
-  expect(dcn_group_norm(&d, p, p, p, p, f, f, p, SIZE_MAX, nullptr) == DCN_OK, "status");
+  expect(dcn_group_norm(&d, at, p, p, p, f, f, p, nf, nullptr) == DCN_OK, "status");
   if (slice) expect(groups >= d.batch * d.groups, "a workgroup for each group");
+  else expect(launches == 2 && chunks * part <= ws, "parts beyond the workspace");
   reset(what);
-  expect(dcn_group_norm_backward(&d, p, p, p, f, f, p, p, p, p, p, SIZE_MAX, nullptr) == DCN_OK, "gradients' status");
+  expect(dcn_group_norm_backward(&d, at, p, p, f, f, p, p, p, p, p, nb, nullptr) == DCN_OK, "gradients' status");
   if (slice) expect(groups >= d.batch * d.groups, "a workgroup for each group of the gradients");
+  if (slice) expect(d.batch == 1 || d.batch * chan <= wb, "sums of the batch elements beyond the workspace");
+  else expect(launches == 2 && chunks * (part + chan) <= wb, "parts of the gradients beyond the workspace");
 }
 
 dcn_attn_desc attn(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int64_t D, int32_t dt) {
@@ -114,6 +124,13 @@ int main() {
     run_norm(norm(65534, 7, 8192, 8192, dt), false, "norm of the most groups");
     run_norm(norm(65534, 3000, 8192, 64, dt), false, "norm of the most batch elements");
     run_norm(norm(1, 2147483647, 1, 1, dt), false, "norm of the most positions");
+    // two passes, whatever the vectors' width: parts stay within the workspace
+    for (int64_t B : {1, 2, 3, 100, 255, 256, 257, 3000})
+      for (int64_t P : {8200, 8201, 16800, 1000003})
+        for (int64_t Cg : {1, 3, 8, 64, 1024})
+          for (int64_t G : {1, 4, 8})
+            for (void* at : {p, static_cast<void*>(mem + (dt == DCN_BF16 ? 2 : 4))})
+              run_norm(norm(B, P, Cg * G, G, dt), false, "norm in two passes", at);
   }
   for (int32_t dt : {static_cast<int32_t>(DCN_F32), static_cast<int32_t>(DCN_BF16)})
     for (int64_t D : {8, 20, 64, 128}) {

@@ -94,3 +94,23 @@ def test_an_empty_batch_with_only_grad_x_launches_nothing(lib):
     d = desc(batch=0)
     r = ctypes.byref(d)
     assert lib.dcn_group_norm_backward(r, FAKE, None, None, FAKE, FAKE, FAKE, FAKE, None, None, None, 0, None) == dcn.OK
+
+
+@pytest.mark.parametrize("shape", [(1000, 49, 256, 32), (8192, 49, 256, 32), (65534, 49, 256, 32), (2000, 16, 1024, 32),
+                                   (64, 16800, 512, 32), (300, 70000, 64, 8), (65534, 49, 256, 256), (1, 1050, 256, 32)],
+                         ids=str)
+@pytest.mark.parametrize("dtype", [dcn.F32, dcn.BF16])
+def test_workspaces_are_those_of_the_parts(lib, shape, dtype):
+    """At most 256 chunks over all batch elements, or one for each: 8 bytes a group, and a channel of
+    the gradients.  (1000 maps of 49 positions and 256 bf16 channels, 25 MB, asked for 590 MB.)"""
+    B, P, C, G = shape
+    d = desc(batch=B, positions=P, channels=C, groups=G, dtype=dtype)
+    chunks = max(B, 256)
+    for backward, row in ((False, 8 * G), (True, 8 * (G + C))):
+        rc, nb = workspace(lib, d, backward)
+        assert rc == dcn.OK and nb <= chunks * row + 512 and nb % 256 == 0
+    # a group's positions in a workgroup's registers, one element a thread at a time: no parts
+    small = desc(batch=B, positions=49, channels=C, groups=G, dtype=dtype)
+    if B * G < 1 << 21 and C // G <= 32:
+        assert workspace(lib, small, False) == (dcn.OK, 0)
+        assert workspace(lib, small, True)[1] <= (8 * B * C + 255 if B > 1 else 0)
