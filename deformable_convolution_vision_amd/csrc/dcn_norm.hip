@@ -63,7 +63,7 @@ struct Args {
   float *mean, *rstd;        // [B][G]
   void *gw, *gb;
   float* gpart;              // [B][G][chunks][2]
-  float* cpart;              // backward: [B][chunks][C][2] (slices: one chunk)
+  float* cpart;              // backward: [B][chunks][C][2] (slices: one chunk, none for a single batch element)
   int64_t P;
   int B, C, G, Cg;
   Cut sum, write;
@@ -659,7 +659,7 @@ __global__ __launch_bounds__(kST) void norm_grad_slice_kernel(Args a) {
   const int64_t at = static_cast<int64_t>(b) * a.P * a.C + g * a.Cg + sub * V;
   const T* x = static_cast<const T*>(a.x) + at;
   const T* go = static_cast<const T*>(a.g) + at;
-  const bool mine = row < rows;
+  const bool mine = row < rows, params = a.gw != nullptr || a.gb != nullptr;
   Vec<T, V> v[HELD], gr[HELD];
 #pragma unroll
   for (int k = 0; k < HELD; ++k)
@@ -697,7 +697,7 @@ __global__ __launch_bounds__(kST) void norm_grad_slice_kernel(Args a) {
     t1 = fmaf(s1[j], w[j], t1);
     t2 = fmaf(s2[j], w[j], t2);
   }
-  if (a.cpart != nullptr) {
+  if (params) {
 #pragma unroll
     for (int j = 0; j < V; ++j) sums[j * kST + threadIdx.x] = make_float2(s1[j], s2[j]);
   }
@@ -723,7 +723,7 @@ __global__ __launch_bounds__(kST) void norm_grad_slice_kernel(Args a) {
         store<T, V>(out + static_cast<int64_t>(row + k * rows) * a.C, y);
       }
   }
-  if (a.cpart == nullptr) return;
+  if (!params) return;
   // the channels' sums over the rows of threads, 16 lanes for each channel
   const int used = min(rows, P);
   for (int c = threadIdx.x / 16; c < a.Cg; c += kST / 16) {
@@ -919,7 +919,6 @@ int backward(const dcn_norm_desc* d, Args* a, hipStream_t stream) {
   if (a->B == 0 && !params) return DCN_OK;   // grad_x is empty: a grid of no batch element is no launch
   const bool whole = fits_slice(d, V, grad_held(sizeof(T)));
   if (a->B > 0 && (whole || fits_slice(d, 1, grad_held(sizeof(T))))) {
-    if (!params) a->cpart = nullptr;
     if (!launch(whole ? grad_slice_kernel<T, V>(d->activation) : grad_slice_kernel<T, 1>(d->activation),
                 dim3((a->B * a->G + 7) / 8 * 8), params ? static_cast<size_t>(V) * kST * sizeof(float2) : 0, a, stream,
                 kST))
