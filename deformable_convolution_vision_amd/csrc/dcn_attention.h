@@ -258,6 +258,13 @@ template <int N>
 __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
+// The same where the places that the loads fill are restrict pointers of the function around it: the
+// wait names them, for the compiler would else take it to concern other memory and might move the
+// accesses that it stands between.
+template <int N>
+__device__ __forceinline__ void wait_loads(const void* cur, const void* to) {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N), "s"((const lds_void*)cur), "s"((const lds_void*)to) : "memory");
+}
 // waits for this wave's LDS reads and writes, but not for its loads, and for the other waves
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 

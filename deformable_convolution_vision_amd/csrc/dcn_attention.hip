@@ -288,7 +288,7 @@ __global__ __launch_bounds__(64 * W) void attn_few_rows_kernel(Args a) {
       const uint32_t m1[1] = {mine};
       typename POperand<T>::type pf[1];
       softmax_step<T>(s, m1, a.c, run, o, pf);
-      if constexpr (VEC) wait_loads<AHEAD * (KL + VL)>();   // this block's values are there
+      if constexpr (VEC) wait_loads<AHEAD * (KL + VL)>(cur, to);   // this block's values are there
 #pragma unroll
       for (int i = 0; i < DT; ++i) o[i] = mma_rows<DP>(cur, 0, 32 * i, pf[0], o[i]);
     };
