@@ -112,47 +112,62 @@ __device__ __forceinline__ void store(T* p, const float (&f)[V]) {
 }
 
 // The normal distribution's lower tail c = Phi(-|z|) = erfc(|z| / sqrt(2)) / 2, and e = exp(-z^2 / 2),
-// which it shares.  With t = 1 / (1 + a |z|), v = 1 - t = a |z| t, the quotient c / (e t) is smooth
-// over 0 <= v < 1 and is taken as a polynomial of degree 8 in v (weighted least squares at Chebyshev
-// points, weights raised where the relative error was largest; 2.1e-8 at most for |z| <= 13.3, beyond
-// which e is 0 in fp32).  v is formed as a product, so what is lost near z = 0 is relative to v; the
-// tail has no difference of near values: in all c is off by (22 + 1.5 z^2) 2^-24 of itself at most
-// (the z^2 from the rounding of the exponential's argument), and so is gelu, which takes c or 1 - c.
-// 5 instructions more than a rational form of the error function of 5 coefficients, which is off by
-// 1.5e-7 and leaves 6e-5 of gelu's value at z in [-3, -2]; erff took a third of the gelu backward.
+// which it shares.  With t = 1 / (1 + a |z|) the quotient c / (e t) is smooth over 0 < t <= 1 and is
+// taken as a polynomial (weighted least squares at Chebyshev points for |z| <= 13.3, beyond which e is
+// 0 in fp32, weights raised where the relative error was largest).  The tail has no difference of near
+// values, so gelu, which takes c or 1 - c, keeps its relative precision for z < 0.
+//  - fp32: degree 8 (2.1e-8) in v = 1 - t = a |z| t, formed as a product, so that what is lost near
+//    z = 0 is relative to v: c is off by (22 + 1.5 z^2) 2^-24 of itself at most, the z^2 from the
+//    rounding of the exponential's argument.
+//  - bf16, whose outputs keep 2^-9: degree 5 (4.6e-6) in t.  With fp32's polynomial 8 x 16800 positions
+//    of 256 channels take 49.9 us forward, and 2 x 16800 31.0 backward; with this one 45.1 and 29.7.
+// (erff takes a third of the gelu backward's instructions; a rational form of the error function of 5
+// coefficients is off by 1.5e-7, which is 6e-5 of gelu's value at z in [-3, -2]; 44.6 and 28.6 us.)
+template <typename T>
 __device__ __forceinline__ float lower_tail(float z, float& e) {
-  const float y = fminf(fabsf(z), 64.f) * 0.26f;   // (an infinity times its reciprocal would be none)
-  const float t = __builtin_amdgcn_rcpf(1.f + y), v = y * t;
   e = __builtin_amdgcn_exp2f(-0.72134752044448170f * z * z);
-  float p = fmaf(0.0308960844f, v, -0.0924284607f);
-  p = fmaf(p, v, 0.0373755172f);
-  p = fmaf(p, v, 0.142099783f);
-  p = fmaf(p, v, -0.0347089954f);
-  p = fmaf(p, v, -0.574499309f);
-  p = fmaf(p, v, 1.12941992f);
-  p = fmaf(p, v, -1.03439236f);
-  p = fmaf(p, v, 0.5f);
-  return p * t * e;
+  if constexpr (sizeof(T) == 2) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.305000007f, 1.f));
+    float p = fmaf(-0.0765512735f, t, 0.200597435f);
+    p = fmaf(p, t, -0.0027701701f);
+    p = fmaf(p, t, 0.139904127f);
+    p = fmaf(p, t, 0.116830379f);
+    p = fmaf(p, t, 0.121991396f);
+    return p * t * e;
+  } else {
+    const float y = fminf(fabsf(z), 64.f) * 0.26f;   // (an infinity times its reciprocal would be none)
+    const float t = __builtin_amdgcn_rcpf(1.f + y), v = y * t;
+    float p = fmaf(0.0308960844f, v, -0.0924284607f);
+    p = fmaf(p, v, 0.0373755172f);
+    p = fmaf(p, v, 0.142099783f);
+    p = fmaf(p, v, -0.0347089954f);
+    p = fmaf(p, v, -0.574499309f);
+    p = fmaf(p, v, 1.12941992f);
+    p = fmaf(p, v, -1.03439236f);
+    p = fmaf(p, v, 0.5f);
+    return p * t * e;
+  }
 }
 // Phi(z)
+template <typename T>
 __device__ __forceinline__ float normal_cdf(float z, float& e) {
-  const float c = lower_tail(z, e);
+  const float c = lower_tail<T>(z, e);
   return z < 0.f ? c : 1.f - c;
 }
 __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
 }
-template <int ACT>
+template <typename T, int ACT>
 __device__ __forceinline__ float act(float z) {
   if (ACT == DCN_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
   if (ACT == DCN_ACT_SILU) return z * sigmoid(z);
   if (ACT == DCN_ACT_GELU) {
     float e;
-    return z * normal_cdf(z, e);
+    return z * normal_cdf<T>(z, e);
   }
   return z;
 }
-template <int ACT>
+template <typename T, int ACT>
 __device__ __forceinline__ float slope(float z) {
   if (ACT == DCN_ACT_RELU) return z > 0.f ? 1.f : 0.f;
   if (ACT == DCN_ACT_SILU) {
@@ -161,7 +176,7 @@ __device__ __forceinline__ float slope(float z) {
   }
   if (ACT == DCN_ACT_GELU) {
     float e;
-    const float cdf = normal_cdf(z, e);
+    const float cdf = normal_cdf<T>(z, e);
     return fmaf(z * 0.39894228040143268f, e, cdf);
   }
   return 1.f;
@@ -372,7 +387,7 @@ __global__ __launch_bounds__(kNT) void norm_write_kernel(Args a) {
         if (row >= r1) break;
         float y[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) y[j] = act<ACT>(fmaf(widen(v[k].e[j]) - mean[j], scale[j], bias[j]));
+        for (int j = 0; j < V; ++j) y[j] = act<T, ACT>(fmaf(widen(v[k].e[j]) - mean[j], scale[j], bias[j]));
         if (next < r1) v[k] = load<T, V>(x + next * a.C + v0 * V);
         store<T, V>(out + row * a.C + v0 * V, y);
       }
@@ -426,7 +441,7 @@ __global__ __launch_bounds__(kNT) void norm_grad_sums_kernel(Args a) {
 #pragma unroll
           for (int j = 0; j < V; ++j) {
             const float n = (widen(v[k].e[j]) - mean[j]) * rstd[j];
-            const float gz = widen(gr[k].e[j]) * slope<ACT>(fmaf(n, w[j], bias[j]));
+            const float gz = widen(gr[k].e[j]) * slope<T, ACT>(fmaf(n, w[j], bias[j]));
             s1[j] += gz;
             s2[j] = fmaf(gz, n, s2[j]);
           }
@@ -545,7 +560,7 @@ __global__ __launch_bounds__(kNT) void norm_grad_write_kernel(Args a) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const float n = (widen(v[k].e[j]) - mean[j]) * rstd[j];
-          const float gz = widen(gr[k].e[j]) * slope<ACT>(fmaf(n, w[j], bias[j]));
+          const float gz = widen(gr[k].e[j]) * slope<T, ACT>(fmaf(n, w[j], bias[j]));
           y[j] = rstd[j] * (fmaf(gz, w[j], -m1[j]) - n * m2[j]);
         }
         if (next < r1) {
@@ -656,7 +671,7 @@ __global__ __launch_bounds__(kST) void norm_slice_kernel(Args a) {
     if (mine && row + k * rows < P) {
       float y[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) y[j] = act<ACT>(fmaf(widen(v[k].e[j]) - m, rstd * w[j], bias[j]));
+      for (int j = 0; j < V; ++j) y[j] = act<T, ACT>(fmaf(widen(v[k].e[j]) - m, rstd * w[j], bias[j]));
       store<T, V>(out + static_cast<int64_t>(row + k * rows) * a.C, y);
     }
 }
@@ -692,7 +707,7 @@ __global__ __launch_bounds__(kST) void norm_grad_slice_kernel(Args a) {
   }
   const auto gz_of = [&](int k, int j, float& n) {
     n = (widen(v[k].e[j]) - mean) * rstd;
-    return widen(gr[k].e[j]) * slope<ACT>(fmaf(n, w[j], bias[j]));
+    return widen(gr[k].e[j]) * slope<T, ACT>(fmaf(n, w[j], bias[j]));
   };
 #pragma unroll
   for (int k = 0; k < HELD; ++k)

@@ -358,8 +358,8 @@ int dcn_cross_attention_backward(const dcn_attn_desc* desc, const void* q, const
  * weight [C] and bias [C] or NULL (1 and 0); act one of dcn_activation (gelu by the error
  * function); mean and rstd [B][groups] float32 are written where not NULL (the backward takes
  * them).  x, weight, bias and out dense in desc->dtype; out may be x.  Arithmetic: fp32, out
- * rounded once.  gelu(z) in fp32 is within (24 + 1.5 z^2) 2^-24 of its value, for z < 0 too, down
- * to where exp(-z^2 / 2) is 0 in fp32.  Rows that start on 16 bytes (C a multiple of 8 bf16 or 4
+ * rounded once.  Before that rounding gelu(z) is within (24 + 1.5 z^2) 2^-24 of its value, for bf16
+ * (100 + 1.5 z^2) 2^-24, for z < 0 too, down to where exp(-z^2 / 2) is 0 in fp32.  Rows that start on 16 bytes (C a multiple of 8 bf16 or 4
  * fp32 elements) are read 16 bytes at a time, others element by element.  The workspace
  * (256-byte aligned) holds partial sums, 8 bytes a group (backward: and a channel) for each of
  * max(batch, 256) chunks at most.  Equal calls give equal bits.

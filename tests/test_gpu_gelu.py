@@ -4,7 +4,8 @@ can lose: Phi(-|z|) is a product of t = 1 / (1 + a |z|), a polynomial in a |z| t
 With u = 2^-24, t carries 3 u (a product, a sum, a reciprocal of 1 unit in the last place), the
 polynomial's argument 5 u of which at most 1.5 times enters, its steps 4 u, the exponential
 1.5 z^2 u from the three roundings of its argument and 2 u of its own, the products 2 u, the
-polynomial itself 0.5 u; gelu's last product 1 u: (24 + 1.5 z^2) u of the value."""
+polynomial itself 0.5 u; gelu's last product 1 u: (24 + 1.5 z^2) u of the value.  For bf16 the
+polynomial is off by 4.6e-6 (77 u) and takes t itself, whose error enters 3 times: (100 + 1.5 z^2) u."""
 
 import numpy as np
 import pytest
@@ -29,7 +30,7 @@ def test_gelu_and_its_slope(positions, dtype):
     w, b = torch.zeros(C, dtype=t, device="cuda"), z.cuda()
     out, mean, rstd = dcn.group_norm_act(x, G, w, b, activation="gelu", return_stats=True)
     zz = z.double().numpy()
-    tol = (24 + 1.5 * zz * zz) * U
+    tol = ({"f32": 24, "bf16": 100}[dtype] + 1.5 * zz * zz) * U
     # 1e-37: results below fp32's smallest normal number may be flushed
     want = zz * ndtr(zz)
     check(out.double().cpu().numpy()[0], np.broadcast_to(want, (positions, C)),
