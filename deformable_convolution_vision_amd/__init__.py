@@ -728,7 +728,7 @@ def dcn_cross_attention_backward(desc: AttnDesc, q, k, v, key_mask, out, lse, gr
 
 def cross_attention_backward(grad_out, query, key, value, out, lse, key_mask=None, scale=None, workspace=None):
     """Gradients of cross_attention on the GPU from its inputs, its out and lse, and the upstream
-    gradient grad_out [B,Lq,Hq,D]: returns dense (grad_query, grad_key, grad_value)."""
+    gradient grad_out [B,Lq,Hq,D] (contiguous): returns dense (grad_query, grad_key, grad_value)."""
     fields = _attention_key(query, key, value, key_mask, scale)
     desc, _, nbytes = _attention_plan(*fields)
     device = query.device

@@ -41,7 +41,13 @@
 //    alone reaches, four waves on a SIMD); about 1580 are measured: the two overlap little.  Eight waves on
 //    two halves of the keys (390 against 371 us then) and the products of one tile among the
 //    exponentials of another (398 against 396) did not change that.
-//  - fp32: the matrix units, 16 times as many cycles as for bf16.
+//  - fp32: the matrix units, 16 times as many cycles as for bf16, at padded heads (32, 64 or 128): 4200
+//    queries over 4200 keys, 8 heads of 40 or 64, 533 us (148 and 237 by the formulas' products at the
+//    library's rate); of 72 to 128, 1310 us (266 to 473): there a CU holds one workgroup of the rows
+//    form and the plan counts two, so 264 tiles take a second round of the chip.  One token of 8 heads
+//    of 64 over 1050 keys: 27 us, the chain of five steps at that rate.
+//  - Rows that are not read 16 bytes at a time: loads of single elements that are done before a tile's
+//    products begin.  2 x 4200 queries over 4200 keys, 8 bf16 heads of 36: 308 us, of 40: 105.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

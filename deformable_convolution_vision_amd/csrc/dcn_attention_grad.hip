@@ -34,8 +34,8 @@
 // the weights beside them, which hardly overlap with the products of the same SIMD; the pass over
 // the rows is 5 us, and adding the parts of split tiles (37 MB written, 28 read again) 8.  Two
 // batches of 300 queries of 8 heads of 32 over 4200 keys, 32.3 us: 27 of the one round of loops,
-// 3 and 4 the launches before and after it.  fp32 (129 queries of 4 heads on 2 of 64 over 515 keys,
-// batch 2, 25.6 us): 19 us are loops of one step each, the two other launches the rest.
+// the rest the launches before and after it (4.8 and 4.7 alone).  fp32 (129 queries of 4 heads on 2 of 64 over 515 keys,
+// batch 2, 25.5 us): 18 us are loops of one step each, the two other launches the rest.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

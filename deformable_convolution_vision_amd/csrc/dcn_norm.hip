@@ -26,13 +26,15 @@
 //
 // Arithmetic: fp32 throughout, every output rounded to its type once.
 //
-// What bounds it, measured: memory.  8 x 16800 positions of 256 bf16 channels (69 MB), silu: 15.1 us for
-// the sums (4.6 TB/s) and 27.4 for the writing pass (5.0 TB/s, a copy's rate), whose second reading of
-// the map is the 14 us that a single reading would save; the chip's registers could hold the map,
-// but its workgroups would have to wait for each other inside a launch.  Gradients at 2 x 16800:
-// 14.2 and 13.5 us for 34.6 and 52 MB, short of that rate because each CU reads only 130 KB.  One map
-// of 1050 positions: 6.4 us in one launch, which is that launch and one workgroup's chain (12.4 us
-// as two passes, host included, against 9.2).
+// What bounds it, measured: memory.  8 x 16800 positions of 256 bf16 channels (69 MB), silu: 15.3 us for
+// the sums (4.5 TB/s) and 27.0 for the writing pass (5.1 TB/s, a copy's rate), 49 us a call on maps that
+// are not in the cache; the second reading is the 14 us that a single one would save (the chip's
+// registers could hold the map, in a cooperative launch whose workgroups wait for each other once:
+// not tried).  Gradients at 2 x 16800: 13.1 us for 34.6 MB (2.6 TB/s: a CU has 32 KB of loads under
+// way) and 13.8 for 52.  fp32 forward at 8 x 16800: 70 us, 55 by its bytes.  One map of 1050 positions:
+// 6.4 us in one launch, which is that launch and one workgroup's chain (12.4 us as two passes, host
+// included, against 9.1).  Groups of a size that is no multiple of a 16-byte vector are read element
+// by element by a slice: 1050 positions of 8 groups of 12 bf16 channels 12.5 us, of 16 channels 8.9.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -604,8 +606,8 @@ __device__ __forceinline__ int unit_of(int n) { return static_cast<int>(blockIdx
 // A group in the registers of a workgroup, read once.  Threads form rows of vpr vectors (those of a
 // group's row) and `rows` positions at a time, so that a thread keeps its channels.  Few workgroups
 // (one for each group and batch element) against one launch and one reading: 1 x 1050 positions of
-// 256 bf16 channels in 32 groups 9.2 us against 12.4 as two passes, 3 x 1551 of 96 fp32 channels in 8
-// groups with their gradients 15.0 against 20.6.
+// 256 bf16 channels in 32 groups 9.1 us against 12.4 as two passes, 3 x 1551 of 96 fp32 channels in 8
+// groups with their gradients 15.0 to 16.0 against 20.6.
 template <typename T, int V, int ACT>
 __global__ __launch_bounds__(kST) void norm_slice_kernel(Args a) {
   __shared__ float2 lds[kST / 64];
@@ -826,7 +828,8 @@ Cut cut_of(const Args& a, int V, int es, int bytes, int64_t total, int64_t most)
 // bytes it took 22 us where rows take 15.6 (8 x 16800 positions of 256 bf16 channels).  The
 // writing pass takes columns of a line of memory (128 bytes), whose few groups are quick to
 // join: whole rows took 27.8 us, these 26.  One workgroup for each CU in both: with two the
-// backward at 2 x 16800 positions took 32 us, with one 26.4 (forward at batch 8: 43.5, 42.7).
+// backward at 2 x 16800 positions took 32 us, with one 26.4 (forward at batch 8: 43.5, 42.7; calls on one
+// map, of which the 256 MB cache holds part).
 void plan(const dcn_norm_desc* d, int V, int es, Args* a) {
   a->B = static_cast<int>(d->batch);
   a->P = d->positions;

@@ -309,8 +309,9 @@ int dcn_ps_roi_pool(const dcn_ps_roi_desc* desc, const void* x, const float* roi
  *    fused projection or of a longer cache are passed as they are.  key_mask [B,Lk] bytes with
  *    mask_stride between batch elements (0 repeats).  out [B,Lq,Hq,D] dense in desc->dtype;
  *    lse [B,Hq,Lq] float32 or NULL.
- *  - Rows whose addresses and strides are multiples of 16 bytes are read 16 bytes at a time;
- *    others element by element.
+ *  - Rows whose addresses and strides are multiples of 16 bytes, whose head_dim is a multiple of
+ *    16 bytes (8 bf16, 4 fp32 elements) and whose positions are at most 2^22 elements apart are read
+ *    16 bytes at a time; others element by element, which takes 4 times as long.
  *  - Arithmetic: scores, softmax statistics and sums in fp32; for bf16 the weights exp(s - max)
  *    are rounded to bf16 as an operand of the second product, and out is rounded once.
  *  - The workspace (256-byte aligned, dcn_cross_attention_workspace_bytes, 0 for many
