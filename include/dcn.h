@@ -311,7 +311,7 @@ int dcn_ps_roi_pool(const dcn_ps_roi_desc* desc, const void* x, const float* roi
  *    lse [B,Hq,Lq] float32 or NULL.
  *  - Rows whose addresses and strides are multiples of 16 bytes, whose head_dim is a multiple of
  *    16 bytes (8 bf16, 4 fp32 elements) and whose positions are at most 2^22 elements apart are read
- *    16 bytes at a time; others element by element, which takes 4 times as long.
+ *    16 bytes at a time; others element by element, which takes 3 to 9 times as long.
  *  - Arithmetic: scores, softmax statistics and sums in fp32; for bf16 the weights exp(s - max)
  *    are rounded to bf16 as an operand of the second product, and out is rounded once.
  *  - The workspace (256-byte aligned, dcn_cross_attention_workspace_bytes, 0 for many
