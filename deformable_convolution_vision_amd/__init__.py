@@ -26,6 +26,11 @@ __all__ = ["Desc", "dcn_output_hw", "dcn_workspace_bytes", "dcn_forward", "dcn_s
            "dcn_cross_attention_backward_workspace_bytes", "dcn_cross_attention_backward", "cross_attention_backward",
            "dcn_group_norm_workspace_bytes", "dcn_group_norm", "group_norm_act",
            "dcn_group_norm_backward_workspace_bytes", "dcn_group_norm_backward", "group_norm_act_backward",
+           "dcn_rotary", "rotary_positions", "dcn_rotary_backward", "rotary_positions_backward",
+           "dcn_residual_norm", "residual_norm", "dcn_residual_norm_backward_workspace_bytes",
+           "dcn_residual_norm_backward", "residual_norm_backward",
+           "dcn_paged_append", "paged_append", "dcn_paged_attention_workspace_bytes", "dcn_paged_attention",
+           "paged_attention",
            "DcnError", "library_path", "load_library", "F32", "BF16"]
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -40,7 +45,9 @@ _EXPORTS = ("dcn_output_hw", "dcn_workspace_bytes", "dcn_forward", "dcn_stage", 
             "dcn_offset_mask", "dcn_cross_attention_workspace_bytes", "dcn_cross_attention",
             "dcn_cross_attention_backward_workspace_bytes", "dcn_cross_attention_backward",
             "dcn_group_norm_workspace_bytes", "dcn_group_norm", "dcn_group_norm_backward_workspace_bytes",
-            "dcn_group_norm_backward")
+            "dcn_group_norm_backward", "dcn_rotary", "dcn_rotary_backward", "dcn_residual_norm",
+            "dcn_residual_norm_backward_workspace_bytes", "dcn_residual_norm_backward", "dcn_paged_append",
+            "dcn_paged_attention_workspace_bytes", "dcn_paged_attention")
 
 
 class DcnError(RuntimeError):
@@ -91,6 +98,47 @@ class NormDesc(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+_I64x2, _I64x3, _I32x4 = ctypes.c_int64 * 2, ctypes.c_int64 * 3, ctypes.c_int32 * 4
+
+
+class RotaryDesc(ctypes.Structure):
+    """Mirror of ``dcn_rotary_desc``."""
+    _fields_ = [("batch", ctypes.c_int64), ("length", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("head_dim", ctypes.c_int64), ("x_stride", _I64x3), ("position_stride", _I64x2),
+                ("axes", ctypes.c_int32), ("sections", _I32x4), ("layout", ctypes.c_int32),
+                ("position_type", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class ResidualDesc(ctypes.Structure):
+    """Mirror of ``dcn_residual_desc``."""
+    _fields_ = [("batch", ctypes.c_int64), ("positions", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("branch_norm", ctypes.c_int32), ("next_norm", ctypes.c_int32),
+                ("gate", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class AppendDesc(ctypes.Structure):
+    """Mirror of ``dcn_append_desc``."""
+    _fields_ = [("batch", ctypes.c_int64), ("length", ctypes.c_int64), ("query_heads", ctypes.c_int64),
+                ("key_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("max_pages", ctypes.c_int64), ("q_stride", _I64x3),
+                ("k_stride", _I64x3), ("v_stride", _I64x3), ("key_page_stride", _I64x3),
+                ("value_page_stride", _I64x3), ("table_stride", ctypes.c_int64), ("position_stride", _I64x2),
+                ("axes", ctypes.c_int32), ("sections", _I32x4), ("layout", ctypes.c_int32),
+                ("position_type", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class PagedDesc(ctypes.Structure):
+    """Mirror of ``dcn_paged_desc``."""
+    _fields_ = [("batch", ctypes.c_int64), ("query_heads", ctypes.c_int64), ("key_heads", ctypes.c_int64),
+                ("head_dim", ctypes.c_int64), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("max_pages", ctypes.c_int64), ("q_stride", _I64x2), ("key_page_stride", _I64x3),
+                ("value_page_stride", _I64x3), ("table_stride", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("dtype", ctypes.c_int32)]
+
+
+ROTARY_LAYOUTS = {"halves": 0, "adjacent": 1, "blocks": 2}
+ROW_NORMS = {"none": 0, "rms": 1, "layer": 2}
+_POSITION_TYPES = {torch.float32: 0, torch.int32: 1}
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
 _lib = None
@@ -154,7 +202,19 @@ def load_library() -> ctypes.CDLL:
     lib.dcn_group_norm.argtypes = [N, P, P, P, P, P, P, P, S, P]
     lib.dcn_group_norm_backward_workspace_bytes.argtypes = [N, ctypes.POINTER(S)]
     lib.dcn_group_norm_backward.argtypes = [N, P, P, P, P, P, P, P, P, P, P, S, P]
-    for name in ("dcn_cross_attention_workspace_bytes", "dcn_cross_attention",
+    lib.dcn_rotary.argtypes = [ctypes.POINTER(RotaryDesc), P, P, P, P, P]
+    lib.dcn_rotary_backward.argtypes = [ctypes.POINTER(RotaryDesc), P, P, P, P, P, P, P]
+    R = ctypes.POINTER(ResidualDesc)
+    lib.dcn_residual_norm.argtypes = [R] + [P] * 12
+    lib.dcn_residual_norm_backward_workspace_bytes.argtypes = [R, ctypes.POINTER(S)]
+    lib.dcn_residual_norm_backward.argtypes = [R] + [P] * 19 + [S, P]
+    lib.dcn_paged_append.argtypes = [ctypes.POINTER(AppendDesc)] + [P] * 13
+    lib.dcn_paged_attention_workspace_bytes.argtypes = [ctypes.POINTER(PagedDesc), ctypes.POINTER(S)]
+    lib.dcn_paged_attention.argtypes = [ctypes.POINTER(PagedDesc)] + [P] * 8 + [S, P]
+    for name in ("dcn_rotary", "dcn_rotary_backward", "dcn_residual_norm",
+                 "dcn_residual_norm_backward_workspace_bytes", "dcn_residual_norm_backward", "dcn_paged_append",
+                 "dcn_paged_attention_workspace_bytes", "dcn_paged_attention",
+                 "dcn_cross_attention_workspace_bytes", "dcn_cross_attention",
                  "dcn_cross_attention_backward_workspace_bytes", "dcn_cross_attention_backward",
                  "dcn_group_norm_workspace_bytes", "dcn_group_norm", "dcn_group_norm_backward_workspace_bytes",
                  "dcn_group_norm_backward"):
@@ -862,3 +922,416 @@ def group_norm_act_backward(grad_out, input, mean, rstd, num_groups, weight=None
           rstd.data_ptr(), grad_out.data_ptr(), gx.data_ptr(), _ptr(gw), _ptr(gb),
           workspace.data_ptr() if nbytes else None, nbytes)
     return gx, gw, gb
+
+
+# The calls below are checked once for each set of shapes, strides, types and devices: what a plan
+# is kept by says all that its checks look at, and no address or value is among it.
+
+def _raw(name: str, *args) -> None:
+    rc = getattr(load_library(), name)(*args)
+    if rc != OK:
+        raise DcnError(rc, name)
+
+
+def _bytes(name: str, desc) -> int:
+    n = ctypes.c_size_t()
+    _raw(name, ctypes.byref(desc), ctypes.byref(n))
+    return n.value
+
+
+def _element_type(dtype) -> int:
+    known = _DTYPES.get(dtype)
+    if known is None:
+        raise TypeError(f"unsupported dtype {dtype}; use float32 or bfloat16")
+    return known
+
+
+def _look(t):
+    """What a plan's checks look at in a tensor (None: none)."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
+
+def _heads(name, look, like=None):
+    """[B, L, H, D] on a GPU with the elements of a head adjacent: shape and the other strides."""
+    shape, stride, dtype, device = look
+    if len(shape) != 4:
+        raise ValueError(f"{name} must have four dimensions, got {tuple(shape)}")
+    if device.type != "cuda" or (like is not None and device != like[3]):
+        raise ValueError(f"{name} must be on {'a GPU' if like is None else like[3]}, got {device}")
+    if like is not None and dtype != like[2]:
+        raise TypeError(f"{name} must be {like[2]}, got {dtype}")
+    if shape[3] > 1 and stride[3] != 1:
+        raise ValueError(f"the elements of a head (the last dimension) of {name} must be adjacent")
+    return shape, stride[:3]
+
+
+def _rotation(positions, frequencies, sections, layout, B, L, device):
+    """The rotation's fields: position strides, axes, sections, layout, position type."""
+    kind = ROTARY_LAYOUTS.get(layout)
+    if kind is None:
+        raise ValueError(f"layout must be one of {', '.join(ROTARY_LAYOUTS)}, got {layout!r}")
+    axes = len(sections)
+    if not 1 <= axes <= 4 or min(sections) < 1:
+        raise ValueError(f"sections must be 1 to 4 numbers of pairs, got {sections}")
+    shape, stride, dtype, at = frequencies
+    if shape != (sum(sections),) or dtype != torch.float32 or at != device or (shape[0] > 1 and stride != (1,)):
+        raise ValueError(f"frequencies must be a contiguous float32 tensor of {sum(sections)} pairs on {device}")
+    if positions is None:
+        return (0, 0), axes, sections, kind, 1
+    shape, stride, dtype, at = positions
+    if dtype not in _POSITION_TYPES:
+        raise TypeError(f"positions must be float32 or int32, got {dtype}")
+    if shape != (B, L, axes) or at != device or (axes > 1 and stride[2] != 1):
+        raise ValueError(f"positions must be [{B}, {L}, {axes}] on {device} with adjacent axes, got {tuple(shape)}")
+    return stride[:2], axes, sections, kind, _POSITION_TYPES[dtype]
+
+
+@functools.lru_cache(maxsize=256)
+def _rotary_plan(x, positions, frequencies, sections, layout):
+    dtype = _element_type(x[2])
+    shape, strides = _heads("input", x)
+    B, L, H, D = shape
+    ps, axes, sections, kind, ptype = _rotation(positions, frequencies, sections, layout, B, L, x[3])
+    if 2 * sum(sections) > D:
+        raise ValueError(f"{sum(sections)} pairs do not fit heads of {D} elements")
+    if H < 1:
+        raise ValueError("input must have one head at least")
+    desc = RotaryDesc(B, L, H, D, _I64x3(*strides), _I64x2(*ps), axes, _I32x4(*sections), kind, ptype, dtype)
+    return desc, ctypes.byref(desc)
+
+
+def rotary_desc(input, positions, frequencies, sections, layout="halves") -> RotaryDesc:
+    """Descriptor of a rotation, for the raw entry points."""
+    return _rotary_plan(_look(input), _look(positions), _look(frequencies), tuple(map(int, sections)), layout)[0]
+
+
+def dcn_rotary(desc: RotaryDesc, x, positions, frequencies, out, stream=None) -> None:
+    """Raw call: tensors (or integer device addresses) laid out as dcn.h states."""
+    _raw("dcn_rotary", ctypes.byref(desc), _ptr(x), _ptr(positions), _ptr(frequencies), _ptr(out), _stream(stream))
+
+
+def rotary_positions(input, positions, frequencies, sections, layout="halves", out=None):
+    """Rotary positions with several axes on the GPU: pair p of every head of input [B,L,H,D] (float32 or
+    bfloat16, elements of a head adjacent, other strides free) turns by positions[b,l,a] *
+    frequencies[p], a the axis whose section p lies in.  positions [B,L,axes] (float32 or int32; an
+    expanded batch is fine), frequencies [sum(sections)] float32, sections the pairs of each of 1 to 4
+    axes.  layout: a pair is elements (p, p + pairs) ("halves"), (2p, 2p + 1) ("adjacent"), or each axis
+    has a block of elements taken by halves ("blocks"); elements behind the pairs are copied.  Returns
+    (or writes to `out`, which may be a contiguous input) [B,L,H,D]."""
+    _, desc = _rotary_plan(_look(input), _look(positions), _look(frequencies), tuple(map(int, sections)), layout)
+    device = input.device
+    if out is None:
+        out = torch.empty(input.shape, dtype=input.dtype, device=device)
+    else:
+        _check_out(out, input.shape, input.dtype, device)
+    _call("dcn_rotary", device, desc, input.data_ptr(), positions.data_ptr(), frequencies.data_ptr(), out.data_ptr())
+    return out
+
+
+def dcn_rotary_backward(desc: RotaryDesc, grad_out, positions, frequencies, x, grad_x, grad_positions,
+                        stream=None) -> None:
+    """Raw call: tensors (or integer device addresses) laid out as dcn.h states; either gradient may
+    be None (not computed)."""
+    _raw("dcn_rotary_backward", ctypes.byref(desc), _ptr(grad_out), _ptr(positions), _ptr(frequencies), _ptr(x),
+         _ptr(grad_x), _ptr(grad_positions), _stream(stream))
+
+
+def rotary_positions_backward(grad_out, positions, frequencies, sections, layout="halves", input=None):
+    """Gradients of rotary_positions on the GPU for the upstream gradient grad_out [B,L,H,D]
+    (contiguous): returns grad_input, or with the forward's input given (grad_input, grad_positions), the
+    latter [B,L,axes] float32."""
+    sections, device = tuple(map(int, sections)), grad_out.device
+    if input is not None and (input.shape != grad_out.shape or input.dtype != grad_out.dtype or input.device != device):
+        raise ValueError("input and grad_out must agree in shape, dtype and device")
+    _, desc = _rotary_plan(_look(grad_out if input is None else input), _look(positions), _look(frequencies), sections,
+                           layout)
+    if not grad_out.is_contiguous():
+        raise ValueError("grad_out must be contiguous")
+    gx = torch.empty(grad_out.shape, dtype=grad_out.dtype, device=device)
+    gp = None if input is None else torch.empty(positions.shape, dtype=torch.float32, device=device)
+    _call("dcn_rotary_backward", device, desc, grad_out.data_ptr(), positions.data_ptr(), frequencies.data_ptr(),
+          _ptr(input), gx.data_ptr(), _ptr(gp))
+    return gx if gp is None else (gx, gp)
+
+
+@functools.lru_cache(maxsize=256)
+def _residual_plan(x, branch, gate, scale, branch_norm, branch_weight, branch_bias, next_norm, next_weight, next_bias,
+                   eps):
+    shape, stride, tdtype, device = x
+    dtype = _element_type(tdtype)
+    if len(shape) < 2 or device.type != "cuda":
+        raise ValueError("input must be a GPU tensor [B, ..., C], channels last")
+    C = shape[-1]
+
+    def dense(look, want):
+        step, strides = 1, []
+        for n in reversed(want):
+            strides.insert(0, step)
+            step *= n
+        return look[0] == want and look[2] == tdtype and look[3] == device and \
+            all(n <= 1 or a == b for n, a, b in zip(want, look[1], strides))
+
+    kinds = [ROW_NORMS.get(n) for n in (branch_norm, next_norm)]
+    if None in kinds:
+        raise ValueError(f"norms must be among {', '.join(ROW_NORMS)}, got {branch_norm!r} and {next_norm!r}")
+    if 0 not in shape and not dense(x, tuple(shape)):
+        raise ValueError("input must be contiguous")
+    if branch[0] != shape or (0 not in shape and not dense(branch, tuple(shape))):
+        raise ValueError(f"branch must be a contiguous {tdtype} tensor of the input's shape {tuple(shape)} on {device}")
+    for name, look in (("scale", scale), ("branch_weight", branch_weight), ("branch_bias", branch_bias),
+                       ("next_weight", next_weight), ("next_bias", next_bias)):
+        if look is not None and not dense(look, (C,)):
+            raise ValueError(f"{name} must be a contiguous {tdtype} tensor of {C} channels on {device}")
+    if kinds[0] == 0 and (branch_weight is not None or branch_bias is not None):
+        raise ValueError("branch_weight and branch_bias need a branch_norm")
+    if kinds[1] == 0 and (next_weight is not None or next_bias is not None):
+        raise ValueError("next_weight and next_bias need a next_norm")
+    B, P = shape[0], 1
+    for n in shape[1:-1]:
+        P *= n
+    kind = 0
+    if gate is not None:
+        if gate[0] == shape and (0 in shape or dense(gate, tuple(shape))):
+            kind = 2
+        elif dense(gate, (B, C)):
+            kind = 1
+        else:
+            raise ValueError(f"gate must be a contiguous {tdtype} tensor of shape {(B, C)} or {tuple(shape)} on {device}")
+    desc = ResidualDesc(B, P, C, eps, kinds[0], kinds[1], kind, dtype, 0)
+    return desc, ctypes.byref(desc), _bytes("dcn_residual_norm_backward_workspace_bytes", desc)
+
+
+def _residual_key(x, branch, gate, scale, branch_norm, branch_weight, branch_bias, next_norm, next_weight, next_bias, eps):
+    return _residual_plan(_look(x), _look(branch), _look(gate), _look(scale), branch_norm, _look(branch_weight),
+                          _look(branch_bias), next_norm, _look(next_weight), _look(next_bias), float(eps))
+
+
+def residual_desc(input, branch, gate=None, scale=None, branch_norm="none", branch_weight=None, branch_bias=None,
+                  next_norm="layer", next_weight=None, next_bias=None, eps=1e-5) -> ResidualDesc:
+    """Descriptor of a join of two blocks, for the raw entry points."""
+    return _residual_key(input, branch, gate, scale, branch_norm, branch_weight, branch_bias, next_norm, next_weight,
+                         next_bias, eps)[0]
+
+
+def dcn_residual_norm(desc: ResidualDesc, x, branch, gate, scale, branch_weight, branch_bias, next_weight, next_bias,
+                      out, next, stats, stream=None) -> None:
+    """Raw call: tensors (or integer device addresses) laid out as dcn.h states."""
+    _raw("dcn_residual_norm", ctypes.byref(desc), *map(_ptr, (x, branch, gate, scale, branch_weight, branch_bias,
+                                                              next_weight, next_bias, out, next, stats)), _stream(stream))
+
+
+def residual_norm(input, branch, gate=None, scale=None, branch_norm="none", branch_weight=None, branch_bias=None,
+                  next_norm="layer", next_weight=None, next_bias=None, eps=1e-5, return_stats=False):
+    """What lies between two blocks, in one pass on the GPU: the norm after a block, its gate and residual
+    scale, the residual sum, and the norm before the next block.  input (the stream) and branch (the
+    block's output) [B, ..., C] (float32 or bfloat16, contiguous); norms over the last dimension, "none",
+    "rms" or "layer", with weights and biases [C] or None; gate [B, C] (shared by a batch element's
+    positions), of the input's shape, or None; scale [C] or None:
+        out = input + gate * scale * branch_norm(branch),  next = next_norm(out)
+    Returns (out, next), next None for next_norm "none"; or (out, next, stats) with stats
+    [B, ..., 4] float32, which residual_norm_backward takes."""
+    _, desc, _ = _residual_key(input, branch, gate, scale, branch_norm, branch_weight, branch_bias, next_norm,
+                               next_weight, next_bias, eps)
+    device = input.device
+    out = torch.empty_like(input)
+    then = None if next_norm == "none" else torch.empty_like(input)
+    stats = torch.empty(input.shape[:-1] + (4,), dtype=torch.float32, device=device) if return_stats else None
+    _call("dcn_residual_norm", device, desc, input.data_ptr(), branch.data_ptr(), _ptr(gate), _ptr(scale),
+          _ptr(branch_weight), _ptr(branch_bias), _ptr(next_weight), _ptr(next_bias), out.data_ptr(), _ptr(then),
+          _ptr(stats))
+    return (out, then, stats) if return_stats else (out, then)
+
+
+def dcn_residual_norm_backward_workspace_bytes(desc: ResidualDesc) -> int:
+    return _bytes("dcn_residual_norm_backward_workspace_bytes", desc)
+
+
+def dcn_residual_norm_backward(desc: ResidualDesc, x, branch, gate, scale, branch_weight, branch_bias, next_weight,
+                               stats, grad_out, grad_next, grad_x, grad_branch, grad_gate, grad_scale,
+                               grad_branch_weight, grad_branch_bias, grad_next_weight, grad_next_bias, workspace,
+                               workspace_bytes: int, stream=None) -> None:
+    """Raw call: tensors (or integer device addresses) laid out as dcn.h states; any gradient may be
+    None (not computed)."""
+    _raw("dcn_residual_norm_backward", ctypes.byref(desc),
+         *map(_ptr, (x, branch, gate, scale, branch_weight, branch_bias, next_weight, stats, grad_out, grad_next, grad_x,
+                     grad_branch, grad_gate, grad_scale, grad_branch_weight, grad_branch_bias, grad_next_weight,
+                     grad_next_bias, workspace)), workspace_bytes, _stream(stream))
+
+
+def residual_norm_backward(grad_out, grad_next, input, branch, stats, gate=None, scale=None, branch_norm="none",
+                           branch_weight=None, branch_bias=None, next_norm="layer", next_weight=None, next_bias=None,
+                           workspace=None):
+    """Gradients of residual_norm on the GPU from its inputs and stats and the upstream gradients grad_out
+    and grad_next of the input's shape (either may be None: zeros).  Returns (grad_input, grad_branch,
+    grad_gate, grad_scale, grad_branch_weight, grad_branch_bias, grad_next_weight, grad_next_bias), None for
+    what is None."""
+    _, desc, nbytes = _residual_key(input, branch, gate, scale, branch_norm, branch_weight, branch_bias, next_norm,
+                                    next_weight, next_bias, 0.0)
+    device, shape, dtype = input.device, input.shape, input.dtype
+    if grad_out is not None:
+        _check_out(grad_out, shape, dtype, device, "grad_out")
+    if grad_next is not None:
+        _check_out(grad_next, shape, dtype, device, "grad_next")
+    _check_out(stats, shape[:-1] + (4,), torch.float32, device, "stats")
+    gx, gy = torch.empty_like(input), torch.empty_like(input)
+    params = [None if t is None else torch.empty_like(t)
+              for t in (gate, scale, branch_weight, branch_bias, next_weight, next_bias)]
+    if nbytes or workspace is not None:
+        workspace = _workspace(workspace, nbytes, device)
+    _call("dcn_residual_norm_backward", device, desc, input.data_ptr(), branch.data_ptr(), _ptr(gate), _ptr(scale),
+          _ptr(branch_weight), _ptr(branch_bias), _ptr(next_weight), stats.data_ptr(), _ptr(grad_out), _ptr(grad_next),
+          gx.data_ptr(), gy.data_ptr(), *map(_ptr, params), workspace.data_ptr() if nbytes else None, nbytes)
+    return gx, gy, *params
+
+
+def _pages(key_pages, value_pages, table, B, written=False):
+    """Shapes and strides of a paged cache and its table."""
+    kshape, ks = _heads("key_pages", key_pages)
+    vshape, vs = _heads("value_pages", value_pages, key_pages)
+    if vshape != kshape:
+        raise ValueError(f"value_pages {tuple(vshape)} must have key_pages' shape {tuple(kshape)}")
+    if kshape[1] < 1 or kshape[2] < 1:
+        raise ValueError("pages must hold one position and one key head at least")
+    if written:
+        for name, strides in (("key_pages", ks), ("value_pages", vs)):
+            if any(n > 1 and s == 0 for n, s in zip(kshape, strides)):
+                raise ValueError(f"{name} must have a place of its own for every row, got strides {strides}")
+    shape, stride, dtype, device = table
+    if dtype != torch.int32 or len(shape) != 2 or shape[0] != B or device != key_pages[3] or \
+            (shape[1] > 1 and stride[1] != 1):
+        raise ValueError(f"page_table must be an int32 tensor [{B}, pages] on {key_pages[3]}, a sequence's entries adjacent")
+    return kshape, ks, vs, shape[1], stride[0]
+
+
+def _counts(name, look, B, device):
+    shape, stride, dtype, at = look
+    if dtype != torch.int32 or shape != (B,) or at != device or (B > 1 and stride != (1,)):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {B} sequences on {device}")
+
+
+@functools.lru_cache(maxsize=256)
+def _append_plan(key, value, key_pages, value_pages, table, starts, counts, query, positions, frequencies, sections,
+                 layout):
+    dtype, device = _element_type(key[2]), key[3]
+    shape, ks = _heads("key", key)
+    B, L, H, D = shape
+    vshape, vs = _heads("value", value, key)
+    if vshape != shape:
+        raise ValueError(f"value {tuple(vshape)} must have key's shape {tuple(shape)}")
+    _heads("key_pages", key_pages, key)
+    kshape, kps, vps, width, ts = _pages(key_pages, value_pages, table, B, written=True)
+    if kshape[2:] != shape[2:]:
+        raise ValueError(f"key {tuple(shape)} does not match key_pages {tuple(kshape)}")
+    _counts("starts", starts, B, device)
+    if counts is not None:
+        _counts("counts", counts, B, device)
+    Hq, qs = 0, (0, 0, 0)
+    if query is not None:
+        qshape, qs = _heads("query", query, key)
+        Hq = qshape[2]
+        if qshape[:2] != shape[:2] or qshape[3] != D or Hq < 1:
+            raise ValueError(f"query {tuple(qshape)} does not match key {tuple(shape)}")
+    rotation = (0, 0), 0, (), 0, 1
+    if frequencies is not None:
+        rotation = _rotation(positions, frequencies, sections, layout, B, L, device)
+        if 2 * sum(sections) > D:
+            raise ValueError(f"{sum(sections)} pairs do not fit heads of {D} elements")
+    elif positions is not None or sections:
+        raise ValueError("positions and sections need frequencies")
+    ps, axes, sections, kind, ptype = rotation
+    desc = AppendDesc(B, L, Hq, H, D, kshape[0], kshape[1], width, _I64x3(*qs), _I64x3(*ks), _I64x3(*vs), _I64x3(*kps),
+                      _I64x3(*vps), ts, _I64x2(*ps), axes, _I32x4(*sections), kind, ptype, dtype)
+    return desc, ctypes.byref(desc)
+
+
+def append_desc(key, value, key_pages, value_pages, page_table, starts, counts=None, query=None, positions=None,
+                frequencies=None, sections=(), layout="halves") -> AppendDesc:
+    """Descriptor of an append to a paged cache, for the raw entry points."""
+    return _append_plan(*map(_look, (key, value, key_pages, value_pages, page_table, starts, counts, query, positions,
+                                     frequencies)), tuple(map(int, sections)), layout)[0]
+
+
+def dcn_paged_append(desc: AppendDesc, q, k, v, positions, frequencies, page_table, starts, counts, q_out, key_pages,
+                     value_pages, lengths, stream=None) -> None:
+    """Raw call: tensors (or integer device addresses) laid out as dcn.h states."""
+    _raw("dcn_paged_append", ctypes.byref(desc), *map(_ptr, (q, k, v, positions, frequencies, page_table, starts, counts,
+                                                             q_out, key_pages, value_pages, lengths)), _stream(stream))
+
+
+def paged_append(key, value, key_pages, value_pages, page_table, starts, counts=None, query=None, positions=None,
+                 frequencies=None, sections=(), layout="halves"):
+    """Appends new keys and values to a paged cache on the GPU, rotated on the way: rows i < counts[b] (all L
+    for None) of key and value [B,L,Hkv,D] become positions starts[b] + i of sequence b, in key_pages and
+    value_pages [pages, page_size, Hkv, D] (written in place; any strides with adjacent elements of a
+    head) where page_table [B, n] (int32) says: position s is row s % page_size of page
+    page_table[b, s // page_size].  starts and counts [B] int32.  With frequencies keys are rotated as
+    rotary_positions does, by `positions` [B,L,axes] or, for None, by starts[b] + i on every axis; query
+    [B,L,Hq,D] too.  Positions outside the table, or whose entry is no page, are not written.
+    Returns lengths [B] (starts + counts), or (lengths, rotated query)."""
+    _, desc = _append_plan(_look(key), _look(value), _look(key_pages), _look(value_pages), _look(page_table),
+                           _look(starts), _look(counts), _look(query), _look(positions), _look(frequencies),
+                           tuple(map(int, sections)), layout)
+    device = key.device
+    lengths = torch.empty_like(starts)
+    out = None if query is None else torch.empty(query.shape, dtype=query.dtype, device=device)
+    _call("dcn_paged_append", device, desc, _ptr(query), key.data_ptr(), value.data_ptr(), _ptr(positions),
+          _ptr(frequencies), page_table.data_ptr(), starts.data_ptr(), _ptr(counts), _ptr(out), key_pages.data_ptr(),
+          value_pages.data_ptr(), lengths.data_ptr())
+    return lengths if query is None else (lengths, out)
+
+
+@functools.lru_cache(maxsize=256)
+def _paged_plan(query, key_pages, value_pages, table, lengths, scale):
+    shape, stride, tdtype, device = query
+    dtype = _element_type(tdtype)
+    if len(shape) != 3 or device.type != "cuda" or (shape[2] > 1 and stride[2] != 1):
+        raise ValueError("query must be a GPU tensor [B,Hq,D], the elements of a head adjacent")
+    _heads("key_pages", key_pages, query)
+    kshape, ks, vs, width, ts = _pages(key_pages, value_pages, table, shape[0])
+    B, Hq, D = shape
+    if kshape[3] != D or Hq < 1 or Hq % kshape[2] != 0:
+        raise ValueError(f"query {tuple(shape)} does not match key_pages {tuple(kshape)}")
+    _counts("lengths", lengths, B, device)
+    desc = PagedDesc(B, Hq, kshape[2], D, kshape[0], kshape[1], width, _I64x2(*stride[:2]), _I64x3(*ks), _I64x3(*vs), ts,
+                     (D or 1) ** -0.5 if scale is None else scale, dtype)
+    return desc, ctypes.byref(desc), _bytes("dcn_paged_attention_workspace_bytes", desc)
+
+
+def paged_desc(query, key_pages, value_pages, page_table, lengths, scale=None) -> PagedDesc:
+    """Descriptor of an attention to a paged cache, for the raw entry points."""
+    return _paged_plan(_look(query), _look(key_pages), _look(value_pages), _look(page_table), _look(lengths),
+                       None if scale is None else float(scale))[0]
+
+
+def dcn_paged_attention_workspace_bytes(desc: PagedDesc) -> int:
+    return _bytes("dcn_paged_attention_workspace_bytes", desc)
+
+
+def dcn_paged_attention(desc: PagedDesc, q, key_pages, value_pages, page_table, lengths, out, lse, workspace,
+                        workspace_bytes: int, stream=None) -> None:
+    """Raw call: tensors (or integer device addresses) laid out as dcn.h states."""
+    _raw("dcn_paged_attention", ctypes.byref(desc), *map(_ptr, (q, key_pages, value_pages, page_table, lengths, out, lse,
+                                                                workspace)), workspace_bytes, _stream(stream))
+
+
+def paged_attention(query, key_pages, value_pages, page_table, lengths, scale=None, return_lse=False, out=None,
+                    workspace=None):
+    """Attention of one new token of each sequence to a paged cache on the GPU: query [B,Hq,D] over the first
+    lengths[b] positions (int32, on the GPU) of key_pages and value_pages [pages, page_size, Hkv, D] (Hkv
+    divides Hq) that page_table [B, n] (int32) names, softmax of scale * q.k (1/sqrt(D) by default).
+    float32 or bfloat16, D <= 128.  Positions whose entry is no page are left out; a sequence without a
+    position gives zeros.  Returns out [B,Hq,D], or (out, lse) with lse [B,Hq] float32."""
+    _, desc, nbytes = _paged_plan(_look(query), _look(key_pages), _look(value_pages), _look(page_table), _look(lengths),
+                                  None if scale is None else float(scale))
+    device = query.device
+    if out is None:
+        out = torch.empty(query.shape, dtype=query.dtype, device=device)
+    else:
+        _check_out(out, query.shape, query.dtype, device)
+    lse = torch.empty(query.shape[:2], dtype=torch.float32, device=device) if return_lse else None
+    if nbytes or workspace is not None:
+        workspace = _workspace(workspace, nbytes, device)
+    _call("dcn_paged_attention", device, desc, query.data_ptr(), key_pages.data_ptr(), value_pages.data_ptr(),
+          page_table.data_ptr(), lengths.data_ptr(), out.data_ptr(), _ptr(lse), workspace.data_ptr() if nbytes else None,
+          nbytes)
+    return (out, lse) if return_lse else out

@@ -392,6 +392,159 @@ int dcn_group_norm_backward(const dcn_norm_desc* desc, const void* x, const void
                             void* grad_weight, void* grad_bias, void* workspace, size_t workspace_bytes,
                             hipStream_t stream);
 
+/* Rotary positions with several axes: where a row stands (the row and column of a map's position, the
+ * frame of a clip, the index of a token) enters queries and keys as rotations of pairs of their elements.
+ * pairs = sections[0] + .. + sections[axes-1]; pair p (axis a of the section it lies in) of every head of
+ * row (b, l) turns by the angle t = positions[b][l][a] * frequencies[p]:
+ *   out1 = x1 cos t - x2 sin t,  out2 = x2 cos t + x1 sin t
+ * where its elements x1, x2 are (p, p + pairs) for DCN_ROTARY_HALVES, (2p, 2p + 1) for
+ * DCN_ROTARY_ADJACENT, and for DCN_ROTARY_BLOCKS axis a's 2 sections[a] adjacent elements are taken by
+ * halves on their own.  Elements from 2 pairs on are copied.
+ *  - x [B][L][H][D] of desc->dtype: elements of a head adjacent, the strides of batch, position and head
+ *    (elements, >= 0) the descriptor's; out dense, and it may be x where that is dense.  positions
+ *    [B][L][axes] of position_type, axes adjacent, strides of batch and position the descriptor's (0
+ *    repeats); frequencies [pairs] float32, radians a unit of position.
+ *  - Arithmetic: angles and their reduction in 64 bits, so that far positions keep their digits (an angle
+ *    is off by 2^-51 of itself, 5e-7 at 2^30); cosines and sines are within 2^-23, products and sums in
+ *    fp32, out rounded once.
+ *  - Rows are read 16, 8, 4 bytes or an element at a time, the widest that fits the addresses, strides,
+ *    pairs (for BLOCKS each section) and head_dim.
+ * DCN_E_ARG: an invalid descriptor (a negative size or stride, no head, axes outside 1 .. 4, a section
+ * below 1, 2 pairs > head_dim, an unknown layout or position type) or a NULL required pointer;
+ * DCN_E_UNSUPPORTED: another dtype, head_dim above 65536 or 2^31 rows of heads; DCN_E_HIP as elsewhere;
+ * all checked before any launch.  batch or length 0: nothing is launched. */
+enum dcn_rotary_layout { DCN_ROTARY_HALVES = 0, DCN_ROTARY_ADJACENT = 1, DCN_ROTARY_BLOCKS = 2 };
+enum dcn_position_type { DCN_POSITION_F32 = 0, DCN_POSITION_I32 = 1 };
+typedef struct dcn_rotary_desc {
+  int64_t batch, length, heads, head_dim;
+  int64_t x_stride[3];                        /* elements: batch, position, head */
+  int64_t position_stride[2];                 /* elements: batch, position */
+  int32_t axes;
+  int32_t sections[4];                        /* pairs of each axis; those from `axes` on are not read */
+  int32_t layout;                             /* enum dcn_rotary_layout */
+  int32_t position_type;                      /* enum dcn_position_type */
+  int32_t dtype;                              /* enum dcn_dtype */
+} dcn_rotary_desc;
+int dcn_rotary(const dcn_rotary_desc* desc, const void* x, const void* positions, const float* frequencies,
+               void* out, hipStream_t stream);
+
+/* Gradients of dcn_rotary for the upstream gradient grad_out [B][L][H][D] (dense): grad_x (dense, may be
+ * grad_out) in desc->dtype, and where grad_positions is not NULL the gradient of every position, [B][L][axes]
+ * float32 dense (fractional positions, such as a detector's reference points, are learnt; an input repeated
+ * by a stride of 0 gets the gradient of every repetition), which takes x too (NULL otherwise).  grad_x may
+ * be NULL.  Sums over heads and pairs in fp32 in a fixed order.  Errors as for dcn_rotary. */
+int dcn_rotary_backward(const dcn_rotary_desc* desc, const void* grad_out, const void* positions,
+                        const float* frequencies, const void* x, void* grad_x, float* grad_positions,
+                        hipStream_t stream);
+
+/* What lies between two blocks of a decoder or encoder layer, in one pass: the norm after a block, its
+ * gate and residual scale, the residual sum, and the norm before the next block.  x (the stream) and branch
+ * (the block's output) [B][P][C]; for each row, N a norm over its C channels:
+ *   out  = x + gate scale (N(branch) branch_weight + branch_bias)
+ *   next = N(out) next_weight + next_bias         (from out before its rounding to dtype)
+ * Norms: DCN_NORM_NONE, DCN_NORM_RMS x / sqrt(mean x^2 + eps), DCN_NORM_LAYER (x - mean) / sqrt(var + eps)
+ * (var over C values).  next_norm NONE: next is not written (and may be NULL).  gate: DCN_GATE_NONE,
+ * DCN_GATE_BATCH [B][C], DCN_GATE_FULL [B][P][C].  scale, weights and biases [C], NULL for 1 and 0; those of
+ * a norm that is NONE are not read.  stats [B][P][4] float32 where not NULL: mean and 1 / deviation of the
+ * branch's row, then of out's (0 and 1 where there is none), which the backward takes.  Everything is dense
+ * in desc->dtype; out may be x or branch, next may be branch (out and next differ).  Arithmetic: fp32, the
+ * variance about the mean, out and next rounded once.  Rows are read 16, 4 bytes (fp32: 16, 8) or an
+ * element at a time, the widest that fits C and the addresses.
+ * DCN_E_ARG: an invalid descriptor (a negative size, no channel, eps negative or not finite, an unknown
+ * norm or gate) or a NULL required pointer; DCN_E_UNSUPPORTED: another dtype, more than 8192 channels,
+ * 2^31 rows, or 65536 batch elements with DCN_GATE_BATCH; DCN_E_HIP as elsewhere; all checked before any
+ * launch.  No rows: nothing is launched. */
+enum dcn_row_norm { DCN_NORM_NONE = 0, DCN_NORM_RMS = 1, DCN_NORM_LAYER = 2 };
+enum dcn_gate { DCN_GATE_NONE = 0, DCN_GATE_BATCH = 1, DCN_GATE_FULL = 2 };
+typedef struct dcn_residual_desc {
+  int64_t batch, positions, channels;
+  float eps;
+  int32_t branch_norm, next_norm;             /* enum dcn_row_norm */
+  int32_t gate;                               /* enum dcn_gate */
+  int32_t dtype;                              /* enum dcn_dtype */
+  int32_t reserved;                           /* 0 */
+} dcn_residual_desc;
+int dcn_residual_norm(const dcn_residual_desc* desc, const void* x, const void* branch, const void* gate,
+                      const void* scale, const void* branch_weight, const void* branch_bias,
+                      const void* next_weight, const void* next_bias, void* out, void* next, float* stats,
+                      hipStream_t stream);
+
+/* Gradients of dcn_residual_norm for the upstream gradients grad_out and grad_next [B][P][C], from the
+ * forward's inputs and stats.  grad_out NULL: zeros; grad_next is not read where next_norm is NONE, and NULL
+ * is zeros otherwise.  Writes grad_x and grad_branch [B][P][C], grad_gate (of gate's shape), and grad_scale,
+ * grad_branch_weight, grad_branch_bias, grad_next_weight, grad_next_bias [C], in desc->dtype.  Any gradient
+ * pointer may be NULL (not computed); the gradient of a weight that is NULL is that at 1; grad_branch_weight
+ * and _bias need a branch norm, grad_next_weight and _bias a next norm, grad_gate a gate (else DCN_E_ARG).
+ * grad_x may be grad_out, grad_branch grad_next.  Sums over rows in fp32 in a fixed order (no atomics); the
+ * workspace (256-byte aligned) holds their parts.  No rows: the parameters' gradients are zeros.  Errors as
+ * for dcn_residual_norm, DCN_E_WORKSPACE as elsewhere. */
+int dcn_residual_norm_backward_workspace_bytes(const dcn_residual_desc* desc, size_t* bytes);
+int dcn_residual_norm_backward(const dcn_residual_desc* desc, const void* x, const void* branch, const void* gate,
+                               const void* scale, const void* branch_weight, const void* branch_bias,
+                               const void* next_weight, const float* stats, const void* grad_out,
+                               const void* grad_next, void* grad_x, void* grad_branch, void* grad_gate,
+                               void* grad_scale, void* grad_branch_weight, void* grad_branch_bias,
+                               void* grad_next_weight, void* grad_next_bias, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream);
+
+/* A cache of keys and values in pages, for decoders that answer token by token.  key_pages and value_pages
+ * [num_pages][page_size][Hkv][D] of desc->dtype, elements of a head adjacent, the strides of page, position
+ * and head (elements, >= 0) the descriptor's, so that heads may come first within a page and keys and values
+ * may share one allocation.  page_table [B][max_pages] int32 (table_stride elements between sequences):
+ * position s of sequence b is row s % page_size of page page_table[b][s / page_size].
+ *
+ * dcn_paged_append: rows i < counts[b] (every i < length when counts is NULL; counts are taken as at most
+ * length) of k and v [B][length][Hkv][D] become positions starts[b] + i of sequence b; keys are rotated on
+ * the way as dcn_rotary does, with the positions given, or starts[b] + i on every axis when positions is NULL.
+ * query_heads > 0: q [B][length][Hq][D] is rotated the same way into q_out (dense; every row, those at and
+ * behind counts[b] too).  axes 0: nothing is rotated.  lengths [B] int32 where not NULL: starts[b] + counts[b]
+ * (it may not be starts or counts).  A position outside the table, or whose table entry is no page of the
+ * cache, is not written; other rows of the cache are left as they are.  Two positions that name one row of
+ * the cache leave either's elements there.  Arithmetic and reads as for dcn_rotary; values are copied.
+ * DCN_E_ARG, DCN_E_UNSUPPORTED (also max_pages * page_size beyond 2^31 - 1, num_pages beyond it), DCN_E_HIP
+ * as for dcn_rotary.  batch 0: nothing is launched. */
+typedef struct dcn_append_desc {
+  int64_t batch, length;
+  int64_t query_heads, key_heads, head_dim;   /* query_heads 0: no queries */
+  int64_t num_pages, page_size, max_pages;
+  int64_t q_stride[3], k_stride[3], v_stride[3];                /* elements: batch, position, head */
+  int64_t key_page_stride[3], value_page_stride[3];             /* elements: page, position, head */
+  int64_t table_stride;                                         /* elements: batch */
+  int64_t position_stride[2];                                   /* elements: batch, position */
+  int32_t axes;                               /* 0 .. 4 */
+  int32_t sections[4];
+  int32_t layout, position_type;
+  int32_t dtype;
+} dcn_append_desc;
+int dcn_paged_append(const dcn_append_desc* desc, const void* q, const void* k, const void* v,
+                     const void* positions, const float* frequencies, const int32_t* page_table,
+                     const int32_t* starts, const int32_t* counts, void* q_out, void* key_pages,
+                     void* value_pages, int32_t* lengths, hipStream_t stream);
+
+/* dcn_paged_attention: one new token of each sequence attends to the first lengths[b] positions of its
+ * pages, with dcn_cross_attention's formulas: q [B][Hq][D] (elements of a head adjacent, strides of batch and
+ * head the descriptor's), Hkv divides Hq, out [B][Hq][D] dense in desc->dtype, lse [B][Hq] float32 or NULL.
+ * lengths [B] int32 on the device, taken as 0 .. max_pages * page_size.  Positions whose table entry is no
+ * page of the cache are left out; a sequence with no position left gets zeros and lse -infinity.  What the
+ * cache holds behind a sequence's length, infinities and NaN included, does not matter.  Long sequences are
+ * split over workgroups by the lengths on the device, and the parts joined in order: equal calls give equal
+ * bits.  Arithmetic as for dcn_cross_attention.  The workspace (256-byte aligned) holds the parts.
+ * DCN_E_ARG, DCN_E_UNSUPPORTED (head_dim > 128, sizes as for dcn_paged_append), DCN_E_WORKSPACE, DCN_E_HIP
+ * as for dcn_cross_attention.  batch 0: nothing is launched. */
+typedef struct dcn_paged_desc {
+  int64_t batch, query_heads, key_heads, head_dim;
+  int64_t num_pages, page_size, max_pages;
+  int64_t q_stride[2];                                          /* elements: batch, head */
+  int64_t key_page_stride[3], value_page_stride[3];             /* elements: page, position, head */
+  int64_t table_stride;                                         /* elements: batch */
+  float scale;
+  int32_t dtype;
+} dcn_paged_desc;
+int dcn_paged_attention_workspace_bytes(const dcn_paged_desc* desc, size_t* bytes);
+int dcn_paged_attention(const dcn_paged_desc* desc, const void* q, const void* key_pages, const void* value_pages,
+                        const int32_t* page_table, const int32_t* lengths, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream);
+
 const char* dcn_status_str(int status);
 
 #ifdef __cplusplus
