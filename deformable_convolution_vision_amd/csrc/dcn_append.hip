@@ -2,10 +2,9 @@
 // and the rotation of the same tokens' queries.
 //
 // Row (b, i) of the new tokens is position s = starts[b] + i of its sequence: row s % page_size of
-// page page_table[b][s / page_size].  Queries, keys and values are one list of heads of that row: a
-// thread forms the angles of its chunk of pairs once and turns that chunk of several heads (values
-// are copied).  Nothing is read before the row's page is known but the row itself, whose loads
-// are under way while the start and the table entry are fetched.
+// page page_table[b][s / page_size].  Queries, keys and values are one list of heads of that row, of which
+// values are copied.  A workgroup's rows share their angles and places in the LDS; the elements' loads are
+// under way while starts, table entries and angles are found.
 //
 // A table entry that is no page of the cache, or a position outside the table, drops the row: the
 // check stands before the address is formed.
@@ -34,79 +33,94 @@ struct AppendArgs {
   int num_pages, page_size, max_pages;
 };
 
-constexpr int kHeads = 4;  // heads under way at a time
-
 template <typename T, int PV, bool ADJ>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
   using V = Vec<T, PV>;
-  const int tid = threadIdx.x, r = tid / a.cut.units, u0 = tid - r * a.cut.units;
-  const int64_t row = (a.first + blockIdx.x) * a.cut.rows + r;
-  if (r >= a.cut.rows || row >= a.rows) return;
-  const int b = static_cast<int>(row / a.per), i = static_cast<int>(row - static_cast<int64_t>(b) * a.per);
-  const int start = a.starts[b];
-  int count = a.L;
-  if (a.counts != nullptr) count = min(max(a.counts[b], 0), a.L);
-  if (i == 0 && u0 == 0 && a.lengths != nullptr) a.lengths[b] = start + count;
-  if (i >= a.L) return;
-  const int64_t s = static_cast<int64_t>(start) + i;
-  int page = -1, place = 0;
-  if (i < count && s >= 0 && s < static_cast<int64_t>(a.max_pages) * a.page_size) {
-    const int at = static_cast<int>(s) / a.page_size;
-    place = static_cast<int>(s) - at * a.page_size;
-    page = a.table[b * a.ts + at];
-  }
-  const bool kept = page >= 0 && page < a.num_pages;
-  const T* const qr = static_cast<const T*>(a.q) + b * a.qs[0] + i * a.qs[1];
-  const T* const kr = static_cast<const T*>(a.k) + b * a.ks[0] + i * a.ks[1];
-  const T* const vr = static_cast<const T*>(a.v) + b * a.vs[0] + i * a.vs[1];
-  T* const qo = static_cast<T*>(a.qo) + row * a.Hq * a.D;   // (rows are B * L here: per == L)
-  T* const ko = static_cast<T*>(a.kp) + (kept ? page * a.kps[0] + place * a.kps[1] : 0);
-  T* const vo = static_cast<T*>(a.vp) + (kept ? page * a.vps[0] + place * a.vps[1] : 0);
-  At at;
-  if (a.t.axes > 0 && a.t.positions != nullptr) {
-    at = at_row(a.t, b, i);
-  } else {
-    at.p0 = at.p1 = at.p2 = at.p3 = static_cast<double>(s);
-  }
-  const int heads = a.Hq + 2 * a.Hkv;
-  for (int u = u0; u < a.cut.units; u += 256) {
-    const int chunk = u % a.cut.chunks, group = u / a.cut.chunks;
-    const Place p = place_of<PV>(a.t, chunk, a.cut.rotated);
-    const bool turns = chunk < a.cut.rotated, second = p.e2 < a.D;
-    float c[PV], sn[PV];
-    if (turns) {
+  constexpr int kUnits = units_of(sizeof(V));
+  __shared__ float2 cs[kTurns];
+  __shared__ int pages[kRows], places[kRows];      // of the rows; page -1: the row has none
+  const int tid = threadIdx.x;
+  const int64_t at = a.first + blockIdx.x, row0 = at / a.cut.groups * a.cut.rows;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(a.cut.rows), a.rows - row0));
+  const int h0 = static_cast<int>(at % a.cut.groups) * a.cut.heads, heads = min(a.cut.heads, a.Hq + 2 * a.Hkv - h0);
+  const int units = a.L > 0 ? rows * static_cast<int>(a.cut.by_row.d) : 0;
+  const auto unit = [&](int u, int& r, int& h, int& chunk) {   // false: no unit
+    r = a.cut.by_row.of(u);
+    const int in_row = u - r * static_cast<int>(a.cut.by_row.d);
+    h = a.cut.by_chunks.of(in_row);
+    chunk = in_row - h * a.cut.chunks;
+    const bool live = u < units && h < heads;
+    h += h0;
+    return live;
+  };
+  V v1[kUnits], v2[kUnits];
+  const auto load = [&](int u0) {
 #pragma unroll
-      for (int j = 0; j < PV; ++j) cos_sin(at.of(a.t, chunk * PV + j), a.t.freq[chunk * PV + j], c[j], sn[j]);
+    for (int k = 0; k < kUnits; ++k) {
+      int r, h, chunk;
+      if (!unit(u0 + k * 256 + tid, r, h, chunk)) continue;
+      const uint32_t row = static_cast<uint32_t>(row0 + r), b = row / static_cast<uint32_t>(a.per), i = row - b * a.per;
+      const Place p = place_of<PV>(a.t, chunk, a.cut.rotated);
+      const T* x = h < a.Hq           ? static_cast<const T*>(a.q) + b * a.qs[0] + i * a.qs[1] + h * a.qs[2]
+                   : h < a.Hq + a.Hkv ? static_cast<const T*>(a.k) + b * a.ks[0] + i * a.ks[1] + (h - a.Hq) * a.ks[2]
+                                      : static_cast<const T*>(a.v) + b * a.vs[0] + i * a.vs[1] + (h - a.Hq - a.Hkv) * a.vs[2];
+      v1[k] = *reinterpret_cast<const V*>(x + p.e1);
+      if (p.e2 < a.D) v2[k] = *reinterpret_cast<const V*>(x + p.e2);
     }
-    for (int h0 = group; h0 < heads; h0 += kHeads * a.cut.groups) {
-      V v1[kHeads], v2[kHeads];
+  };
+  load(0);
+  for (int r = tid; r < rows; r += 256) {
+    const uint32_t row = static_cast<uint32_t>(row0 + r), b = row / static_cast<uint32_t>(a.per), i = row - b * a.per;
+    const int start = a.starts[b];
+    int count = a.L, page = -1, place = 0;
+    if (a.counts != nullptr) count = min(max(a.counts[b], 0), a.L);
+    if (i == 0 && h0 == 0 && a.lengths != nullptr) a.lengths[b] = start + count;
+    const int64_t s = static_cast<int64_t>(start) + i;
+    if (static_cast<int>(i) < count && s >= 0 && s < static_cast<int64_t>(a.max_pages) * a.page_size) {
+      const int n = static_cast<int>(s) / a.page_size;
+      place = static_cast<int>(s) - n * a.page_size;
+      page = a.table[b * a.ts + n];
+    }
+    pages[r] = page >= 0 && page < a.num_pages ? page : -1;
+    places[r] = place;
+  }
+  if (units == 0) return;
+  for (int i = tid; i < rows * a.t.pairs; i += 256) {
+    const int r = a.cut.by_pairs.of(i), pair = i - r * a.t.pairs;
+    const uint32_t row = static_cast<uint32_t>(row0 + r), b = row / static_cast<uint32_t>(a.per), l = row - b * a.per;
+    const double pos = a.t.positions != nullptr ? position_of(a.t, b, l, axis_of(a.t, pair))
+                                                : static_cast<double>(static_cast<int64_t>(a.starts[b]) + l);
+    float c, s;
+    cos_sin(pos, a.t.freq[pair], c, s);
+    cs[i] = make_float2(c, s);
+  }
+  __syncthreads();
+  for (int u0 = 0; u0 < units; u0 += kUnits * 256) {
+    if (u0 > 0) load(u0);
 #pragma unroll
-      for (int n = 0; n < kHeads; ++n) {
-        const int h = h0 + n * a.cut.groups;
-        if (h >= heads) break;
-        const T* x = h < a.Hq             ? qr + h * a.qs[2]
-                     : h < a.Hq + a.Hkv ? kr + (h - a.Hq) * a.ks[2]
-                                        : vr + (h - a.Hq - a.Hkv) * a.vs[2];
-        v1[n] = *reinterpret_cast<const V*>(x + p.e1);
-        if (second) v2[n] = *reinterpret_cast<const V*>(x + p.e2);
+    for (int k = 0; k < kUnits; ++k) {
+      int r, h, chunk;
+      if (!unit(u0 + k * 256 + tid, r, h, chunk)) continue;
+      const Place p = place_of<PV>(a.t, chunk, a.cut.rotated);
+      const int page = pages[r], place = places[r];
+      T* y = h < a.Hq           ? static_cast<T*>(a.qo) + ((row0 + r) * a.Hq + h) * a.D
+             : h < a.Hq + a.Hkv ? static_cast<T*>(a.kp) + page * a.kps[0] + place * a.kps[1] + (h - a.Hq) * a.kps[2]
+                                : static_cast<T*>(a.vp) + page * a.vps[0] + place * a.vps[1] + (h - a.Hq - a.Hkv) * a.vps[2];
+      if (chunk < a.cut.rotated && h < a.Hq + a.Hkv) {
+        float c[PV], s[PV], x1[PV], x2[PV], y1[PV], y2[PV];
+        const float2* turns = cs + r * a.t.pairs + chunk * PV;
+#pragma unroll
+        for (int j = 0; j < PV; ++j) {
+          c[j] = turns[j].x;
+          s[j] = turns[j].y;
+        }
+        pairs_of<T, PV, ADJ>(v1[k], v2[k], x1, x2);
+        turn<PV>(c, s, x1, x2, y1, y2);
+        vectors_of<T, PV, ADJ>(y1, y2, v1[k], v2[k]);
       }
-#pragma unroll
-      for (int n = 0; n < kHeads; ++n) {
-        const int h = h0 + n * a.cut.groups;
-        if (h >= heads) break;
-        T* y = h < a.Hq             ? qo + static_cast<int64_t>(h) * a.D
-               : h < a.Hq + a.Hkv ? ko + (h - a.Hq) * a.kps[2]
-                                  : vo + (h - a.Hq - a.Hkv) * a.vps[2];
-        if (turns && h < a.Hq + a.Hkv) {
-          float x1[PV], x2[PV], y1[PV], y2[PV];
-          pairs_of<T, PV, ADJ>(v1[n], v2[n], x1, x2);
-          turn<PV>(c, sn, x1, x2, y1, y2);
-          vectors_of<T, PV, ADJ>(y1, y2, v1[n], v2[n]);
-        }
-        if (h < a.Hq || kept) {
-          *reinterpret_cast<V*>(y + p.e1) = v1[n];
-          if (second) *reinterpret_cast<V*>(y + p.e2) = v2[n];
-        }
+      if (h < a.Hq || page >= 0) {
+        *reinterpret_cast<V*>(y + p.e1) = v1[k];
+        if (p.e2 < a.D) *reinterpret_cast<V*>(y + p.e2) = v2[k];
       }
     }
   }
@@ -140,7 +154,7 @@ int check(const dcn_append_desc* d) {
   if (d->dtype != DCN_F32 && d->dtype != DCN_BF16) return DCN_E_UNSUPPORTED;
   const double big = 2147483647.;
   const double heads = static_cast<double>(d->query_heads) + 2. * d->key_heads, length = d->length > 0 ? d->length : 1;
-  if (d->head_dim > 65536 || heads > big || d->batch > big || length > big || d->batch * length * heads > big ||
+  if (d->head_dim > 2 * kTurns || heads > big || d->batch > big || length > big || d->batch * length * heads > big ||
       d->num_pages > big || d->page_size > big || static_cast<double>(d->max_pages) * d->page_size > big)
     return DCN_E_UNSUPPORTED;
   return DCN_OK;
@@ -200,10 +214,10 @@ extern "C" int dcn_paged_append(const dcn_append_desc* d, const void* q, const v
   for (const void* p : {k, v, static_cast<const void*>(key_pages), static_cast<const void*>(value_pages)}) w = fit(w, es, p);
   for (const int64_t* s : {a.ks, a.vs, a.kps, a.vps}) w = fit(w, s, 3);
   if (a.Hq > 0) w = fit(fit(fit(w, es, q), es, q_out), a.qs, 3);
-  a.cut = cut_of(w, a.t.pairs, d->head_dim, a.rows, a.Hq + 2 * a.Hkv);
+  a.cut = cut_of(w, es, a.t.pairs, d->head_dim, a.rows, a.Hq + 2 * a.Hkv);
   void* args[] = {&a};
-  return launch(kernel_of(bf16, w, d->layout == DCN_ROTARY_ADJACENT), (a.rows + a.cut.rows - 1) / a.cut.rows, args,
-                &a.first, stream)
+  return launch(kernel_of(bf16, w, d->layout == DCN_ROTARY_ADJACENT),
+                (a.rows + a.cut.rows - 1) / a.cut.rows * a.cut.groups, args, &a.first, stream)
              ? DCN_OK
              : DCN_E_HIP;
 }

@@ -12,12 +12,17 @@
 // A wave takes blocks of 32 positions on its own: their keys come straight from memory as the first
 // product's operand, their values through registers and the wave's own part of the LDS, from where they are
 // read transposed.  A block's page entries are fetched two blocks ahead and its rows one block ahead, so
-// that a page's look-up is never waited for in line.  Pages of any size: each position has its own address.
+// that a page's look-up is never waited for in line.  Pages of any size: each position has its own address,
+// formed by one lane and handed to the lanes that load its row through the LDS.
 //
 // Lengths are known on the device only, so every workgroup derives from them which part it has
-// (parts_of): all sequences' steps are shared out evenly over as many workgroups as the chip
+// (share_of): the blocks of all sequences are dealt out evenly over as many workgroups as the chip
 // holds.  A sequence of one part is written as it is; others leave their parts (maximum, sum, undivided output),
 // which paged_join_kernel adds in order.
+//
+// Arithmetic: as dcn_attention.hip, but for bf16 the weights enter the second product as two operands, 2^-15
+// of the weight in all: the matrix units wait for memory here, and the output is then as near the exact one
+// as its own rounding.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -42,10 +47,14 @@ struct PagedArgs {
   int64_t qs[2], ks[3], vs[3], ts;
   int B, Hq, Hkv, g, D;
   int tiles;               // of 16 rows, of a key head
-  int num_pages, page_size, capacity;
-  int slots;               // parts of a key head's tile that the plan aims at
+  int num_pages, page_size, max_pages, capacity;
+  int split;               // whether sequences may have several parts
+  int aim;                 // parts of a key head's tile that the division aims at,
+  int least;               // of so many blocks at least
   int grid;                // workgroups of a key head's tile (the most parts that there can be)
-  int64_t first;           // workgroups of launches before this one
+  uint32_t first;          // workgroups of launches before this one
+  uint32_t page_m;         // position / page_size is the upper half of position * page_m, shifted by page_s
+  int page_s;              // (page_m 0: pages of one position)
   float c;                 // scale * log2(e)
 };
 
@@ -88,81 +97,112 @@ __device__ __forceinline__ float sum_of_4(float x) {
   return sum_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
-__device__ __forceinline__ int length_of(const PagedArgs& a, int b) { return min(max(a.lengths[b], 0), a.capacity); }
+// ---- which workgroup has what
 
-// Which part of which sequence workgroup `index` of a key head's tile has: a step is `keys` positions, and
-// a sequence of n steps has ceil(n / quota) parts, one at least.  quota: so many steps that all parts
-// fit `slots` (where there are sequences enough to fill the chip anyway, slots is more than it holds).
-// All lanes of a wave take part; b < 0: no part is left for this workgroup.
-struct Part {
-  int b, split, splits, per, steps;
-  int before;              // parts of the sequences before it
-};
-__device__ __forceinline__ int wave_sum(int v) {
-#pragma unroll
-  for (int w = 1; w < 64; w <<= 1) v += __shfl_xor(v, w, 64);
+__device__ __forceinline__ int length_of(const PagedArgs& a, int b) { return min(max(a.lengths[b], 0), a.capacity); }
+// blocks of sequence b0 + lane (0 where there is none)
+__device__ __forceinline__ int blocks_of(const PagedArgs& a, int b0) {
+  const int b = b0 + (threadIdx.x & 63);
+  return b < a.B ? (length_of(a, b) + kKeys - 1) / kKeys : 0;
+}
+__device__ __forceinline__ int parts_of(int blocks, int quota) { return max(1, (blocks + quota - 1) / quota); }
+
+// sums of the lanes up to each one
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int from_lane(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, ROWS == 0xf);
+}
+__device__ __forceinline__ int running_sum(int v) {
+  v += from_lane<0x111, 0xf>(v);     // 1, 2, 4, 8 lanes below, within 16
+  v += from_lane<0x112, 0xf>(v);
+  v += from_lane<0x114, 0xf>(v);
+  v += from_lane<0x118, 0xf>(v);
+  v += from_lane<0x142, 0xa>(v);     // the last lane of the 16 below
+  v += from_lane<0x143, 0xc>(v);     // of the 32 below
   return v;
 }
-__device__ __forceinline__ Part parts_of(const PagedArgs& a, int index, int keys) {
-  const int lane = threadIdx.x & 63;
-  int64_t total = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 64) {
-    int n = 0;
-    if (b0 + lane < a.B) n = (length_of(a, b0 + lane) + keys - 1) / keys;
-    total += wave_sum(n);
+__device__ __forceinline__ int lanes_total(int v) { return __builtin_amdgcn_readlane(running_sum(v), 63); }
+
+// Blocks of a part: the fewest with which all sequences together have at most `aim` parts (aim is at least
+// as many as there are sequences, so the search ends: it grows until one part holds the longest).  The same in all
+// workgroups of both launches.  mine: blocks_of(a, 0).
+__device__ __forceinline__ int quota_of(const PagedArgs& a, int mine) {
+  float total = 0.f;     // (as near as the search's first guess needs)
+  for (int b0 = 0; b0 < a.B; b0 += 64) total += static_cast<float>(lanes_total(b0 == 0 ? mine : blocks_of(a, b0)));
+  int quota = max(a.least, static_cast<int>(total / static_cast<float>(a.aim)));
+  while (true) {
+    int parts = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 64) {
+      const int n = b0 == 0 ? mine : blocks_of(a, b0);
+      parts += lanes_total(b0 + static_cast<int>(threadIdx.x & 63) < a.B ? parts_of(n, quota) : 0);
+    }
+    if (parts <= a.aim) return quota;
+    quota += max(1, quota / 16);
   }
-  const int quota = max(1, static_cast<int>((total + a.slots - 1) / a.slots));
-  Part p = {-1, 0, 1, quota, 0, 0};
+}
+
+// The part of workgroup `index` of a key head's tile: blocks first .. last - 1 of sequence b, one of `parts`
+// parts, which follow `before` parts of the sequences before it.  b < 0: no part is left for this workgroup.
+struct Share {
+  int b, first, last, parts, number;
+};
+__device__ __forceinline__ Share share_of(const PagedArgs& a, int index) {
+  if (a.split == 0) return {index, 0, (length_of(a, index) + kKeys - 1) / kKeys, 1, index};
+  const int lane = threadIdx.x & 63, mine = blocks_of(a, 0), quota = quota_of(a, mine);
   int before = 0;
   for (int b0 = 0; b0 < a.B; b0 += 64) {
-    int n = 0, mine = 0;
-    if (b0 + lane < a.B) {
-      n = (length_of(a, b0 + lane) + keys - 1) / keys;
-      mine = max(1, (n + quota - 1) / quota);
-    }
-    int upto = mine;       // parts of this chunk's sequences up to this one
-#pragma unroll
-    for (int w = 1; w < 64; w <<= 1) {
-      const int v = __shfl_up(upto, w, 64);
-      if (lane >= w) upto += v;
-    }
-    const int at = index - before;
-    const uint64_t hit = __ballot(at < upto && at >= upto - mine && mine > 0);
+    const int n = b0 == 0 ? mine : blocks_of(a, b0), parts = b0 + lane < a.B ? parts_of(n, quota) : 0;
+    const int upto = running_sum(parts), at = index - before;
+    const uint64_t hit = __ballot(at < upto && at >= upto - parts);
     if (hit != 0) {
-      const int who = __builtin_ctzll(hit);
-      const int end = __builtin_amdgcn_readlane(upto, who), have = __builtin_amdgcn_readlane(mine, who);
-      p.b = b0 + who;
-      p.splits = have;
-      p.split = at - (end - have);
-      p.steps = __builtin_amdgcn_readlane(n, who);
-      p.before = before + end - have;
-      return p;
+      const int who = __builtin_ctzll(hit), blocks = __builtin_amdgcn_readlane(n, who),
+                have = __builtin_amdgcn_readlane(parts, who), part = at - (__builtin_amdgcn_readlane(upto, who) - have);
+      const int first = part * quota;
+      return {b0 + who, first, min(blocks, first + quota), have, index};
     }
     before += __builtin_amdgcn_readlane(upto, 63);
   }
-  return p;
+  return {-1, 0, 0, 1, index};
 }
 
 __device__ uint4 paged_zero_row[32];   // what positions without a row read: 512 bytes, a row of 128 fp32
 
-template <typename T, int DP, int W, bool VEC>
+// How rows are read: 16 bytes at a time and no wider than they are (the head is the padded one), 16 bytes at a
+// time where they have them, or element by element.
+enum Rows { kWhole, kVectors, kElements };
+
+template <typename T, int DP, int W, Rows ROWS>
 __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
   constexpr int DT = DP / 16, KS = DP / 32, VPR = DP * static_cast<int>(sizeof(T)) / 16, VL = kKeys * VPR / 64, KV = Elem<T>::kVec;
+  constexpr int CD = DT / 2;                                     // columns of 16 elements that are joined at a time
   constexpr int OST = 20;                                        // row of the join's tile of 16 rows x 16, padded
-  constexpr int kLds = W * kKeys * DP * static_cast<int>(sizeof(T)), kJoin = (W * 16 * OST + 2 * W * 16) * 4;
+  constexpr int kLds = W * kKeys * DP * static_cast<int>(sizeof(T)), kJoin = (CD * W * 16 * OST + 2 * W * 16) * 4;
   __shared__ __attribute__((aligned(16))) unsigned char smem[kLds > kJoin ? kLds : kJoin];
+  __shared__ ulonglong2 rows[W][kKeys];                          // addresses of a block's keys and values
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, quad = lane >> 4,
             wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t at = a.first + blockIdx.x;
-  const int heads = a.Hkv * a.tiles, ht = static_cast<int>(at % heads), hk = ht / a.tiles, tile = ht % a.tiles;
-  const Part part = parts_of(a, static_cast<int>(at / heads), kKeys * W);
+  const uint32_t at = a.first + blockIdx.x, heads = a.Hkv * a.tiles, index = at / heads, ht = at - index * heads;
+  const int hk = ht / a.tiles, tile = ht - hk * a.tiles;
+  const Share part = share_of(a, index);
   if (part.b < 0) return;
   const int length = length_of(a, part.b);
-  const int s0 = part.split * part.per, s1 = min(part.steps, s0 + part.per);
   T* const lds = reinterpret_cast<T*>(smem) + wave * kKeys * DP;
   const int32_t* table = a.table + part.b * a.ts;
   const T* const kp = static_cast<const T*>(a.k) + hk * a.ks[2];
   const T* const vp = static_cast<const T*>(a.v) + hk * a.vs[2];
+
+  // Where position `lane % 32` of a block lies: its page (-1: none) and its place there.
+  struct Where {
+    int page, place;
+  };
+  const auto entry = [&](int block) {
+    const int key = block * kKeys + (lane & 31), n = a.page_m == 0 ? key : static_cast<int>(__umulhi(key, a.page_m) >> a.page_s);
+    int page = -1;
+    if (n < a.max_pages) page = table[n];      // (not held up by the length, which the first block's is fetched with)
+    if (block >= part.last || key >= length) page = -1;
+    return Where{page, key - n * a.page_size};
+  };
+  Where next = entry(part.first + wave);
 
   // the query head of this lane's column
   const int row = tile * 16 + col;
@@ -174,59 +214,55 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
     for (int i = 0; i < KS; ++i)
 #pragma unroll
       for (int h = 0; h < 8 / KV; ++h) {
-        const uint4 u = load_vec<T, VEC>(qp, 0, 32 * i + 8 * quad + KV * h, a.D, live).u;
+        const uint4 u = load_vec<T, ROWS != kElements>(qp, 0, 32 * i + 8 * quad + KV * h, a.D, live).u;
         __builtin_memcpy(reinterpret_cast<char*>(&qf[i]) + 16 * h, &u, 16);
       }
   }
 
-  // Block i of this wave: positions (s0 + i) * 32 W + 32 wave ...  Lane j < 32 (and j + 32) holds the page of position j.
-  const auto entry = [&](int step) {
-    const int key = (step * W + wave) * kKeys + (lane & 31);
-    return step < s1 && key < length ? table[key / a.page_size] : -1;
-  };
   Frag<T> kf[2][KS];
   Vec16<T> vf[VL];
   uint32_t kept = 0;   // of the block in kf, vf: positions that count
   const T* const zeros = reinterpret_cast<const T*>(paged_zero_row);
-  const auto fetch = [&](int step, int page) {
-    const int k0 = (step * W + wave) * kKeys, key = k0 + (lane & 31);
-    const bool in = page >= 0 && page < a.num_pages;     // (an entry is only read for positions that exist)
-    kept = static_cast<uint32_t>(__ballot(in));
-    const int place = key - key / a.page_size * a.page_size;
+  // 16 bytes of a row from element d on; zeros beyond D
+  const auto take = [&](const T* r, int d) {
+    if constexpr (ROWS == kWhole) return load16(r + d);
+    if constexpr (ROWS == kVectors) return load16(d < a.D ? r + d : zeros);
+    return load_vec<T, false>(r, 0, d, a.D, true).u;
+  };
+  const auto fetch = [&](const Where& w) {
+    const bool ok = w.page >= 0 && w.page < a.num_pages;
+    kept = static_cast<uint32_t>(__ballot(ok));
+    wave_order();
+    if (lane < kKeys)
+      rows[wave][lane] = make_ulonglong2(
+          reinterpret_cast<uint64_t>(ok ? kp + w.page * a.ks[0] + w.place * a.ks[1] : zeros),
+          reinterpret_cast<uint64_t>(ok ? vp + w.page * a.vs[0] + w.place * a.vs[1] : zeros));
+    wave_order();
+    const T *kr[2], *vr[VL];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int j = 16 * t + col, pg = __shfl(page, j, 64), pl = __shfl(place, j, 64);
-      const bool ok = (kept >> j) & 1u;
-      const T* r = kp + (ok ? pg * a.ks[0] + pl * a.ks[1] : 0);
+    for (int t = 0; t < 2; ++t) kr[t] = reinterpret_cast<const T*>(rows[wave][16 * t + col].x);
+#pragma unroll
+    for (int n = 0; n < VL; ++n) vr[n] = reinterpret_cast<const T*>(rows[wave][(n * 64 + lane) / VPR].y);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int i = 0; i < KS; ++i)
 #pragma unroll
         for (int h = 0; h < 8 / KV; ++h) {
-          const int d = 32 * i + 8 * quad + KV * h;
-          uint4 u;
-          if (VEC) u = load16(ok && d < a.D ? r + d : zeros);
-          else u = load_vec<T, false>(r, 0, d, a.D, ok).u;
+          const uint4 u = take(kr[t], 32 * i + 8 * quad + KV * h);
           __builtin_memcpy(reinterpret_cast<char*>(&kf[t][i]) + 16 * h, &u, 16);
         }
-    }
 #pragma unroll
-    for (int n = 0; n < VL; ++n) {
-      const int j = (n * 64 + lane) / VPR, d = (n * 64 + lane) % VPR * KV, pg = __shfl(page, j, 64), pl = __shfl(place, j, 64);
-      const bool ok = (kept >> j) & 1u;
-      const T* r = vp + (ok ? pg * a.vs[0] + pl * a.vs[1] : 0);
-      if (VEC) vf[n].u = load16(ok && d < a.D ? r + d : zeros);
-      else vf[n] = load_vec<T, false>(r, 0, d, a.D, ok);
-    }
+    for (int n = 0; n < VL; ++n) vf[n].u = take(vr[n], (n * 64 + lane) % VPR * KV);
   };
 
   f32x4 o[DT];
 #pragma unroll
   for (int i = 0; i < DT; ++i) o[i] = zero_acc4();
   float m = kNegInf, l = 0.f;
-  int next = entry(s0);
-  fetch(s0, next);
-  next = entry(s0 + 1);
-  for (int step = s0; step < s1; ++step) {
+  fetch(next);
+  next = entry(part.first + wave + W);
+  for (int block = part.first + wave; block < part.last; block += W) {
     // this block's scores; its values move to the LDS
     f32x4 s[2];
 #pragma unroll
@@ -243,15 +279,15 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
     }
     wave_order();
     const uint32_t word = kept;
-    if (step + 1 < s1) fetch(step + 1, next);
-    next = entry(step + 2);
+    if (block + W < part.last) fetch(next);
+    next = entry(block + 2 * W);
     if (word != 0) {
       float mt = kNegInf;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          if (!((word >> (16 * t + 4 * quad + r)) & 1u)) s[t][r] = kNegInf;
+          if (word != 0xffffffffu && !((word >> (16 * t + 4 * quad + r)) & 1u)) s[t][r] = kNegInf;
           mt = fmaxf(mt, s[t][r]);
         }
       mt = max_of_4(mt) * a.c;
@@ -275,9 +311,16 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
         }
       if constexpr (sizeof(T) == 2) {
         typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-        Frag<T> pf;
+        // A weight as two operands: its upper 16 bits, lowered a little first so that something is left, and the
+        // rest, rounded (2^-15 of the weight).  Both are positive, for a rest of 0 or below would make an infinite
+        // value's product NaN.
+        Frag<T> pf, pr;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) pf.w[j] = pack_bf16(p[2 * j], p[2 * j + 1]);
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t h0 = __float_as_uint(p[2 * j] * 0.9921875f), h1 = __float_as_uint(p[2 * j + 1] * 0.9921875f);
+          pf.w[j] = __builtin_amdgcn_perm(h1, h0, 0x07060302);
+          pr.w[j] = pack_bf16(p[2 * j] - __uint_as_float(h0 & 0xffff0000u), p[2 * j + 1] - __uint_as_float(h1 & 0xffff0000u));
+        }
 #pragma unroll
         for (int i = 0; i < DT; ++i) {
           Frag<T> vt;
@@ -286,6 +329,7 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
             vt.s[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                 (lds_s16x4*)(lds + Tile<T, DP>::at(16 * t + 4 * quad + (col >> 2), 16 * i + 4 * (col & 3))));
           o[i] = mma16(vt, pf, o[i]);
+          o[i] = mma16(vt, pr, o[i]);
         }
       } else {
 #pragma unroll
@@ -301,24 +345,26 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
   }
   l = sum_of_4(l);
 
-  // the waves' parts of the 16 rows, 16 elements of the head at a time
-  float* const os = reinterpret_cast<float*>(smem);              // [W][16][OST]
-  float* const fs = os + W * 16 * OST;                           // [W][16] maxima
+  // the waves' parts of the 16 rows, CD columns of 16 elements of the head at a time: 64 threads for each column
+  float* const os = reinterpret_cast<float*>(smem);              // [CD][W][16][OST]
+  float* const fs = os + CD * W * 16 * OST;                      // [W][16] maxima
   float* const ls = fs + W * 16;                                 // [W][16] sums
   __syncthreads();
   if (quad == 0) {
     fs[wave * 16 + col] = m;
     ls[wave * 16 + col] = l;
   }
-  const int rr = (tid & 63) / 4, d0 = (tid & 3) * 4, to = tile * 16 + rr, head = hk * a.g + to;
-  const bool writes = tid < 64 && to < a.g;
+  const int rr = lane / 4, d0 = (lane & 3) * 4, to = tile * 16 + rr, head = hk * a.g + to;
+  const bool writes = wave < CD && to < a.g;
   float f[W], mm = kNegInf, ll = 0.f, inv = 1.f;
-  // parts are numbered by head tile, then along the tile's workgroups
-  const int64_t prow = (static_cast<int64_t>(ht) * a.grid + part.before + part.split) * 16 + rr;
+  const int64_t prow = (static_cast<int64_t>(ht) * a.grid + part.number) * 16 + rr;
 #pragma unroll
-  for (int i = 0; i < DT; ++i) {
+  for (int i = 0; i < DT; i += CD) {
     if (i > 0) __syncthreads();
-    *reinterpret_cast<float4*>(os + (wave * 16 + col) * OST + 4 * quad) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+#pragma unroll
+    for (int c = 0; c < CD; ++c)
+      *reinterpret_cast<float4*>(os + ((c * W + wave) * 16 + col) * OST + 4 * quad) =
+          make_float4(o[i + c][0], o[i + c][1], o[i + c][2], o[i + c][3]);
     __syncthreads();
     if (!writes) continue;
     if (i == 0) {
@@ -330,31 +376,33 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
         f[j] = exp2_fast(fs[j * 16 + rr] - ms);
         ll = fmaf(f[j], ls[j * 16 + rr], ll);
       }
-      if (part.splits > 1) {
-        if (d0 == 0) *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(mm, ll);
+      const bool once = wave == 0 && d0 == 0;
+      if (part.parts > 1) {
+        if (once) *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(mm, ll);
       } else {
         inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);      // no position: zeros; a NaN sum stays NaN
-        if (d0 == 0 && a.lse != nullptr)
+        if (once && a.lse != nullptr)
           a.lse[static_cast<int64_t>(part.b) * a.Hq + head] = ll == 0.f ? kNegInf : fmaf(ms, kLn2, logf(ll));
       }
     }
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-      const float4 v = *reinterpret_cast<const float4*>(os + (j * 16 + rr) * OST + d0);
+      const float4 v = *reinterpret_cast<const float4*>(os + ((wave * W + j) * 16 + rr) * OST + d0);
       acc.x = fmaf(f[j], v.x, acc.x);
       acc.y = fmaf(f[j], v.y, acc.y);
       acc.z = fmaf(f[j], v.z, acc.z);
       acc.w = fmaf(f[j], v.w, acc.w);
     }
-    if (part.splits > 1) {
-      *reinterpret_cast<float4*>(a.part + prow * DP + 16 * i + d0) = acc;
+    const int d = 16 * (i + wave) + d0;
+    if (part.parts > 1) {
+      *reinterpret_cast<float4*>(a.part + prow * DP + d) = acc;
     } else {
       T* op = static_cast<T*>(a.out) + (static_cast<int64_t>(part.b) * a.Hq + head) * a.D;
       const float vals[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (16 * i + d0 + j < a.D) op[16 * i + d0 + j] = narrow<T>(vals[j]);
+        if (d + j < a.D) op[d + j] = narrow<T>(vals[j]);
     }
   }
 }
@@ -362,30 +410,21 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
 // Adds the parts of a sequence that was split: one workgroup for each sequence and query head; 8 threads of
 // every 4 elements (16, 32 for smaller heads) take its parts in turn.
 template <typename T, int DP>
-__global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a, int keys) {
+__global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a) {
   constexpr int V4 = DP / 4, S = 256 / V4;
   __shared__ float4 acc_of[S][V4 + 1];
   __shared__ float2 ml_of[S];
-  const int64_t at = a.first + blockIdx.x;
-  const int b = static_cast<int>(at / a.Hq), head = static_cast<int>(at % a.Hq), hk = head / a.g, row = head % a.g,
+  const uint32_t at = a.first + blockIdx.x;
+  const int b = at / a.Hq, head = at - b * a.Hq, hk = head / a.g, row = head % a.g,
             tile = row / 16, rr = row % 16;
   // the same division into parts as the first launch's: this sequence's first part
-  const int lane = threadIdx.x & 63;
-  int64_t total = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 64) {
-    int n = 0;
-    if (b0 + lane < a.B) n = (length_of(a, b0 + lane) + keys - 1) / keys;
-    total += wave_sum(n);
-  }
-  const int quota = max(1, static_cast<int>((total + a.slots - 1) / a.slots));
+  const int mine = blocks_of(a, 0), quota = quota_of(a, mine), splits = parts_of((length_of(a, b) + kKeys - 1) / kKeys, quota);
+  if (splits == 1) return;
   int before = 0;
   for (int b0 = 0; b0 < b; b0 += 64) {
-    int mine = 0;
-    if (b0 + lane < b) mine = max(1, ((length_of(a, b0 + lane) + keys - 1) / keys + quota - 1) / quota);
-    before += wave_sum(mine);
+    const int n = b0 == 0 ? mine : blocks_of(a, b0);
+    before += lanes_total(b0 + static_cast<int>(threadIdx.x & 63) < b ? parts_of(n, quota) : 0);
   }
-  const int steps = (length_of(a, b) + keys - 1) / keys, splits = max(1, (steps + quota - 1) / quota);
-  if (splits == 1) return;
   const int64_t p0 = ((static_cast<int64_t>(hk) * a.tiles + tile) * a.grid + before) * 16 + rr;
   const int d = threadIdx.x % V4, k = threadIdx.x / V4;
   float m = kNegInf, l = 0.f;
@@ -447,42 +486,61 @@ int check(const dcn_paged_desc* d) {
   return DCN_OK;
 }
 
-// Waves of a workgroup, and positions of a step of it.
-constexpr int waves_for(int es, int dp) { return es == 4 && dp == 128 ? 4 : 8; }
+// Waves of a workgroup.  Wide: as many as the registers of a CU hold, for the shortest chain of blocks.  Narrow:
+// half of that, so that one workgroup's start and end pass while another streams.
+constexpr int waves_for(int es, int dp, bool wide) {
+  return es == 2 ? (dp == 128 ? (wide ? 8 : 4) : wide ? 16 : 8) : dp == 128 ? 4 : wide ? 8 : 4;
+}
 
 struct PagedPlan {
-  int dp, waves, tiles, slots, grid;
+  int dp, waves, tiles, aim, least, grid;
+  bool split, wide, rounds;
 };
+// The division into parts.  A sequence has several only where its blocks may be more than kChain for each wave of a
+// wide workgroup: below, the launch that joins them costs more than it saves (one sequence, 8 heads of 64:
+// 1050 positions 10.2 us whole, 12.4 in parts; 2100 15.0 and 12.8).  Few sequences: one round of wide workgroups
+// (16800 positions 14.8 us, of narrow ones 15.5).  Many: kRounds rounds of narrow ones, in which their
+// lengths even out, but of kLeast blocks for each wave at least (32 sequences to 4200, 8 heads of 64, in one round
+// 55 us, 48 in two or three; 64 to 2000, 4 of 128: 47.7 us with parts of one block, 46.2 of three, 56 of twelve).
+constexpr int kChain = 3, kRounds = 3, kLeast = 3;
 PagedPlan plan_of(const dcn_paged_desc* d) {
   PagedPlan p{};
+  const int es = d->dtype == DCN_BF16 ? 2 : 4;
   p.dp = padded_head(d->head_dim);
-  p.waves = waves_for(d->dtype == DCN_BF16 ? 2 : 4, p.dp);
-  const int64_t g = d->query_heads / d->key_heads, capacity = d->max_pages * d->page_size;
+  const int64_t g = d->query_heads / d->key_heads, blocks = (d->max_pages * d->page_size + kKeys - 1) / kKeys;
   p.tiles = static_cast<int>((g + 15) / 16);
-  // two workgroups a CU; all parts of a key head's tile fit where sequences are fewer than half of them
-  const int64_t room = std::max<int64_t>(1, 2 * kCUs / (d->key_heads * p.tiles));
-  p.slots = static_cast<int>(d->batch <= room / 2 ? room - d->batch : 4 * room);
-  // ceil(n / quota) parts of each sequence: below slots + batch in all
-  const int64_t steps = (capacity + kKeys * p.waves - 1) / (kKeys * p.waves);
-  p.grid = static_cast<int>(std::min<int64_t>(p.slots + d->batch, d->batch * std::max<int64_t>(1, steps)));
+  const int64_t heads = d->key_heads * p.tiles, groups = d->batch * heads;
+  p.split = blocks > kChain * waves_for(es, p.dp, true);
+  const int64_t room = std::max<int64_t>(1, kCUs / heads);     // parts of a key head's tile in one round of wide workgroups
+  p.rounds = 4 * d->batch > room;
+  p.wide = p.split ? !p.rounds : groups <= kCUs;
+  p.waves = waves_for(es, p.dp, p.wide);
+  p.aim = static_cast<int>(p.rounds ? d->batch + kRounds * 2 * room : room);
+  p.least = (p.rounds ? kLeast : 1) * p.waves;
+  p.grid = p.split ? p.aim : static_cast<int>(d->batch);
   return p;
 }
 size_t workspace_of(const dcn_paged_desc* d, const PagedPlan& p, size_t* ml_at) {
   *ml_at = 0;
-  if (p.grid <= d->batch) return 0;     // no sequence can have two parts
+  if (!p.split) return 0;
   const size_t rows = static_cast<size_t>(d->key_heads) * p.tiles * p.grid * 16;
   *ml_at = rows * p.dp * 4;
   return (*ml_at + rows * 8 + 255) / 256 * 256;
 }
 
+template <typename T, int DP, int W>
+const void* paged_fn(Rows rows) {
+  return rows == kWhole     ? reinterpret_cast<const void*>(&paged_kernel<T, DP, W, kWhole>)
+         : rows == kVectors ? reinterpret_cast<const void*>(&paged_kernel<T, DP, W, kVectors>)
+                            : reinterpret_cast<const void*>(&paged_kernel<T, DP, W, kElements>);
+}
 template <typename T, int DP>
-const void* paged_fn(bool vec) {
-  return vec ? reinterpret_cast<const void*>(&paged_kernel<T, DP, waves_for(sizeof(T), DP), true>)
-             : reinterpret_cast<const void*>(&paged_kernel<T, DP, waves_for(sizeof(T), DP), false>);
+const void* paged_fn(bool wide, Rows rows) {
+  return wide ? paged_fn<T, DP, waves_for(sizeof(T), DP, true)>(rows) : paged_fn<T, DP, waves_for(sizeof(T), DP, false)>(rows);
 }
 template <typename T>
-const void* paged_fn(int dp, bool vec) {
-  return dp == 32 ? paged_fn<T, 32>(vec) : dp == 64 ? paged_fn<T, 64>(vec) : paged_fn<T, 128>(vec);
+const void* paged_fn(const PagedPlan& p, Rows rows) {
+  return p.dp == 32 ? paged_fn<T, 32>(p.wide, rows) : p.dp == 64 ? paged_fn<T, 64>(p.wide, rows) : paged_fn<T, 128>(p.wide, rows);
 }
 template <typename T>
 const void* join_fn(int dp) {
@@ -493,7 +551,7 @@ const void* join_fn(int dp) {
 bool launch_paged(const void* fn, int64_t n, int threads, void** args, PagedArgs* a, hipStream_t stream) {
   constexpr int64_t kMost = int64_t{1} << 21;   // a dispatch counts its threads in 32 bits
   for (int64_t first = 0; first < n; first += kMost) {
-    a->first = first;
+    a->first = static_cast<uint32_t>(first);
     const int64_t now = n - first < kMost ? n - first : kMost;
     if (hipLaunchKernel(fn, dim3(static_cast<unsigned>(now)), dim3(threads), args, 0, stream) != hipSuccess) return false;
   }
@@ -564,23 +622,32 @@ extern "C" int dcn_paged_attention(const dcn_paged_desc* d, const void* q, const
   a.tiles = p.tiles;
   a.num_pages = static_cast<int>(d->num_pages);
   a.page_size = static_cast<int>(d->page_size);
+  a.max_pages = cache ? static_cast<int>(d->max_pages) : 0;
   a.capacity = cache ? static_cast<int>(d->max_pages * d->page_size) : 0;
-  a.slots = p.slots;
+  a.split = p.split;
+  a.aim = p.aim;
+  a.least = p.least;
   a.grid = p.grid;
   a.c = d->scale * kLog2e;
   const bool bf16 = d->dtype == DCN_BF16;
   const int es = bf16 ? 2 : 4;
   const bool vec = vec_rows(q, d->q_stride, 2, d->head_dim, es) && vec_rows(key_pages, d->key_page_stride, 3, d->head_dim, es) &&
                    vec_rows(value_pages, d->value_page_stride, 3, d->head_dim, es);
+  const Rows rows = !vec ? kElements : a.D == p.dp ? kWhole : kVectors;
+  if (d->page_size > 1) {
+    // of positions below 2^31: with 2^s >= page_size, 2^(31 + s) / page_size rounded up is off by less than 2^-31 of it
+    int s = 0;
+    while ((int64_t{1} << s) < d->page_size) ++s;
+    a.page_m = static_cast<uint32_t>(((uint64_t{1} << (31 + s)) + d->page_size - 1) / d->page_size);
+    a.page_s = s - 1;
+  }
   void* args[] = {&a};
-  if (!launch_paged(bf16 ? paged_fn<uint16_t>(p.dp, vec) : paged_fn<float>(p.dp, vec),
+  if (!launch_paged(bf16 ? paged_fn<uint16_t>(p, rows) : paged_fn<float>(p, rows),
                     static_cast<int64_t>(p.grid) * a.Hkv * a.tiles, 64 * p.waves, args, &a, stream))
     return DCN_E_HIP;
-  if (need > 0) {
-    int keys = kKeys * p.waves;
-    void* join_args[] = {&a, &keys};
+  if (p.split) {
     if (!launch_paged(bf16 ? join_fn<uint16_t>(p.dp) : join_fn<float>(p.dp), static_cast<int64_t>(a.B) * a.Hq, 256,
-                      join_args, &a, stream))
+                      args, &a, stream))
       return DCN_E_HIP;
   }
   return DCN_OK;

@@ -49,6 +49,7 @@ struct Args {
   int runs;                      // of a batch element where a gate is shared by its positions, else of all rows
   int P, C, B;
   int n1, n2, gkind;
+  int sums, sum_of[kSums];       // sums over the rows that are wanted
   float eps, inv;                // 1 / C
 };
 
@@ -212,12 +213,20 @@ __global__ __launch_bounds__(TR == 0 ? 1024 : 256) void residual_norm_kernel(Arg
   param<T, V>(a.w2, 0, l, 1.f, w2);
   param<T, V>(a.b2, 0, l, 0.f, b2);
   param<T, V>(a.scale, 0, l, 1.f, sc);
-  for (int64_t row = blockIdx.x * a.per_run + mine; row < r1; row += step) {
+  Raw<T, V> x, y, gt;
+  const auto fetch = [&](int64_t row) {
+    y = load<T, V>(a.y, row, l);
+    x = load<T, V>(a.x, row, l);
+    if (a.gkind != DCN_GATE_NONE) gt = load<T, V>(a.gate, a.gkind == DCN_GATE_FULL ? row : row / a.P, l);
+  };
+  const int64_t r0 = blockIdx.x * a.per_run + mine;
+  if (r0 < r1) fetch(r0);
+  for (int64_t row = r0; row < r1; row += step) {
     float f[kE], o[kE], g[kE];
-    const Raw<T, V> x = load<T, V>(a.x, row, l);
-    floats<T, V>(load<T, V>(a.y, row, l), f);
-    if (a.gkind != DCN_GATE_NONE) param<T, V>(a.gate, a.gkind == DCN_GATE_FULL ? row : row / a.P, l, 1.f, g);
+    floats<T, V>(y, f);
     floats<T, V>(x, o);
+    floats<T, V>(gt, g);
+    if (row + step < r1) fetch(row + step);     // the next row's loads are under way over this one's sums
     float m1, r1s, m2, r2s;
     normalise<V, TR>(f, a.n1, a, l, red, turn, m1, r1s);
 #pragma unroll
@@ -262,20 +271,34 @@ __global__ __launch_bounds__(NT) void residual_grad_kernel(Args a) {
   for (int n = 0; n < kSums; ++n)
 #pragma unroll
     for (int i = 0; i < kE; ++i) sum[n][i] = 0.f;
+  Raw<T, V> ry, rx, rgo, rgn, rg;
+  float4 rst = make_float4(0.f, 1.f, 0.f, 1.f);
+  const auto fetch = [&](int64_t row) {
+    ry = load<T, V>(a.y, row, l);
+    if (a.n2 != DCN_NORM_NONE) {
+      rx = load<T, V>(a.x, row, l);
+      rgn = a.gn != nullptr ? load<T, V>(a.gn, row, l) : Raw<T, V>{};
+    }
+    rgo = a.go != nullptr ? load<T, V>(a.go, row, l) : Raw<T, V>{};
+    if (a.gkind == DCN_GATE_FULL) rg = load<T, V>(a.gate, row, l);
+    rst = *reinterpret_cast<const float4*>(a.stats + row * 4);
+  };
+  if (r0 + mine < r1) fetch(r0 + mine);
   for (int64_t row = r0 + mine; row < r1; row += STEP) {
-    const float4 st = *reinterpret_cast<const float4*>(a.stats + row * 4);
+    const float4 st = rst;
     float v[kE], u[kE], d[kE], z[kE], gn[kE];
-    floats<T, V>(load<T, V>(a.y, row, l), v);
-    if (a.gkind == DCN_GATE_FULL) param<T, V>(a.gate, row, l, 1.f, g);
-    param<T, V>(a.go, row, l, 0.f, d);
+    floats<T, V>(ry, v);
+    floats<T, V>(rx, u);
+    floats<T, V>(rgn, gn);
+    floats<T, V>(rgo, d);
+    if (a.gkind == DCN_GATE_FULL) floats<T, V>(rg, g);
+    if (row + STEP < r1) fetch(row + STEP);     // the next row's loads are under way over this one's sums
 #pragma unroll
     for (int i = 0; i < kE; ++i) {
       v[i] = l.at<V>(i / V) < l.C ? (v[i] - st.x) * st.y : 0.f;
       z[i] = fmaf(v[i], w1[i], b1[i]);
     }
     if (a.n2 != DCN_NORM_NONE) {
-      floats<T, V>(load<T, V>(a.x, row, l), u);
-      param<T, V>(a.gn, row, l, 0.f, gn);
       float s[2] = {0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < kE; ++i) {
@@ -347,51 +370,38 @@ __global__ __launch_bounds__(NT) void residual_grad_kernel(Args a) {
   }
 }
 
-// Adds the runs' parts: 32 channels of a workgroup, 16 threads for each.
+// Adds the runs' parts of one sum (blockIdx.y: of those that are wanted, then a shared gate's batch
+// elements): 16 channels of a workgroup, 64 threads for each, so that a thread's loads are all under way at once.
 template <typename T>
-__global__ __launch_bounds__(512) void residual_params_kernel(Args a) {
-  __shared__ float red[kSums][16][33];
-  const int c = blockIdx.x * 32 + threadIdx.x % 32, k = threadIdx.x / 32;
+__global__ __launch_bounds__(1024) void residual_params_kernel(Args a) {
+  __shared__ float red[64][17];
+  const int lane = threadIdx.x % 16, k = threadIdx.x / 16, c = blockIdx.x * 16 + lane;
   const bool shared_gate = a.gkind == DCN_GATE_BATCH, in = c < a.C;
-  const int batches = shared_gate ? a.B : 1;
-  float total[kSums] = {0.f, 0.f, 0.f, 0.f, 0.f};
-  const auto value = [&](const void* p, int64_t at, float none) {
-    return p != nullptr && in ? widen(static_cast<const T*>(p)[at]) : none;
-  };
-  const float sc = value(a.scale, c, 1.f);
-  for (int b = 0; b < batches; ++b) {
-    float s[kSums] = {0.f, 0.f, 0.f, 0.f, 0.f};
-    if (in)
-      for (int r = k; r < a.runs; r += 16) {
-        const float* p = a.part + (static_cast<int64_t>(b) * a.runs + r) * kSums * a.C + c;
-#pragma unroll
-        for (int n = 0; n < kSums; ++n) s[n] += p[n * a.C];
-      }
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < kSums; ++n) red[n][k][threadIdx.x % 32] = s[n];
-    __syncthreads();
-    if (k == 0 && in) {
-#pragma unroll
-      for (int n = 0; n < kSums; ++n) {
-        s[n] = 0.f;
-        for (int j = 0; j < 16; ++j) s[n] += red[n][j][threadIdx.x % 32];
-      }
-      const float g = shared_gate ? value(a.gate, static_cast<int64_t>(b) * a.C + c, 1.f) : 1.f;
-      if (shared_gate && a.ggate != nullptr)
-        static_cast<T*>(a.ggate)[static_cast<int64_t>(b) * a.C + c] = narrow<T>(sc * s[2]);
-      total[0] += s[0];
-      total[1] += s[1];
-#pragma unroll
-      for (int n = 2; n < kSums; ++n) total[n] = fmaf(g, s[n], total[n]);
+  const int b = static_cast<int>(blockIdx.y) - a.sums;                  // >= 0: the gate's gradient of a batch element
+  const int n = b >= 0 ? 2 : a.sum_of[blockIdx.y];
+  const int r0 = b >= 0 ? b * a.runs : 0, r1 = b >= 0 ? r0 + a.runs : a.runs * (shared_gate ? a.B : 1);
+  const T* gate = b < 0 && n >= 2 && shared_gate ? static_cast<const T*>(a.gate) : nullptr;
+  float s = 0.f;
+  if (in) {
+    const float* part = a.part + static_cast<int64_t>(n) * a.C + c;
+#pragma unroll 8
+    for (int r = r0 + k; r < r1; r += 64) {
+      const float p = part[static_cast<int64_t>(r) * kSums * a.C];
+      s = gate == nullptr ? s + p : fmaf(widen(gate[static_cast<int64_t>(r / a.runs) * a.C + c]), p, s);
     }
   }
+  red[k][lane] = s;
+  __syncthreads();
+  if (k >= 4) return;
+  s = 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) s += red[4 * j + k][lane];
+  s += __shfl_xor(s, 16, 64);
+  s += __shfl_xor(s, 32, 64);
   if (k != 0 || !in) return;
-  if (a.gw2 != nullptr) static_cast<T*>(a.gw2)[c] = narrow<T>(total[0]);
-  if (a.gb2 != nullptr) static_cast<T*>(a.gb2)[c] = narrow<T>(total[1]);
-  if (a.gscale != nullptr) static_cast<T*>(a.gscale)[c] = narrow<T>(total[2]);
-  if (a.gw1 != nullptr) static_cast<T*>(a.gw1)[c] = narrow<T>(sc * total[3]);
-  if (a.gb1 != nullptr) static_cast<T*>(a.gb1)[c] = narrow<T>(sc * total[4]);
+  if ((b >= 0 || n >= 3) && a.scale != nullptr) s *= widen(static_cast<const T*>(a.scale)[c]);
+  void* to = b >= 0 ? a.ggate : n == 0 ? a.gw2 : n == 1 ? a.gb2 : n == 2 ? a.gscale : n == 3 ? a.gw1 : a.gb1;
+  static_cast<T*>(to)[b >= 0 ? static_cast<int64_t>(b) * a.C + c : c] = narrow<T>(s);
 }
 
 // ---- host side
@@ -405,7 +415,7 @@ int check(const dcn_residual_desc* d) {
   if (d->dtype != DCN_F32 && d->dtype != DCN_BF16) return DCN_E_UNSUPPORTED;
   const double big = 2147483647.;
   if (d->channels > kMaxC || d->batch > big || d->positions > big ||
-      static_cast<double>(d->batch) * d->positions > big || (d->gate == DCN_GATE_BATCH && d->batch > 65535))
+      static_cast<double>(d->batch) * d->positions > big || (d->gate == DCN_GATE_BATCH && d->batch > 65530))
     return DCN_E_UNSUPPORTED;
   return DCN_OK;
 }
@@ -421,11 +431,12 @@ Shape shape_of(int64_t C) {
   return {tr, 256, 256 / tr};
 }
 
+constexpr int64_t kRuns = 512, kForwardRuns = 1024;   // workgroups at most: 2 and 4 a CU
 // Runs of the gradients: two workgroups for each CU at most, and whole steps of rows.
 void runs_of(const dcn_residual_desc* d, const Shape& s, int* runs, int64_t* per_run) {
   const bool shared_gate = d->gate == DCN_GATE_BATCH;
   const int64_t rows = shared_gate ? d->positions : d->batch * d->positions;
-  int64_t n = shared_gate ? std::max<int64_t>(1, 512 / std::max<int64_t>(1, d->batch)) : 512;
+  int64_t n = shared_gate ? std::max<int64_t>(1, kRuns / std::max<int64_t>(1, d->batch)) : kRuns;
   *per_run = std::max<int64_t>(1, (rows + n - 1) / n);
   *per_run = (*per_run + s.step - 1) / s.step * s.step;
   *runs = static_cast<int>((rows + *per_run - 1) / *per_run);
@@ -489,14 +500,17 @@ int width_of(const dcn_residual_desc* d, const void* const (&ptrs)[N]) {
   return 1;
 }
 
-bool launch(const void* fn, int64_t groups, int threads, Args* a, hipStream_t stream) {
+bool launch(const void* fn, dim3 groups, int threads, Args* a, hipStream_t stream) {
   void* args[] = {a};
-  return hipLaunchKernel(fn, dim3(static_cast<unsigned>(groups)), dim3(threads), args, 0, stream) == hipSuccess;
+  return hipLaunchKernel(fn, groups, dim3(threads), args, 0, stream) == hipSuccess;
 }
 
-bool params_wanted(const dcn_residual_desc* d, const Args& a) {
-  return a.gscale != nullptr || a.gw1 != nullptr || a.gb1 != nullptr || a.gw2 != nullptr || a.gb2 != nullptr ||
-         (d->gate == DCN_GATE_BATCH && a.ggate != nullptr);
+// Notes which sums over the rows are wanted; how many outputs [C] the second launch writes.
+int64_t wanted_sums(Args* a) {
+  const void* to[kSums] = {a->gw2, a->gb2, a->gscale, a->gw1, a->gb1};
+  for (int n = 0; n < kSums; ++n)
+    if (to[n] != nullptr) a->sum_of[a->sums++] = n;
+  return a->sums + (a->gkind == DCN_GATE_BATCH && a->ggate != nullptr ? a->B : 0);
 }
 
 }  // namespace
@@ -538,8 +552,8 @@ extern "C" int dcn_residual_norm(const dcn_residual_desc* d, const void* x, cons
   const Shape s = shape_of(d->channels);
   // runs of several steps share a thread's parameters
   const int64_t steps = (a.rows + s.step - 1) / s.step;
-  a.per_run = std::max<int64_t>(1, (steps + 4095) / 4096) * s.step;
-  return launch(kernel_of(d->dtype == DCN_BF16, w, s, false), (a.rows + a.per_run - 1) / a.per_run, s.threads, &a,
+  a.per_run = std::max<int64_t>(1, (steps + kForwardRuns - 1) / kForwardRuns) * s.step;
+  return launch(kernel_of(d->dtype == DCN_BF16, w, s, false), dim3((a.rows + a.per_run - 1) / a.per_run), s.threads, &a,
                 stream)
              ? DCN_OK
              : DCN_E_HIP;
@@ -600,12 +614,13 @@ extern "C" int dcn_residual_norm_backward(const dcn_residual_desc* d, const void
   a.gb1 = grad_branch_bias;
   a.gw2 = grad_next_weight;
   a.gb2 = grad_next_bias;
-  const bool bf16 = d->dtype == DCN_BF16, params = params_wanted(d, a);
+  const bool bf16 = d->dtype == DCN_BF16;
+  const int64_t outputs = wanted_sums(&a);
   const Shape s = shape_of(d->channels);
   if (any) {
     runs_of(d, s, &a.runs, &a.per_run);
     const int64_t groups = static_cast<int64_t>(a.runs) * (d->gate == DCN_GATE_BATCH ? a.B : 1);
-    if (params) {
+    if (outputs > 0) {
       size_t need = 0;
       rc = dcn_residual_norm_backward_workspace_bytes(d, &need);
       if (rc != DCN_OK) return rc;
@@ -616,12 +631,12 @@ extern "C" int dcn_residual_norm_backward(const dcn_residual_desc* d, const void
     const int w = width_of(d, {a.x, a.y, a.gate, a.scale, a.w1, a.b1, a.w2, a.go, a.gn, static_cast<const void*>(a.out),
                                static_cast<const void*>(a.next),
                                d->gate == DCN_GATE_FULL ? static_cast<const void*>(a.ggate) : nullptr});
-    if (!launch(kernel_of(bf16, w, s, true), groups, s.threads, &a, stream)) return DCN_E_HIP;
+    if (!launch(kernel_of(bf16, w, s, true), dim3(groups), s.threads, &a, stream)) return DCN_E_HIP;
   }
-  if (params &&
+  if (outputs > 0 &&
       !launch(bf16 ? reinterpret_cast<const void*>(&residual_params_kernel<uint16_t>)
                    : reinterpret_cast<const void*>(&residual_params_kernel<float>),
-              (d->channels + 31) / 32, 512, &a, stream))
+              dim3((d->channels + 15) / 16, outputs), 1024, &a, stream))
     return DCN_E_HIP;
   return DCN_OK;
 }

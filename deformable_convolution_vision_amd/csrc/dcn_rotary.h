@@ -1,10 +1,10 @@
 // dcn_rotary.h -- what rotary positions (dcn_rotary.hip) and the paged cache's append
-// (dcn_append.hip) share: the angles, a pair's place in its head, vectors of a row, and the
-// host-side checks.  Not part of the public ABI.
+// (dcn_append.hip) share: the angles, a pair's place in its head, vectors of a row, how rows fall to
+// workgroups, and the host-side checks.  Not part of the public ABI.
 //
-// A thread takes a chunk of PV pairs of one row: their cosines and sines are formed once and serve
-// the same chunk of several heads.  The chunk's elements are two vectors of PV, wherever the layout
-// has them.
+// A workgroup takes a few rows.  It forms the cosines and sines of their angles once, in the LDS, where
+// every head of the rows reads them; the elements' loads are under way meanwhile.  A thread's unit is a
+// chunk of PV pairs of one head: two vectors of PV elements, wherever the layout has them.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -70,28 +70,22 @@ __device__ __forceinline__ void cos_sin(double pos, float f, float& c, float& s)
   s = (k & 2) != 0 ? -b : b;
 }
 
-// The positions of a row on its axes.
-struct At {
-  double p0 = 0., p1 = 0., p2 = 0., p3 = 0.;
-  __device__ __forceinline__ double of(const Turns& t, int pair) const {
-    const double a = p0, b = p1, c = p2, d = p3;   // values: a choice among the members would be one among addresses
-    return pair >= t.end[2] ? d : pair >= t.end[1] ? c : pair >= t.end[0] ? b : a;
-  }
-};
-__device__ __forceinline__ At at_row(const Turns& t, int b, int row) {
-  const int64_t o = b * t.ps[0] + row * t.ps[1];
-  const auto axis = [&](int a) {
-    if (a >= t.axes) return 0.;
-    return t.whole ? static_cast<double>(static_cast<const int32_t*>(t.positions)[o + a])
-                   : static_cast<double>(static_cast<const float*>(t.positions)[o + a]);
-  };
-  At at;
-  at.p0 = axis(0);
-  at.p1 = axis(1);
-  at.p2 = axis(2);
-  at.p3 = axis(3);
-  return at;
+// The axis that a pair turns with.
+__device__ __forceinline__ int axis_of(const Turns& t, int pair) {
+  return (pair >= t.end[0]) + (pair >= t.end[1]) + (pair >= t.end[2]);
 }
+__device__ __forceinline__ double position_of(const Turns& t, int b, int row, int axis) {
+  const int64_t o = b * t.ps[0] + row * t.ps[1] + axis;
+  return t.whole ? static_cast<double>(static_cast<const int32_t*>(t.positions)[o])
+                 : static_cast<double>(static_cast<const float*>(t.positions)[o]);
+}
+
+// Division by a number that is known on the host, of n < 2^16 (both): the product with 2^32 / d, rounded
+// up, is then off by less than 1 / d.
+struct Div {
+  uint32_t d, m;
+  __device__ __forceinline__ int of(int n) const { return d == 1 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), m)); }
+};
 
 // The first elements of a chunk's two vectors.
 struct Place {
@@ -106,7 +100,7 @@ __device__ __forceinline__ Place place_of(const Turns& t, int chunk, int rotated
   const int p = chunk * PV;
   if (t.layout == DCN_ROTARY_HALVES) return {p, p + t.pairs};
   if (t.layout == DCN_ROTARY_ADJACENT) return {2 * p, 2 * p + PV};
-  const int a = (p >= t.end[0]) + (p >= t.end[1]) + (p >= t.end[2]);
+  const int a = axis_of(t, p);
   const int n = (a < t.axes - 1 ? t.end[a] : t.pairs) - t.start[a];
   return {p + t.start[a], p + t.start[a] + n};
 }
@@ -202,24 +196,41 @@ inline int fit(int w, const int64_t* strides, int n) {
   return w;
 }
 
-// How rows fall to workgroups of 256: a row has `chunks` chunks, `rotated` of them of pairs, the others
-// copied; its heads are dealt to `groups` threads of each chunk.
+// How rows and heads fall to workgroups of 256: `rows` rows and `heads` heads of each, of which a row has
+// `groups`; a head has `chunks` chunks, `rotated` of them of pairs, the others copied.
+constexpr int kTurns = 2048;      // cosines and sines of a workgroup: 16 KB
+// Units of a thread under way at a time, by the bytes of a vector.  Two of 16 bytes fill the memory's queues and leave
+// workgroups small enough for an even last round (rotary_c3_batch8 with 1, 2, 4 units: 32.9, 33.0, 36.6
+// us); narrower ones take four (2 bytes, 16800 rows of 8 heads of 37: 21.7, 13.5, 12.1 us).
+constexpr int units_of(int bytes) { return bytes == 16 ? 2 : 4; }
+constexpr int kRows = 64;         // the most rows of a workgroup
 struct Cut {
-  int chunks, rotated, groups;
-  int units;               // threads of a row: chunks * groups
-  int rows;                // of a workgroup
+  int chunks, rotated, rows, heads, groups;
+  Div by_chunks, by_row, by_pairs;   // by_row: heads * chunks
 };
-// Heads share a thread's angles, but where rows are few each thread takes fewer of them, down to one: the
-// chip wants 2^17 threads (two waves on each SIMD).
-inline Cut cut_of(int width, int pairs, int64_t head_dim, int64_t rows, int64_t heads) {
+inline Div div_by(int64_t d) {
+  return {static_cast<uint32_t>(d < 1 ? 1 : d), static_cast<uint32_t>(d < 2 ? 0 : (int64_t{1} << 32) / d + 1)};
+}
+// Rows share nothing, so a workgroup takes as many as fill its threads' units; where there are fewer than
+// four workgroups a CU then, fewer rows each, and fewer heads of one row.
+inline Cut cut_of(int width, int es, int pairs, int64_t head_dim, int64_t rows, int64_t heads) {
   Cut c{};
   c.rotated = pairs / width;
   c.chunks = c.rotated + static_cast<int>((head_dim - 2 * pairs + 2 * width - 1) / (2 * width));
-  const int64_t want = (int64_t{1} << 17) / (rows * c.chunks);
-  c.groups = static_cast<int>(want < 1 ? 1 : want > heads ? heads : want);
-  if (static_cast<int64_t>(c.chunks) * c.groups > 256) c.groups = c.chunks >= 256 ? 1 : 256 / c.chunks;
-  c.units = c.chunks * c.groups;
-  c.rows = c.units >= 256 ? 1 : 256 / c.units;
+  const int64_t most = units_of(width * es) * 256, wanted = 4 * 256;
+  int64_t h = heads * c.chunks <= most ? heads : most / c.chunks > 1 ? most / c.chunks : 1;
+  if (rows * ((heads + h - 1) / h) < wanted && h * c.chunks > 256) h = 256 / c.chunks > 1 ? 256 / c.chunks : 1;
+  int64_t r = most / (h * c.chunks);
+  if (pairs > 0 && r > kTurns / pairs) r = kTurns / pairs;
+  const int64_t least = (256 + h * c.chunks - 1) / (h * c.chunks);   // a unit for each thread
+  if (r > rows / wanted) r = rows / wanted > least ? rows / wanted : r < least ? r : least;
+  if (r > kRows) r = kRows;
+  c.rows = static_cast<int>(r < 1 ? 1 : r);
+  c.heads = static_cast<int>(h);
+  c.groups = static_cast<int>((heads + h - 1) / h);
+  c.by_chunks = div_by(c.chunks);
+  c.by_row = div_by(h * c.chunks);
+  c.by_pairs = div_by(pairs);
   return c;
 }
 

@@ -12,8 +12,8 @@
 //
 //   grad_pos[b][l][a] = sum over heads and the axis's pairs of freq[p] (gx2 x1 - gx1 x2).
 //
-// A workgroup takes whole rows, so a row's sum over its heads stays in it: threads leave their sums
-// in the LDS and one thread for each row and axis adds them in order.
+// For the position's gradient a workgroup has all heads of its rows, and each unit leaves its sum for each
+// axis in the LDS, where one thread for each row and axis adds them in order.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -38,101 +38,109 @@ struct Args {
   float sign;              // 1, or -1 to turn back
 };
 
-constexpr int kHeads = 4;  // heads under way at a time
-
 template <typename T, int PV, bool ADJ, bool POS>
 __global__ __launch_bounds__(256) void rotary_kernel(Args a) {
-  __shared__ float red[POS ? 4 * 256 : 1];
-  const int tid = threadIdx.x, r = tid / a.cut.units, u0 = tid - r * a.cut.units;
-  const int64_t row = (a.first + blockIdx.x) * a.cut.rows + r;
-  const bool live = r < a.cut.rows && row < a.rows;
-  float sums[4] = {0.f, 0.f, 0.f, 0.f};
-  if (live) {
-    const int b = static_cast<int>(row / a.L), l = static_cast<int>(row - static_cast<int64_t>(b) * a.L);
-    const At at = at_row(a.t, b, l);
-    const T* const xr = static_cast<const T*>(a.x) + b * a.xs[0] + l * a.xs[1];
-    const T* const x0r = POS ? static_cast<const T*>(a.x0) + b * a.x0s[0] + l * a.x0s[1] : nullptr;
-    T* const yr = static_cast<T*>(a.out) + row * a.H * a.D;
-    for (int u = u0; u < a.cut.units; u += 256) {   // once, unless a row has more units than a workgroup threads
-      const int chunk = u % a.cut.chunks, group = u / a.cut.chunks;
-      const Place p = place_of<PV>(a.t, chunk, a.cut.rotated);
-      const bool turns = chunk < a.cut.rotated, second = p.e2 < a.D;
-      float c[PV], s[PV], f[PV], moved[PV];
+  using V = Vec<T, PV>;
+  constexpr int kUnits = units_of(sizeof(V));
+  __shared__ float2 cs[kTurns];
+  __shared__ float red[POS ? 4 * kUnits * 256 : 1];
+  const int tid = threadIdx.x;
+  const int64_t at = a.first + blockIdx.x, row0 = (POS ? at : at / a.cut.groups) * a.cut.rows;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(a.cut.rows), a.rows - row0));
+  // the heads of this workgroup; for the position's gradient one group of them after the other
+  const int g0 = POS ? 0 : static_cast<int>(at % a.cut.groups), g1 = POS ? a.cut.groups : g0 + 1;
+  float sum = 0.f;
+  for (int g = g0; g < g1; ++g) {
+    const int h0 = g * a.cut.heads, heads = min(a.cut.heads, a.H - h0);
+    const int units = rows * static_cast<int>(a.cut.by_row.d);
+    for (int u0 = 0; u0 < units; u0 += kUnits * 256) {
+      V v1[kUnits], v2[kUnits], w1[POS ? kUnits : 1], w2[POS ? kUnits : 1];
+      const auto unit = [&](int k, int& r, int& h, int& chunk) {   // false: no unit
+        const int u = u0 + k * 256 + tid;
+        r = a.cut.by_row.of(u);
+        const int in_row = u - r * static_cast<int>(a.cut.by_row.d);
+        h = a.cut.by_chunks.of(in_row);
+        chunk = in_row - h * a.cut.chunks;
+        return u < units && h < heads;
+      };
 #pragma unroll
-      for (int j = 0; j < PV; ++j) {
-        c[j] = 1.f;
-        s[j] = f[j] = moved[j] = 0.f;
-      }
-      if (turns) {
-#pragma unroll
-        for (int j = 0; j < PV; ++j) {
-          f[j] = a.t.freq[chunk * PV + j];
-          cos_sin(at.of(a.t, chunk * PV + j), f[j], c[j], s[j]);
-          s[j] *= a.sign;
+      for (int k = 0; k < kUnits; ++k) {
+        int r, h, chunk;
+        if (!unit(k, r, h, chunk)) continue;
+        const uint32_t row = static_cast<uint32_t>(row0 + r), b = row / static_cast<uint32_t>(a.L), l = row - b * a.L;
+        const Place p = place_of<PV>(a.t, chunk, a.cut.rotated);
+        const T* x = static_cast<const T*>(a.x) + b * a.xs[0] + l * a.xs[1] + (h0 + h) * a.xs[2];
+        v1[k] = *reinterpret_cast<const V*>(x + p.e1);
+        if (p.e2 < a.D) v2[k] = *reinterpret_cast<const V*>(x + p.e2);
+        if (POS && chunk < a.cut.rotated) {
+          const T* x0 = static_cast<const T*>(a.x0) + b * a.x0s[0] + l * a.x0s[1] + (h0 + h) * a.x0s[2];
+          w1[k] = *reinterpret_cast<const V*>(x0 + p.e1);
+          w2[k] = *reinterpret_cast<const V*>(x0 + p.e2);
         }
       }
-      using V = Vec<T, PV>;
-      for (int h0 = group; h0 < a.H; h0 += kHeads * a.cut.groups) {
-        V v1[kHeads], v2[kHeads], w1[kHeads], w2[kHeads];
-#pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
-          const int h = h0 + i * a.cut.groups;
-          if (h >= a.H) break;
-          const T* x = xr + h * a.xs[2];
-          v1[i] = *reinterpret_cast<const V*>(x + p.e1);
-          if (second) v2[i] = *reinterpret_cast<const V*>(x + p.e2);
-          if (POS && turns) {
-            const T* x0 = x0r + h * a.x0s[2];
-            w1[i] = *reinterpret_cast<const V*>(x0 + p.e1);
-            w2[i] = *reinterpret_cast<const V*>(x0 + p.e2);
-          }
+      if (g == g0 && u0 == 0) {
+        for (int i = tid; i < rows * a.t.pairs; i += 256) {
+          const int r = a.cut.by_pairs.of(i), pair = i - r * a.t.pairs;
+          const uint32_t row = static_cast<uint32_t>(row0 + r), b = row / static_cast<uint32_t>(a.L), l = row - b * a.L;
+          float c, s;
+          cos_sin(position_of(a.t, b, l, axis_of(a.t, pair)), a.t.freq[pair], c, s);
+          cs[i] = make_float2(c, a.sign * s);
         }
+        __syncthreads();
+      }
 #pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
-          const int h = h0 + i * a.cut.groups;
-          if (h >= a.H) break;
-          T* y = yr + static_cast<int64_t>(h) * a.D;
-          if (turns) {
-            float x1[PV], x2[PV], y1[PV], y2[PV];
-            pairs_of<T, PV, ADJ>(v1[i], v2[i], x1, x2);
+      for (int k = 0; k < kUnits; ++k) {
+        int r, h, chunk;
+        const bool live = unit(k, r, h, chunk);
+        float moved[4] = {0.f, 0.f, 0.f, 0.f};
+        if (live) {
+          const Place p = place_of<PV>(a.t, chunk, a.cut.rotated);
+          if (chunk < a.cut.rotated) {
+            float c[PV], s[PV], x1[PV], x2[PV], y1[PV], y2[PV];
+            const float2* turns = cs + r * a.t.pairs + chunk * PV;
+#pragma unroll
+            for (int j = 0; j < PV; ++j) {
+              c[j] = turns[j].x;
+              s[j] = turns[j].y;
+            }
+            pairs_of<T, PV, ADJ>(v1[k], v2[k], x1, x2);
             turn<PV>(c, s, x1, x2, y1, y2);
             if (POS) {
-              float o1[PV], o2[PV];
-              pairs_of<T, PV, ADJ>(w1[i], w2[i], o1, o2);
+              pairs_of<T, PV, ADJ>(w1[k], w2[k], x1, x2);
 #pragma unroll
-              for (int j = 0; j < PV; ++j) moved[j] += y2[j] * o1[j] - y1[j] * o2[j];
+              for (int j = 0; j < PV; ++j) {
+                const int pair = chunk * PV + j, axis = axis_of(a.t, pair);
+                const float m = a.t.freq[pair] * (y2[j] * x1[j] - y1[j] * x2[j]);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) moved[n] += axis == n ? m : 0.f;
+              }
             }
-            vectors_of<T, PV, ADJ>(y1, y2, v1[i], v2[i]);
+            vectors_of<T, PV, ADJ>(y1, y2, v1[k], v2[k]);
           }
           if (!POS || a.out != nullptr) {
-            *reinterpret_cast<V*>(y + p.e1) = v1[i];
-            if (second) *reinterpret_cast<V*>(y + p.e2) = v2[i];
+            T* y = static_cast<T*>(a.out) + ((row0 + r) * a.H + h0 + h) * a.D;
+            *reinterpret_cast<V*>(y + p.e1) = v1[k];
+            if (p.e2 < a.D) *reinterpret_cast<V*>(y + p.e2) = v2[k];
           }
         }
-      }
-      if (POS && turns) {
+        if constexpr (POS) {
 #pragma unroll
-        for (int j = 0; j < PV; ++j) {
-          const int pair = chunk * PV + j, axis = (pair >= a.t.end[0]) + (pair >= a.t.end[1]) + (pair >= a.t.end[2]);
-#pragma unroll
-          for (int n = 0; n < 4; ++n) sums[n] += axis == n ? f[j] * moved[j] : 0.f;
+          for (int n = 0; n < 4; ++n)
+            if (n < a.t.axes) red[n * kUnits * 256 + k * 256 + tid] = moved[n];
         }
+      }
+      if constexpr (POS) {
+        // thread i adds up row i / axes, axis i % axes: the units of this turn that are the row's
+        __syncthreads();
+        const int r = tid / a.t.axes, n = tid - r * a.t.axes, per = static_cast<int>(a.cut.by_row.d);
+        if (r < rows)
+          for (int u = max(r * per, u0); u < min((r + 1) * per, u0 + kUnits * 256); ++u) sum += red[n * kUnits * 256 + u - u0];
+        __syncthreads();
       }
     }
   }
   if constexpr (POS) {
-#pragma unroll
-    for (int n = 0; n < 4; ++n) red[n * 256 + tid] = sums[n];
-    __syncthreads();
-    const int units = min(a.cut.units, 256);
-    for (int i = tid; i < a.cut.rows * a.t.axes; i += 256) {
-      const int rr = i / a.t.axes, n = i - rr * a.t.axes;
-      const int64_t to = (a.first + blockIdx.x) * a.cut.rows + rr;
-      if (to >= a.rows) break;
-      float sum = 0.f;
-      for (int u = 0; u < units; ++u) sum += red[n * 256 + rr * units + u];
-      a.gp[to * a.t.axes + n] = sum;
-    }
+    if (tid < rows * a.t.axes) a.gp[row0 * a.t.axes + tid] = sum;
   }
 }
 
@@ -164,7 +172,7 @@ int check(const dcn_rotary_desc* d) {
   if (rc != DCN_OK) return rc;
   if (d->dtype != DCN_F32 && d->dtype != DCN_BF16) return DCN_E_UNSUPPORTED;
   const double big = 2147483648.;
-  if (d->head_dim > 65536 || static_cast<double>(d->batch) * d->length * d->heads >= big || d->batch >= big ||
+  if (d->head_dim > 2 * kTurns || static_cast<double>(d->batch) * d->length * d->heads >= big || d->batch >= big ||
       d->length >= big || d->heads >= big)
     return DCN_E_UNSUPPORTED;
   return DCN_OK;
@@ -181,9 +189,10 @@ int run(const dcn_rotary_desc* d, Args* a, const void* positions, const float* f
   int w = fit(fit(width_of(a->t, d->sections, d->head_dim, es), es, a->x), es, a->out);
   w = fit(w, a->xs, 3);
   if (a->x0 != nullptr) w = fit(fit(w, es, a->x0), a->x0s, 3);
-  a->cut = cut_of(w, a->t.pairs, d->head_dim, a->rows, d->heads);
+  a->cut = cut_of(w, es, a->t.pairs, d->head_dim, a->rows, d->heads);
   void* args[] = {a};
-  return launch(kernel_of(bf16, w, adjacent, a->gp != nullptr), (a->rows + a->cut.rows - 1) / a->cut.rows, args,
+  const int64_t groups = a->gp != nullptr ? 1 : a->cut.groups;
+  return launch(kernel_of(bf16, w, adjacent, a->gp != nullptr), (a->rows + a->cut.rows - 1) / a->cut.rows * groups, args,
                 &a->first, stream)
              ? DCN_OK
              : DCN_E_HIP;

@@ -411,7 +411,7 @@ int dcn_group_norm_backward(const dcn_norm_desc* desc, const void* x, const void
  *    pairs (for BLOCKS each section) and head_dim.
  * DCN_E_ARG: an invalid descriptor (a negative size or stride, no head, axes outside 1 .. 4, a section
  * below 1, 2 pairs > head_dim, an unknown layout or position type) or a NULL required pointer;
- * DCN_E_UNSUPPORTED: another dtype, head_dim above 65536 or 2^31 rows of heads; DCN_E_HIP as elsewhere;
+ * DCN_E_UNSUPPORTED: another dtype, head_dim above 4096 or 2^31 rows of heads; DCN_E_HIP as elsewhere;
  * all checked before any launch.  batch or length 0: nothing is launched. */
 enum dcn_rotary_layout { DCN_ROTARY_HALVES = 0, DCN_ROTARY_ADJACENT = 1, DCN_ROTARY_BLOCKS = 2 };
 enum dcn_position_type { DCN_POSITION_F32 = 0, DCN_POSITION_I32 = 1 };
@@ -452,7 +452,7 @@ int dcn_rotary_backward(const dcn_rotary_desc* desc, const void* grad_out, const
  * element at a time, the widest that fits C and the addresses.
  * DCN_E_ARG: an invalid descriptor (a negative size, no channel, eps negative or not finite, an unknown
  * norm or gate) or a NULL required pointer; DCN_E_UNSUPPORTED: another dtype, more than 8192 channels,
- * 2^31 rows, or 65536 batch elements with DCN_GATE_BATCH; DCN_E_HIP as elsewhere; all checked before any
+ * 2^31 rows, or more than 65530 batch elements with DCN_GATE_BATCH; DCN_E_HIP as elsewhere; all checked before any
  * launch.  No rows: nothing is launched. */
 enum dcn_row_norm { DCN_NORM_NONE = 0, DCN_NORM_RMS = 1, DCN_NORM_LAYER = 2 };
 enum dcn_gate { DCN_GATE_NONE = 0, DCN_GATE_BATCH = 1, DCN_GATE_FULL = 2 };
@@ -528,7 +528,8 @@ int dcn_paged_append(const dcn_append_desc* desc, const void* q, const void* k, 
  * page of the cache are left out; a sequence with no position left gets zeros and lse -infinity.  What the
  * cache holds behind a sequence's length, infinities and NaN included, does not matter.  Long sequences are
  * split over workgroups by the lengths on the device, and the parts joined in order: equal calls give equal
- * bits.  Arithmetic as for dcn_cross_attention.  The workspace (256-byte aligned) holds the parts.
+ * bits.  Arithmetic as for dcn_cross_attention, but for bf16 a weight enters the second product as two bf16
+ * operands (2^-15 of it is lost).  The workspace (256-byte aligned, 0 bytes for short tables) holds the parts.
  * DCN_E_ARG, DCN_E_UNSUPPORTED (head_dim > 128, sizes as for dcn_paged_append), DCN_E_WORKSPACE, DCN_E_HIP
  * as for dcn_cross_attention.  batch 0: nothing is launched. */
 typedef struct dcn_paged_desc {
