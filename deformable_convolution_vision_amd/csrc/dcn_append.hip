@@ -3,8 +3,8 @@
 //
 // Row (b, i) of the new tokens is position s = starts[b] + i of its sequence: row s % page_size of
 // page page_table[b][s / page_size].  Queries, keys and values are one list of heads of that row, of which
-// values are copied.  A workgroup's rows share their angles and places in the LDS; the elements' loads are
-// under way while starts, table entries and angles are found.
+// values are not turned.  A workgroup's rows share their angles and places in the LDS; the first elements'
+// loads are under way while starts, table entries and angles are found (turn_heads).
 //
 // A table entry that is no page of the cache, or a position outside the table, drops the row: the
 // check stands before the address is formed.
@@ -12,12 +12,16 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "dcn.h"
 #include "dcn_rotary.h"
 
 namespace dcn {
 namespace rotary {
 namespace {
+
+constexpr int kRows = 256;   // the most rows of a workgroup
 
 struct AppendArgs {
   const void *q, *k, *v;
@@ -27,117 +31,88 @@ struct AppendArgs {
   Turns t;
   Cut cut;
   int64_t qs[3], ks[3], vs[3], kps[3], vps[3], ts;
-  int64_t rows, first;     // B * max(L, 1); workgroups of launches before this one
+  uint32_t first;          // workgroups of launches before this one
+  int rows;                // B * max(L, 1)
   int L, per;              // rows of a sequence, and max(L, 1)
   int Hq, Hkv, D;
   int num_pages, page_size, max_pages;
 };
 
-template <typename T, int PV, bool ADJ>
+template <typename T, int WV, int PV, bool ADJ>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
-  using V = Vec<T, PV>;
-  constexpr int kUnits = units_of(sizeof(V));
-  __shared__ float2 cs[kTurns];
+  extern __shared__ float2 cs[];
+  __shared__ __attribute__((aligned(16))) unsigned char held[4 * kWave];
   __shared__ int pages[kRows], places[kRows];      // of the rows; page -1: the row has none
-  const int tid = threadIdx.x;
-  const int64_t at = a.first + blockIdx.x, row0 = at / a.cut.groups * a.cut.rows;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(a.cut.rows), a.rows - row0));
-  const int h0 = static_cast<int>(at % a.cut.groups) * a.cut.heads, heads = min(a.cut.heads, a.Hq + 2 * a.Hkv - h0);
-  const int units = a.L > 0 ? rows * static_cast<int>(a.cut.by_row.d) : 0;
-  const auto unit = [&](int u, int& r, int& h, int& chunk) {   // false: no unit
-    r = a.cut.by_row.of(u);
-    const int in_row = u - r * static_cast<int>(a.cut.by_row.d);
-    h = a.cut.by_chunks.of(in_row);
-    chunk = in_row - h * a.cut.chunks;
-    const bool live = u < units && h < heads;
-    h += h0;
-    return live;
-  };
-  V v1[kUnits], v2[kUnits];
-  const auto load = [&](int u0) {
-#pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      int r, h, chunk;
-      if (!unit(u0 + k * 256 + tid, r, h, chunk)) continue;
-      const uint32_t row = static_cast<uint32_t>(row0 + r), b = row / static_cast<uint32_t>(a.per), i = row - b * a.per;
-      const Place p = place_of<PV>(a.t, chunk, a.cut.rotated);
-      const T* x = h < a.Hq           ? static_cast<const T*>(a.q) + b * a.qs[0] + i * a.qs[1] + h * a.qs[2]
-                   : h < a.Hq + a.Hkv ? static_cast<const T*>(a.k) + b * a.ks[0] + i * a.ks[1] + (h - a.Hq) * a.ks[2]
-                                      : static_cast<const T*>(a.v) + b * a.vs[0] + i * a.vs[1] + (h - a.Hq - a.Hkv) * a.vs[2];
-      v1[k] = *reinterpret_cast<const V*>(x + p.e1);
-      if (p.e2 < a.D) v2[k] = *reinterpret_cast<const V*>(x + p.e2);
-    }
-  };
-  load(0);
-  for (int r = tid; r < rows; r += 256) {
-    const uint32_t row = static_cast<uint32_t>(row0 + r), b = row / static_cast<uint32_t>(a.per), i = row - b * a.per;
-    const int start = a.starts[b];
-    int count = a.L, page = -1, place = 0;
-    if (a.counts != nullptr) count = min(max(a.counts[b], 0), a.L);
-    if (i == 0 && h0 == 0 && a.lengths != nullptr) a.lengths[b] = start + count;
-    const int64_t s = static_cast<int64_t>(start) + i;
-    if (static_cast<int>(i) < count && s >= 0 && s < static_cast<int64_t>(a.max_pages) * a.page_size) {
-      const int n = static_cast<int>(s) / a.page_size;
-      place = static_cast<int>(s) - n * a.page_size;
-      page = a.table[b * a.ts + n];
-    }
-    pages[r] = page >= 0 && page < a.num_pages ? page : -1;
-    places[r] = place;
-  }
-  if (units == 0) return;
-  for (int i = tid; i < rows * a.t.pairs; i += 256) {
-    const int r = a.cut.by_pairs.of(i), pair = i - r * a.t.pairs;
-    const uint32_t row = static_cast<uint32_t>(row0 + r), b = row / static_cast<uint32_t>(a.per), l = row - b * a.per;
-    const double pos = a.t.positions != nullptr ? position_of(a.t, b, l, axis_of(a.t, pair))
-                                                : static_cast<double>(static_cast<int64_t>(a.starts[b]) + l);
-    float c, s;
-    cos_sin(pos, a.t.freq[pair], c, s);
-    cs[i] = make_float2(c, s);
-  }
-  __syncthreads();
-  for (int u0 = 0; u0 < units; u0 += kUnits * 256) {
-    if (u0 > 0) load(u0);
-#pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      int r, h, chunk;
-      if (!unit(u0 + k * 256 + tid, r, h, chunk)) continue;
-      const Place p = place_of<PV>(a.t, chunk, a.cut.rotated);
-      const int page = pages[r], place = places[r];
-      T* y = h < a.Hq           ? static_cast<T*>(a.qo) + ((row0 + r) * a.Hq + h) * a.D
-             : h < a.Hq + a.Hkv ? static_cast<T*>(a.kp) + page * a.kps[0] + place * a.kps[1] + (h - a.Hq) * a.kps[2]
+  const uint32_t at = a.first + blockIdx.x, block = at / a.cut.groups;
+  const int row0 = static_cast<int>(block) * a.cut.rows, rows = min(a.cut.rows, a.rows - row0);
+  const int b0 = static_cast<int>(static_cast<uint32_t>(row0) / static_cast<uint32_t>(a.per)), l0 = row0 - b0 * a.per;
+  const int h0 = static_cast<int>(at - block * a.cut.groups) * a.cut.heads, heads = min(a.cut.heads, a.Hq + 2 * a.Hkv - h0);
+  // (a ragged batch: all rows behind the tokens of their sequence; only their queries are read)
+  const bool dead = a.counts != nullptr && l0 + rows <= a.per && l0 >= a.counts[b0];
+  turn_heads<T, WV, PV, ADJ>(
+      a.t, a.cut, a.L > 0 ? rows * a.cut.heads : 0, reinterpret_cast<T*>(held + (threadIdx.x >> 6) * kWave), cs,
+      [&](int n) {
+        const int r = a.cut.by_heads.of(n), h = h0 + min(n - r * a.cut.heads, heads - 1);
+        const Row w = row_of(b0, l0, r, a.per);
+        const int b = w.b, i = w.l;
+        if (dead && h >= a.Hq) return static_cast<const T*>(nullptr);
+        return h < a.Hq           ? static_cast<const T*>(a.q) + b * a.qs[0] + i * a.qs[1] + h * a.qs[2]
+               : h < a.Hq + a.Hkv ? static_cast<const T*>(a.k) + b * a.ks[0] + i * a.ks[1] + (h - a.Hq) * a.ks[2]
+                                  : static_cast<const T*>(a.v) + b * a.vs[0] + i * a.vs[1] + (h - a.Hq - a.Hkv) * a.vs[2];
+      },
+      [&](int n) -> T* {
+        const int r = a.cut.by_heads.of(n), i = n - r * a.cut.heads, h = h0 + i;
+        if (i >= heads) return nullptr;
+        if (h < a.Hq) return static_cast<T*>(a.qo) + (static_cast<int64_t>(row0 + r) * a.Hq + h) * a.D;
+        const int page = pages[r], place = places[r];
+        if (page < 0) return nullptr;
+        return h < a.Hq + a.Hkv ? static_cast<T*>(a.kp) + page * a.kps[0] + place * a.kps[1] + (h - a.Hq) * a.kps[2]
                                 : static_cast<T*>(a.vp) + page * a.vps[0] + place * a.vps[1] + (h - a.Hq - a.Hkv) * a.vps[2];
-      if (chunk < a.cut.rotated && h < a.Hq + a.Hkv) {
-        float c[PV], s[PV], x1[PV], x2[PV], y1[PV], y2[PV];
-        const float2* turns = cs + r * a.t.pairs + chunk * PV;
-#pragma unroll
-        for (int j = 0; j < PV; ++j) {
-          c[j] = turns[j].x;
-          s[j] = turns[j].y;
+      },
+      [&](int n) {
+        const int r = a.cut.by_heads.of(n);
+        return h0 + n - r * a.cut.heads < a.Hq + a.Hkv ? r : -1;
+      },
+      [&] {
+        for (int r = threadIdx.x; r < rows; r += 256) {
+          const Row w = row_of(b0, l0, r, a.per);
+          const int b = w.b, i = w.l, start = a.starts[b];
+          int count = a.L, page = -1, place = 0;
+          if (a.counts != nullptr) count = min(max(a.counts[b], 0), a.L);
+          if (i == 0 && h0 == 0 && a.lengths != nullptr) a.lengths[b] = start + count;
+          const int64_t s = static_cast<int64_t>(start) + i;
+          if (i < count && s >= 0 && s < static_cast<int64_t>(a.max_pages) * a.page_size) {
+            const int n = static_cast<int>(s) / a.page_size;
+            place = static_cast<int>(s) - n * a.page_size;
+            page = a.table[b * a.ts + n];
+          }
+          pages[r] = page >= 0 && page < a.num_pages ? page : -1;
+          places[r] = place;
         }
-        pairs_of<T, PV, ADJ>(v1[k], v2[k], x1, x2);
-        turn<PV>(c, s, x1, x2, y1, y2);
-        vectors_of<T, PV, ADJ>(y1, y2, v1[k], v2[k]);
-      }
-      if (h < a.Hq || page >= 0) {
-        *reinterpret_cast<V*>(y + p.e1) = v1[k];
-        if (p.e2 < a.D) *reinterpret_cast<V*>(y + p.e2) = v2[k];
-      }
-    }
-  }
+        if (a.L > 0)
+          form_turns(a.t, a.cut.log_pairs, rows, 1.f, cs, [&](int r, int axis) {
+            const Row w = row_of(b0, l0, r, a.per);
+            return a.t.positions != nullptr ? position_of(a.t, w.b, w.l, axis)
+                                            : static_cast<double>(static_cast<int64_t>(a.starts[w.b]) + w.l);
+          });
+        __syncthreads();
+      });
 }
 
-template <typename T, int PV>
+template <typename T, int WV, int PV>
 const void* kernel_of(bool adjacent) {
-  return adjacent ? reinterpret_cast<const void*>(&append_kernel<T, PV, true>)
-                  : reinterpret_cast<const void*>(&append_kernel<T, PV, false>);
+  return adjacent && PV > 1 ? reinterpret_cast<const void*>(&append_kernel<T, WV, PV, (PV > 1)>)
+                            : reinterpret_cast<const void*>(&append_kernel<T, WV, PV, false>);
 }
-const void* kernel_of(bool bf16, int width, bool adjacent) {
-  if (bf16)
-    return width == 8   ? kernel_of<uint16_t, 8>(adjacent)
-           : width == 4 ? kernel_of<uint16_t, 4>(adjacent)
-           : width == 2 ? kernel_of<uint16_t, 2>(adjacent)
-                        : kernel_of<uint16_t, 1>(false);
-  return width == 4 ? kernel_of<float, 4>(adjacent) : width == 2 ? kernel_of<float, 2>(adjacent) : kernel_of<float, 1>(false);
+const void* kernel_of(bool bf16, int wv, int pv, bool adjacent) {
+  if (bf16) {
+    if (wv == 8) return pv == 8 ? kernel_of<uint16_t, 8, 8>(adjacent) : pv == 2 ? kernel_of<uint16_t, 8, 2>(adjacent)
+                                                                                : kernel_of<uint16_t, 8, 1>(adjacent);
+    if (wv == 2) return pv == 2 ? kernel_of<uint16_t, 2, 2>(adjacent) : kernel_of<uint16_t, 2, 1>(adjacent);
+    return kernel_of<uint16_t, 1, 1>(adjacent);
+  }
+  if (wv == 4) return pv == 4 ? kernel_of<float, 4, 4>(adjacent) : kernel_of<float, 4, 1>(adjacent);
+  return kernel_of<float, 1, 1>(adjacent);
 }
 
 int check(const dcn_append_desc* d) {
@@ -154,7 +129,7 @@ int check(const dcn_append_desc* d) {
   if (d->dtype != DCN_F32 && d->dtype != DCN_BF16) return DCN_E_UNSUPPORTED;
   const double big = 2147483647.;
   const double heads = static_cast<double>(d->query_heads) + 2. * d->key_heads, length = d->length > 0 ? d->length : 1;
-  if (d->head_dim > 2 * kTurns || heads > big || d->batch > big || length > big || d->batch * length * heads > big ||
+  if (d->head_dim > kMostD || heads > big || d->batch > big || length > big || d->batch * length * heads > big ||
       d->num_pages > big || d->page_size > big || static_cast<double>(d->max_pages) * d->page_size > big)
     return DCN_E_UNSUPPORTED;
   return DCN_OK;
@@ -200,7 +175,7 @@ extern "C" int dcn_paged_append(const dcn_append_desc* d, const void* q, const v
   a.ts = d->table_stride;
   a.L = static_cast<int>(d->length);
   a.per = rows ? a.L : 1;
-  a.rows = d->batch * a.per;
+  a.rows = static_cast<int>(d->batch * a.per);
   a.Hq = static_cast<int>(d->query_heads);
   a.Hkv = static_cast<int>(d->key_heads);
   a.D = static_cast<int>(d->head_dim);
@@ -210,14 +185,18 @@ extern "C" int dcn_paged_append(const dcn_append_desc* d, const void* q, const v
   a.t = turns_of(d->axes, d->sections, d->layout, d->position_type, d->position_stride, positions, frequencies);
   const bool bf16 = d->dtype == DCN_BF16;
   const int es = bf16 ? 2 : 4;
-  int w = width_of(a.t, d->sections, d->head_dim, es);
+  int w = 16 / es;
+  while (w > 1 && d->head_dim % w != 0) w = narrower(w, es);
   for (const void* p : {k, v, static_cast<const void*>(key_pages), static_cast<const void*>(value_pages)}) w = fit(w, es, p);
-  for (const int64_t* s : {a.ks, a.vs, a.kps, a.vps}) w = fit(w, s, 3);
-  if (a.Hq > 0) w = fit(fit(fit(w, es, q), es, q_out), a.qs, 3);
-  a.cut = cut_of(w, es, a.t.pairs, d->head_dim, a.rows, a.Hq + 2 * a.Hkv);
+  for (const int64_t* s : {a.ks, a.vs, a.kps, a.vps}) w = fit(w, es, s, 3);
+  if (a.Hq > 0) w = fit(fit(fit(w, es, q), es, q_out), es, a.qs, 3);
+  const int pv = pairs_at_once(a.t, d->sections, w, es);
+  a.cut = cut_of(w, pv, es, a.t.pairs, d->head_dim, a.rows, a.Hq + 2 * a.Hkv);
+  a.cut.rows = std::min(a.cut.rows, kRows);
   void* args[] = {&a};
-  return launch(kernel_of(bf16, w, d->layout == DCN_ROTARY_ADJACENT),
-                (a.rows + a.cut.rows - 1) / a.cut.rows * a.cut.groups, args, &a.first, stream)
+  return launch(kernel_of(bf16, w, pv, d->layout == DCN_ROTARY_ADJACENT),
+                (static_cast<int64_t>(a.rows) + a.cut.rows - 1) / a.cut.rows * a.cut.groups, args,
+                turns_bytes(a.cut, a.t), &a.first, stream)
              ? DCN_OK
              : DCN_E_HIP;
 }

@@ -3,8 +3,8 @@
 // workgroups, and the host-side checks.  Not part of the public ABI.
 //
 // A workgroup takes a few rows.  It forms the cosines and sines of their angles once, in the LDS, where
-// every head of the rows reads them; the elements' loads are under way meanwhile.  A thread's unit is a
-// chunk of PV pairs of one head: two vectors of PV elements, wherever the layout has them.
+// every head of the rows reads them.  Heads pass through the LDS (turn_heads): memory is read and written in
+// whole vectors, one after the other, whatever pairs the layout makes of the elements.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -87,17 +87,12 @@ struct Div {
   __device__ __forceinline__ int of(int n) const { return d == 1 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), m)); }
 };
 
-// The first elements of a chunk's two vectors.
+// The first elements of a chunk's two vectors: PV pairs from p on.
 struct Place {
   int e1, e2;
 };
 template <int PV>
-__device__ __forceinline__ Place place_of(const Turns& t, int chunk, int rotated) {
-  if (chunk >= rotated) {   // behind the pairs: copied
-    const int e = 2 * t.pairs + (chunk - rotated) * 2 * PV;
-    return {e, e + PV};
-  }
-  const int p = chunk * PV;
+__device__ __forceinline__ Place place_of(const Turns& t, int p) {
   if (t.layout == DCN_ROTARY_HALVES) return {p, p + t.pairs};
   if (t.layout == DCN_ROTARY_ADJACENT) return {2 * p, 2 * p + PV};
   const int a = axis_of(t, p);
@@ -142,6 +137,130 @@ __device__ __forceinline__ void turn(const float (&c)[PV], const float (&s)[PV],
   }
 }
 
+// Row r of a workgroup whose first row is l0 of batch element b0 (L rows each).
+struct Row {
+  int b, l;
+};
+__device__ __forceinline__ Row row_of(int b0, int l0, int r, int L) {
+  Row w = {b0, l0 + r};
+  if (w.l >= L) {          // (seldom: the division is left out of the common case)
+    const int n = static_cast<int>(static_cast<uint32_t>(w.l) / static_cast<uint32_t>(L));
+    w.b += n;
+    w.l -= n * L;
+  }
+  return w;
+}
+
+// Cosines and sines of the rows' angles into the LDS, [row][pair], by all 256 threads: a thread keeps its pair and
+// takes rows in turn, four positions on their way at a time.  position(row): of the pair's axis.
+template <typename P>
+__device__ __forceinline__ void form_turns(const Turns& t, int log_pairs, int rows, float sign, float2* cs, P position) {
+  const int step = 256 >> log_pairs;
+  for (int pair = threadIdx.x & ((1 << log_pairs) - 1); pair < t.pairs; pair += 256) {
+    const float f = t.freq[pair];
+    const int axis = axis_of(t, pair);
+    for (int r0 = threadIdx.x >> log_pairs; r0 < rows; r0 += 4 * step) {
+      double p[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) p[k] = r0 + k * step < rows ? position(r0 + k * step, axis) : 0.;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (r0 + k * step >= rows) break;
+        float c, s;
+        cos_sin(p[k], f, c, s);
+        cs[(r0 + k * step) * t.pairs + pair] = make_float2(c, sign * s);
+      }
+    }
+  }
+}
+
+// How rows and heads fall to workgroups of 256.
+constexpr int kTurns = 2048;      // cosines and sines of a workgroup at most: 16 KB
+constexpr int kWave = 2048;       // bytes of heads of a wave in the LDS;
+constexpr int held_by(int bytes) { return bytes == 2 ? kWave / 2 : kWave; }   // so many are used with vectors of so many
+constexpr int kMostD = 512;       // elements of a head
+struct Cut {
+  int rows, heads, groups;        // of a workgroup: rows, and heads of each, of which a row has `groups` groups
+  int at_once;                    // heads of a wave at a time
+  int vectors, chunks;            // of a head
+  Div by_heads, by_vectors, by_chunks;
+  int log_pairs;                  // 2^log_pairs: threads that share a row's angles out, up to 256
+};
+
+// Orders a wave's LDS accesses of different lanes (no instruction: a wave's are carried out in order).
+__device__ __forceinline__ void wave_order() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
+// So many bytes in one register access.
+template <int BYTES>
+struct Bytes;
+template <>
+struct Bytes<16> { typedef uint32_t type __attribute__((ext_vector_type(4))); };
+template <>
+struct Bytes<4> { using type = uint32_t; };
+template <>
+struct Bytes<2> { using type = uint16_t; };
+
+// Moves heads 0 .. n-1 of a workgroup, at_once of them by each wave in turn, from from(i) to to(i) (null: not
+// written), turned by the angles of row turned(i) (below 0: not turned).  WV: elements of a vector of memory; PV:
+// pairs of a chunk, a vector of the LDS.  between(): called by every thread once the first heads' loads are under
+// way; forms the angles.  The next heads' loads are under way while a wave's heads are turned.
+template <typename T, int WV, int PV, bool ADJ, typename From, typename To, typename Turned, typename Between>
+__device__ __forceinline__ void turn_heads(const Turns& t, const Cut& c, int n, T* lds, const float2* cs, From from, To to,
+                                           Turned turned, Between between) {
+  constexpr int NV = held_by(WV * static_cast<int>(sizeof(T))) / (64 * WV * static_cast<int>(sizeof(T)));
+  using M = typename Bytes<WV * static_cast<int>(sizeof(T))>::type;
+  using V = Vec<T, PV>;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), step = 4 * c.at_once,
+            vectors = c.at_once * c.vectors, chunks = c.at_once * c.chunks, D = c.vectors * WV;
+  M held[NV];
+  const auto fetch = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = k * 64 + lane, g = c.by_vectors.of(v);
+      if (v >= vectors || i0 + g >= n) continue;
+      const T* x = from(i0 + g);
+      if (x != nullptr) held[k] = *reinterpret_cast<const M*>(x + (v - g * c.vectors) * WV);
+    }
+  };
+  const int first = wave * c.at_once;
+  fetch(first);
+  between();
+  for (int i0 = first; i0 < n; i0 += step) {
+    wave_order();
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (k * 64 + lane < vectors) *reinterpret_cast<M*>(lds + (k * 64 + lane) * WV) = held[k];
+    wave_order();
+    if (i0 + step < n) fetch(i0 + step);
+    for (int q = lane; q < chunks; q += 64) {
+      const int g = c.by_chunks.of(q), p0 = (q - g * c.chunks) * PV, row = i0 + g < n ? turned(i0 + g) : -1;
+      if (row < 0) continue;
+      const Place p = place_of<PV>(t, p0);
+      V u = *reinterpret_cast<const V*>(lds + g * D + p.e1), v = *reinterpret_cast<const V*>(lds + g * D + p.e2);
+      const float2* turns = cs + row * t.pairs + p0;
+      float co[PV], si[PV], x1[PV], x2[PV], y1[PV], y2[PV];
+#pragma unroll
+      for (int j = 0; j < PV; ++j) {
+        co[j] = turns[j].x;
+        si[j] = turns[j].y;
+      }
+      pairs_of<T, PV, ADJ>(u, v, x1, x2);
+      turn<PV>(co, si, x1, x2, y1, y2);
+      vectors_of<T, PV, ADJ>(y1, y2, u, v);
+      *reinterpret_cast<V*>(lds + g * D + p.e1) = u;
+      *reinterpret_cast<V*>(lds + g * D + p.e2) = v;
+    }
+    wave_order();
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = k * 64 + lane, g = c.by_vectors.of(v);
+      if (v >= vectors || i0 + g >= n) continue;
+      T* y = to(i0 + g);
+      if (y != nullptr) *reinterpret_cast<M*>(y + (v - g * c.vectors) * WV) = *reinterpret_cast<const M*>(lds + v * WV);
+    }
+  }
+}
+
 // ---- host side
 
 // Checks of the rotation's fields: DCN_OK or a negative status.
@@ -176,72 +295,68 @@ inline Turns turns_of(int32_t axes, const int32_t* sections, int32_t layout, int
   return t;
 }
 
-// The widest vectors, in elements, that a rotation of these sections allows: the pairs of a chunk are
-// then whole within each run of the layout.  `fit` halves it further for addresses and strides.
-inline int width_of(const Turns& t, const int32_t* sections, int64_t head_dim, int es) {
-  int w = 16 / es;
-  while (w > 1 && (t.pairs % w != 0 || head_dim % w != 0)) w /= 2;
+// Elements of the vectors that fit memory at an address or along strides, of those that there are kernels for:
+// 16 bytes, 4 (bf16), one element.
+inline int narrower(int w, int es) { return es == 2 && w > 2 ? 2 : 1; }
+inline int fit(int w, int es, const void* p) {
+  while (w > 1 && reinterpret_cast<uintptr_t>(p) % (static_cast<unsigned>(w) * es) != 0) w = narrower(w, es);
+  return w;
+}
+inline int fit(int w, int es, const int64_t* strides, int n) {
+  for (int i = 0; i < n; ++i)
+    while (w > 1 && strides[i] % w != 0) w = narrower(w, es);
+  return w;
+}
+// Pairs of a chunk: as many as a vector of memory has elements, if every run of the layout is whole chunks.
+inline int pairs_at_once(const Turns& t, const int32_t* sections, int w, int es) {
+  while (w > 1 && t.pairs % w != 0) w = narrower(w, es);
   if (t.layout == DCN_ROTARY_BLOCKS)
     for (int a = 0; a < t.axes; ++a)
-      while (w > 1 && sections[a] % w != 0) w /= 2;
-  return w;
-}
-inline int fit(int w, int es, const void* p) {
-  while (w > 1 && reinterpret_cast<uintptr_t>(p) % (static_cast<unsigned>(w) * es) != 0) w /= 2;
-  return w;
-}
-inline int fit(int w, const int64_t* strides, int n) {
-  for (int i = 0; i < n; ++i)
-    while (w > 1 && strides[i] % w != 0) w /= 2;
+      while (w > 1 && sections[a] % w != 0) w = narrower(w, es);
   return w;
 }
 
-// How rows and heads fall to workgroups of 256: `rows` rows and `heads` heads of each, of which a row has
-// `groups`; a head has `chunks` chunks, `rotated` of them of pairs, the others copied.
-constexpr int kTurns = 2048;      // cosines and sines of a workgroup: 16 KB
-// Units of a thread under way at a time, by the bytes of a vector.  Two of 16 bytes fill the memory's queues and leave
-// workgroups small enough for an even last round (rotary_c3_batch8 with 1, 2, 4 units: 32.9, 33.0, 36.6
-// us); narrower ones take four (2 bytes, 16800 rows of 8 heads of 37: 21.7, 13.5, 12.1 us).
-constexpr int units_of(int bytes) { return bytes == 16 ? 2 : 4; }
-constexpr int kRows = 64;         // the most rows of a workgroup
-struct Cut {
-  int chunks, rotated, rows, heads, groups;
-  Div by_chunks, by_row, by_pairs;   // by_row: heads * chunks
-};
 inline Div div_by(int64_t d) {
   return {static_cast<uint32_t>(d < 1 ? 1 : d), static_cast<uint32_t>(d < 2 ? 0 : (int64_t{1} << 32) / d + 1)};
 }
-// Rows share nothing, so a workgroup takes as many as fill its threads' units; where there are fewer than
-// four workgroups a CU then, fewer rows each, and fewer heads of one row.
-inline Cut cut_of(int width, int es, int pairs, int64_t head_dim, int64_t rows, int64_t heads) {
+// A workgroup takes two or three times what its waves hold, in whole rows where they are short: of these the number
+// that leaves the least of the last turn unused, fewer turns where that is equal (24 heads of 128, 33600 rows: 2
+// rows, 3/4 of two turns, 108 us; 4 rows, three turns, 90).  Four turns were slower than three wherever tried.  Where that leaves fewer
+// than four workgroups a CU, fewer rows each, and fewer heads of one row, down to what a wave holds.
+inline Cut cut_of(int wv, int pv, int es, int pairs, int64_t head_dim, int64_t rows, int64_t heads) {
   Cut c{};
-  c.rotated = pairs / width;
-  c.chunks = c.rotated + static_cast<int>((head_dim - 2 * pairs + 2 * width - 1) / (2 * width));
-  const int64_t most = units_of(width * es) * 256, wanted = 4 * 256;
-  int64_t h = heads * c.chunks <= most ? heads : most / c.chunks > 1 ? most / c.chunks : 1;
-  if (rows * ((heads + h - 1) / h) < wanted && h * c.chunks > 256) h = 256 / c.chunks > 1 ? 256 / c.chunks : 1;
-  int64_t r = most / (h * c.chunks);
-  if (pairs > 0 && r > kTurns / pairs) r = kTurns / pairs;
-  const int64_t least = (256 + h * c.chunks - 1) / (h * c.chunks);   // a unit for each thread
-  if (r > rows / wanted) r = rows / wanted > least ? rows / wanted : r < least ? r : least;
-  if (r > kRows) r = kRows;
-  c.rows = static_cast<int>(r < 1 ? 1 : r);
+  c.at_once = static_cast<int>(held_by(wv * es) / (head_dim * es));
+  c.vectors = static_cast<int>(head_dim / wv);
+  c.chunks = pairs / pv;
+  const int64_t turn = int64_t{4} * c.at_once, wanted = 4 * 256;
+  int64_t h = heads < 2 * turn ? heads : 2 * turn;
+  while (h > c.at_once && rows * ((heads + h - 1) / h) < wanted) h = (h + 1) / 2;
+  int64_t most = 3 * turn / h;
+  if (pairs > 0 && most > kTurns / pairs) most = kTurns / pairs;
+  if (most > rows / wanted) most = rows / wanted;
+  const auto turns = [&](int64_t r) { return (r * h + turn - 1) / turn; };
+  int64_t best = most > 1 ? most : 1;
+  for (int64_t r = best - 1; r >= 1 && turns(r) >= 2; --r)
+    if (r * turns(best) >= best * turns(r)) best = r;      // rows a turn: as many, in fewer turns
+  c.rows = static_cast<int>(best);
   c.heads = static_cast<int>(h);
   c.groups = static_cast<int>((heads + h - 1) / h);
+  c.by_heads = div_by(h);
+  c.by_vectors = div_by(c.vectors);
   c.by_chunks = div_by(c.chunks);
-  c.by_row = div_by(h * c.chunks);
-  c.by_pairs = div_by(pairs);
+  while (c.log_pairs < 8 && (1 << c.log_pairs) < pairs) ++c.log_pairs;
   return c;
 }
 
 // Launches n workgroups of 256 threads; a dispatch counts its threads in 32 bits, so beyond 2^23 of them
 // they go in several launches, each of which is told (*first) how many went before it.
-inline bool launch(const void* fn, int64_t n, void** args, int64_t* first, hipStream_t stream) {
+inline size_t turns_bytes(const Cut& c, const Turns& t) { return static_cast<size_t>(c.rows) * t.pairs * sizeof(float2); }
+inline bool launch(const void* fn, int64_t n, void** args, size_t lds, uint32_t* first, hipStream_t stream) {
   constexpr int64_t kMost = int64_t{1} << 23;
   for (int64_t at = 0; at < n; at += kMost) {
-    *first = at;
+    *first = static_cast<uint32_t>(at);
     const int64_t now = n - at < kMost ? n - at : kMost;
-    if (hipLaunchKernel(fn, dim3(static_cast<unsigned>(now)), dim3(256), args, 0, stream) != hipSuccess) return false;
+    if (hipLaunchKernel(fn, dim3(static_cast<unsigned>(now)), dim3(256), args, lds, stream) != hipSuccess) return false;
   }
   return true;
 }

@@ -12,11 +12,14 @@
 //
 //   grad_pos[b][l][a] = sum over heads and the axis's pairs of freq[p] (gx2 x1 - gx1 x2).
 //
-// For the position's gradient a workgroup has all heads of its rows, and each unit leaves its sum for each
-// axis in the LDS, where one thread for each row and axis adds them in order.
+// The rotation, either way, is rotary_kernel (turn_heads does the work).  With the position's gradient it is
+// rotary_grad_kernel: a workgroup has all heads of its rows, a thread takes chunks of pairs straight from memory and
+// leaves each one's sum for each axis in the LDS, where one thread for each row and axis adds them in order.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "dcn.h"
 #include "dcn_rotary.h"
@@ -28,76 +31,119 @@ namespace {
 struct Args {
   const void* x;           // forward: x; backward: grad_out
   const void* x0;          // backward of positions: x
-  void* out;               // out or grad_x (backward: may be null)
+  void* out;               // out or grad_x (backward of positions: may be null)
   float* gp;               // [B][L][axes]
   Turns t;
   Cut cut;
   int64_t xs[3], x0s[3];   // strides of x and x0: batch, row, head
-  int64_t rows, first;     // B * L; workgroups of launches before this one
+  uint32_t first;          // workgroups of launches before this one
+  int rows;                // B * L
   int L, H, D;
   float sign;              // 1, or -1 to turn back
+  // rotary_grad_kernel: chunks of a head, `turned` of them of pairs and the others copied
+  int turned;
+  Div by_row;              // chunks of a row
 };
 
-template <typename T, int PV, bool ADJ, bool POS>
+template <typename T, int WV, int PV, bool ADJ>
 __global__ __launch_bounds__(256) void rotary_kernel(Args a) {
+  extern __shared__ float2 cs[];
+  __shared__ __attribute__((aligned(16))) unsigned char held[4 * kWave];
+  const uint32_t at = a.first + blockIdx.x, block = at / a.cut.groups;
+  const int row0 = static_cast<int>(block) * a.cut.rows, rows = min(a.cut.rows, a.rows - row0);
+  const int h0 = static_cast<int>(at - block * a.cut.groups) * a.cut.heads, heads = min(a.cut.heads, a.H - h0);
+  const int b0 = static_cast<int>(static_cast<uint32_t>(row0) / static_cast<uint32_t>(a.L)), l0 = row0 - b0 * a.L;
+  // head i of the workgroup: its row and place there (the last group of heads may be smaller than the others)
+  const auto row = [&](int i) { return a.cut.by_heads.of(i); };
+  const auto head = [&](int i, int r) { return i - r * a.cut.heads; };
+  turn_heads<T, WV, PV, ADJ>(
+      a.t, a.cut, rows * a.cut.heads, reinterpret_cast<T*>(held + (threadIdx.x >> 6) * kWave), cs,
+      [&](int i) {
+        const int r = row(i), h = min(head(i, r), heads - 1);
+        const Row w = row_of(b0, l0, r, a.L);
+        return static_cast<const T*>(a.x) + w.b * a.xs[0] + w.l * a.xs[1] + (h0 + h) * a.xs[2];
+      },
+      [&](int i) {
+        const int r = row(i), h = head(i, r);
+        return h < heads ? static_cast<T*>(a.out) + (static_cast<int64_t>(row0 + r) * a.H + h0 + h) * a.D : nullptr;
+      },
+      row,
+      [&] {
+        form_turns(a.t, a.cut.log_pairs, rows, a.sign, cs, [&](int r, int axis) {
+          const Row w = row_of(b0, l0, r, a.L);
+          return position_of(a.t, w.b, w.l, axis);
+        });
+        __syncthreads();
+      });
+}
+
+// Chunks of a thread under way at a time.
+constexpr int kUnits = 2;
+
+template <typename T, int PV, bool ADJ>
+__global__ __launch_bounds__(256) void rotary_grad_kernel(Args a) {
   using V = Vec<T, PV>;
-  constexpr int kUnits = units_of(sizeof(V));
-  __shared__ float2 cs[kTurns];
-  __shared__ float red[POS ? 4 * kUnits * 256 : 1];
+  extern __shared__ float2 cs[];
+  __shared__ float red[4 * kUnits * 256];
   const int tid = threadIdx.x;
-  const int64_t at = a.first + blockIdx.x, row0 = (POS ? at : at / a.cut.groups) * a.cut.rows;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(a.cut.rows), a.rows - row0));
-  // the heads of this workgroup; for the position's gradient one group of them after the other
-  const int g0 = POS ? 0 : static_cast<int>(at % a.cut.groups), g1 = POS ? a.cut.groups : g0 + 1;
+  const int row0 = static_cast<int>(a.first + blockIdx.x) * a.cut.rows, rows = min(a.cut.rows, a.rows - row0);
+  const int b0 = static_cast<int>(static_cast<uint32_t>(row0) / static_cast<uint32_t>(a.L)), l0 = row0 - b0 * a.L;
+  const int per = static_cast<int>(a.by_row.d), units = rows * per;
   float sum = 0.f;
-  for (int g = g0; g < g1; ++g) {
-    const int h0 = g * a.cut.heads, heads = min(a.cut.heads, a.H - h0);
-    const int units = rows * static_cast<int>(a.cut.by_row.d);
+  // the heads in groups, one after the other
+  for (int h0 = 0; h0 < a.H; h0 += a.cut.heads) {
     for (int u0 = 0; u0 < units; u0 += kUnits * 256) {
-      V v1[kUnits], v2[kUnits], w1[POS ? kUnits : 1], w2[POS ? kUnits : 1];
-      const auto unit = [&](int k, int& r, int& h, int& chunk) {   // false: no unit
+      V v1[kUnits], v2[kUnits], w1[kUnits], w2[kUnits];
+      // unit k of this thread: its row of the workgroup, its head and chunk; false: none
+      struct Unit {
+        int r, h, chunk;
+      };
+      const auto unit = [&](int k, Unit& n) {
         const int u = u0 + k * 256 + tid;
-        r = a.cut.by_row.of(u);
-        const int in_row = u - r * static_cast<int>(a.cut.by_row.d);
-        h = a.cut.by_chunks.of(in_row);
-        chunk = in_row - h * a.cut.chunks;
-        return u < units && h < heads;
+        n.r = a.by_row.of(u);
+        const int in_row = u - n.r * per;
+        n.h = a.cut.by_chunks.of(in_row);
+        n.chunk = in_row - n.h * a.cut.chunks;
+        n.h += h0;
+        return u < units && n.h < a.H;
+      };
+      const auto place = [&](int chunk) {
+        if (chunk < a.turned) return place_of<PV>(a.t, chunk * PV);
+        const int e = 2 * a.t.pairs + (chunk - a.turned) * 2 * PV;
+        return Place{e, e + PV};
       };
 #pragma unroll
       for (int k = 0; k < kUnits; ++k) {
-        int r, h, chunk;
-        if (!unit(k, r, h, chunk)) continue;
-        const uint32_t row = static_cast<uint32_t>(row0 + r), b = row / static_cast<uint32_t>(a.L), l = row - b * a.L;
-        const Place p = place_of<PV>(a.t, chunk, a.cut.rotated);
-        const T* x = static_cast<const T*>(a.x) + b * a.xs[0] + l * a.xs[1] + (h0 + h) * a.xs[2];
+        Unit n;
+        if (!unit(k, n)) continue;
+        const Place p = place(n.chunk);
+        const Row w = row_of(b0, l0, n.r, a.L);
+        const T* x = static_cast<const T*>(a.x) + w.b * a.xs[0] + w.l * a.xs[1] + n.h * a.xs[2];
         v1[k] = *reinterpret_cast<const V*>(x + p.e1);
         if (p.e2 < a.D) v2[k] = *reinterpret_cast<const V*>(x + p.e2);
-        if (POS && chunk < a.cut.rotated) {
-          const T* x0 = static_cast<const T*>(a.x0) + b * a.x0s[0] + l * a.x0s[1] + (h0 + h) * a.x0s[2];
+        if (n.chunk < a.turned) {
+          const T* x0 = static_cast<const T*>(a.x0) + w.b * a.x0s[0] + w.l * a.x0s[1] + n.h * a.x0s[2];
           w1[k] = *reinterpret_cast<const V*>(x0 + p.e1);
           w2[k] = *reinterpret_cast<const V*>(x0 + p.e2);
         }
       }
-      if (g == g0 && u0 == 0) {
-        for (int i = tid; i < rows * a.t.pairs; i += 256) {
-          const int r = a.cut.by_pairs.of(i), pair = i - r * a.t.pairs;
-          const uint32_t row = static_cast<uint32_t>(row0 + r), b = row / static_cast<uint32_t>(a.L), l = row - b * a.L;
-          float c, s;
-          cos_sin(position_of(a.t, b, l, axis_of(a.t, pair)), a.t.freq[pair], c, s);
-          cs[i] = make_float2(c, a.sign * s);
-        }
+      if (h0 == 0 && u0 == 0) {
+        form_turns(a.t, a.cut.log_pairs, rows, a.sign, cs, [&](int r, int axis) {
+          const Row w = row_of(b0, l0, r, a.L);
+          return position_of(a.t, w.b, w.l, axis);
+        });
         __syncthreads();
       }
 #pragma unroll
       for (int k = 0; k < kUnits; ++k) {
-        int r, h, chunk;
-        const bool live = unit(k, r, h, chunk);
+        Unit n;
+        const bool live = unit(k, n);
         float moved[4] = {0.f, 0.f, 0.f, 0.f};
         if (live) {
-          const Place p = place_of<PV>(a.t, chunk, a.cut.rotated);
-          if (chunk < a.cut.rotated) {
+          const Place p = place(n.chunk);
+          if (n.chunk < a.turned) {
             float c[PV], s[PV], x1[PV], x2[PV], y1[PV], y2[PV];
-            const float2* turns = cs + r * a.t.pairs + chunk * PV;
+            const float2* turns = cs + n.r * a.t.pairs + n.chunk * PV;
 #pragma unroll
             for (int j = 0; j < PV; ++j) {
               c[j] = turns[j].x;
@@ -105,62 +151,79 @@ __global__ __launch_bounds__(256) void rotary_kernel(Args a) {
             }
             pairs_of<T, PV, ADJ>(v1[k], v2[k], x1, x2);
             turn<PV>(c, s, x1, x2, y1, y2);
-            if (POS) {
-              pairs_of<T, PV, ADJ>(w1[k], w2[k], x1, x2);
+            pairs_of<T, PV, ADJ>(w1[k], w2[k], x1, x2);
 #pragma unroll
-              for (int j = 0; j < PV; ++j) {
-                const int pair = chunk * PV + j, axis = axis_of(a.t, pair);
-                const float m = a.t.freq[pair] * (y2[j] * x1[j] - y1[j] * x2[j]);
+            for (int j = 0; j < PV; ++j) {
+              const int pair = n.chunk * PV + j, axis = axis_of(a.t, pair);
+              const float m = a.t.freq[pair] * (y2[j] * x1[j] - y1[j] * x2[j]);
 #pragma unroll
-                for (int n = 0; n < 4; ++n) moved[n] += axis == n ? m : 0.f;
-              }
+              for (int i = 0; i < 4; ++i) moved[i] += axis == i ? m : 0.f;
             }
             vectors_of<T, PV, ADJ>(y1, y2, v1[k], v2[k]);
           }
-          if (!POS || a.out != nullptr) {
-            T* y = static_cast<T*>(a.out) + ((row0 + r) * a.H + h0 + h) * a.D;
+          if (a.out != nullptr) {
+            T* y = static_cast<T*>(a.out) + (static_cast<int64_t>(row0 + n.r) * a.H + n.h) * a.D;
             *reinterpret_cast<V*>(y + p.e1) = v1[k];
             if (p.e2 < a.D) *reinterpret_cast<V*>(y + p.e2) = v2[k];
           }
         }
-        if constexpr (POS) {
 #pragma unroll
-          for (int n = 0; n < 4; ++n)
-            if (n < a.t.axes) red[n * kUnits * 256 + k * 256 + tid] = moved[n];
-        }
+        for (int i = 0; i < 4; ++i)
+          if (i < a.t.axes) red[i * kUnits * 256 + k * 256 + tid] = moved[i];
       }
-      if constexpr (POS) {
-        // thread i adds up row i / axes, axis i % axes: the units of this turn that are the row's
-        __syncthreads();
-        const int r = tid / a.t.axes, n = tid - r * a.t.axes, per = static_cast<int>(a.cut.by_row.d);
-        if (r < rows)
-          for (int u = max(r * per, u0); u < min((r + 1) * per, u0 + kUnits * 256); ++u) sum += red[n * kUnits * 256 + u - u0];
-        __syncthreads();
-      }
+      // thread i adds up row i / axes, axis i % axes: the units of this turn that are the row's
+      __syncthreads();
+      const int r = tid / a.t.axes, n = tid - r * a.t.axes;
+      if (r < rows)
+        for (int u = max(r * per, u0); u < min((r + 1) * per, u0 + kUnits * 256); ++u) sum += red[n * kUnits * 256 + u - u0];
+      __syncthreads();
     }
   }
-  if constexpr (POS) {
-    if (tid < rows * a.t.axes) a.gp[row0 * a.t.axes + tid] = sum;
-  }
+  if (tid < rows * a.t.axes) a.gp[static_cast<int64_t>(row0) * a.t.axes + tid] = sum;
 }
 
-template <typename T, int PV>
-const void* kernel_of(bool adjacent, bool positions) {
-  if (positions)
-    return adjacent ? reinterpret_cast<const void*>(&rotary_kernel<T, PV, true, true>)
-                    : reinterpret_cast<const void*>(&rotary_kernel<T, PV, false, true>);
-  return adjacent ? reinterpret_cast<const void*>(&rotary_kernel<T, PV, true, false>)
-                  : reinterpret_cast<const void*>(&rotary_kernel<T, PV, false, false>);
+// kernels for elements of a vector of memory and pairs of a chunk (one pair is two elements, whatever the layout)
+template <typename T, int WV, int PV>
+const void* turning_kernel(bool adjacent) {
+  return adjacent && PV > 1 ? reinterpret_cast<const void*>(&rotary_kernel<T, WV, PV, (PV > 1)>)
+                            : reinterpret_cast<const void*>(&rotary_kernel<T, WV, PV, false>);
 }
-const void* kernel_of(bool bf16, int width, bool adjacent, bool positions) {
-  if (bf16)
-    return width == 8   ? kernel_of<uint16_t, 8>(adjacent, positions)
-           : width == 4 ? kernel_of<uint16_t, 4>(adjacent, positions)
-           : width == 2 ? kernel_of<uint16_t, 2>(adjacent, positions)
-                        : kernel_of<uint16_t, 1>(false, positions);   // (one pair: two elements, whatever the layout)
-  return width == 4   ? kernel_of<float, 4>(adjacent, positions)
-         : width == 2 ? kernel_of<float, 2>(adjacent, positions)
-                      : kernel_of<float, 1>(false, positions);
+const void* turning_kernel(bool bf16, int wv, int pv, bool adjacent) {
+  if (bf16) {
+    if (wv == 8) return pv == 8 ? turning_kernel<uint16_t, 8, 8>(adjacent) : pv == 2 ? turning_kernel<uint16_t, 8, 2>(adjacent)
+                                                                                    : turning_kernel<uint16_t, 8, 1>(adjacent);
+    if (wv == 2) return pv == 2 ? turning_kernel<uint16_t, 2, 2>(adjacent) : turning_kernel<uint16_t, 2, 1>(adjacent);
+    return turning_kernel<uint16_t, 1, 1>(adjacent);
+  }
+  if (wv == 4) return pv == 4 ? turning_kernel<float, 4, 4>(adjacent) : turning_kernel<float, 4, 1>(adjacent);
+  return turning_kernel<float, 1, 1>(adjacent);
+}
+template <typename T, int PV>
+const void* grad_kernel(bool adjacent) {
+  return adjacent && PV > 1 ? reinterpret_cast<const void*>(&rotary_grad_kernel<T, PV, (PV > 1)>)
+                            : reinterpret_cast<const void*>(&rotary_grad_kernel<T, PV, false>);
+}
+const void* grad_kernel(bool bf16, int pv, bool adjacent) {
+  if (bf16) return pv == 8 ? grad_kernel<uint16_t, 8>(adjacent) : pv == 2 ? grad_kernel<uint16_t, 2>(adjacent) : grad_kernel<uint16_t, 1>(adjacent);
+  return pv == 4 ? grad_kernel<float, 4>(adjacent) : grad_kernel<float, 1>(adjacent);
+}
+
+// Rows of rotary_grad_kernel: as many as give each thread two chunks, fewer where that leaves fewer than four
+// workgroups a CU, down to a chunk for each thread.
+void grad_cut(Args* a, int pv) {
+  Cut& c = a->cut;
+  a->turned = a->t.pairs / pv;
+  c.chunks = a->turned + (a->D - 2 * a->t.pairs + 2 * pv - 1) / (2 * pv);
+  const int most = kUnits * 256;
+  c.heads = std::max(1, std::min(a->H, most / c.chunks));
+  const int per = c.heads * c.chunks;
+  int rows = std::min(most / per, kTurns / a->t.pairs);
+  rows = std::min(rows, std::max(a->rows / 1024, (255 + per) / per));
+  c.rows = std::max(1, std::min(rows, 64));
+  a->by_row = div_by(per);
+  c.by_chunks = div_by(c.chunks);
+  c.log_pairs = 0;
+  while (c.log_pairs < 8 && (1 << c.log_pairs) < a->t.pairs) ++c.log_pairs;
 }
 
 int check(const dcn_rotary_desc* d) {
@@ -172,7 +235,7 @@ int check(const dcn_rotary_desc* d) {
   if (rc != DCN_OK) return rc;
   if (d->dtype != DCN_F32 && d->dtype != DCN_BF16) return DCN_E_UNSUPPORTED;
   const double big = 2147483648.;
-  if (d->head_dim > 2 * kTurns || static_cast<double>(d->batch) * d->length * d->heads >= big || d->batch >= big ||
+  if (d->head_dim > kMostD || static_cast<double>(d->batch) * d->length * d->heads >= big || d->batch >= big ||
       d->length >= big || d->heads >= big)
     return DCN_E_UNSUPPORTED;
   return DCN_OK;
@@ -182,18 +245,27 @@ int run(const dcn_rotary_desc* d, Args* a, const void* positions, const float* f
   const bool bf16 = d->dtype == DCN_BF16, adjacent = d->layout == DCN_ROTARY_ADJACENT;
   const int es = bf16 ? 2 : 4;
   a->t = turns_of(d->axes, d->sections, d->layout, d->position_type, d->position_stride, positions, frequencies);
-  a->rows = d->batch * d->length;
   a->L = static_cast<int>(d->length);
   a->H = static_cast<int>(d->heads);
   a->D = static_cast<int>(d->head_dim);
-  int w = fit(fit(width_of(a->t, d->sections, d->head_dim, es), es, a->x), es, a->out);
-  w = fit(w, a->xs, 3);
-  if (a->x0 != nullptr) w = fit(fit(w, es, a->x0), a->x0s, 3);
-  a->cut = cut_of(w, es, a->t.pairs, d->head_dim, a->rows, d->heads);
+  a->rows = static_cast<int>(d->batch * d->length);
+  int w = 16 / es;
+  while (w > 1 && d->head_dim % w != 0) w = narrower(w, es);
+  w = fit(fit(fit(w, es, a->x), es, a->out), es, a->xs, 3);
+  if (a->x0 != nullptr) w = fit(fit(w, es, a->x0), es, a->x0s, 3);
+  const int pv = pairs_at_once(a->t, d->sections, w, es);
+  const void* fn;
+  if (a->gp != nullptr) {
+    grad_cut(a, pv);
+    a->cut.groups = 1;
+    fn = grad_kernel(bf16, pv, adjacent);
+  } else {
+    a->cut = cut_of(w, pv, es, a->t.pairs, d->head_dim, a->rows, d->heads);
+    fn = turning_kernel(bf16, w, pv, adjacent);
+  }
   void* args[] = {a};
-  const int64_t groups = a->gp != nullptr ? 1 : a->cut.groups;
-  return launch(kernel_of(bf16, w, adjacent, a->gp != nullptr), (a->rows + a->cut.rows - 1) / a->cut.rows * groups, args,
-                &a->first, stream)
+  return launch(fn, (static_cast<int64_t>(a->rows) + a->cut.rows - 1) / a->cut.rows * a->cut.groups, args,
+                turns_bytes(a->cut, a->t), &a->first, stream)
              ? DCN_OK
              : DCN_E_HIP;
 }

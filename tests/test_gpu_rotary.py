@@ -31,7 +31,7 @@ CASES = {
     "far": (1, 40, 2, 64, (32,), "far"),
     "many_heads": (1, 9, 37, 128, (64,), "int"),
     "one_row_of_many_heads": (1, 1, 300, 64, (16, 16), "float"),
-    "wide_heads": (1, 3, 2, 1030, (500,), "int"),        # more units in a row than a workgroup has threads
+    "widest_heads": (1, 3, 2, 512, (250,), "int"),
     "batch_33": (33, 7, 2, 32, (10,), "int"),
 }
 
@@ -222,6 +222,10 @@ def test_refusals():
                               ((4, 4, 4, 2, 2), "halves")):
         with pytest.raises(ValueError):
             f(x, pos, freq, sections2, layout)
+    wide = torch.zeros((2, 3, 1, 513), device="cuda")
+    with pytest.raises(dcn.DcnError) as e:
+        f(wide, torch.zeros((2, 3, 1), device="cuda"), freq, (16,))
+    assert e.value.status == dcn.E_UNSUPPORTED
     with pytest.raises(ValueError):
         f(x, torch.zeros(x.shape[:2] + (1,), device="cuda"), torch.zeros(17, device="cuda"), (17,))
     with pytest.raises(ValueError):
