@@ -665,7 +665,7 @@ def deform_conv2d_layer(input, weight_om, bias_om, weight, bias=None, stride=1, 
 def _call(name: str, device, *args) -> None:
     """An entry point of the library on the current stream of `device`."""
     fn = getattr(load_library(), name)
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():   # (a tensor on the device: the runtime is up)
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
     else:
         with torch.cuda.device(device):
@@ -927,6 +927,24 @@ def group_norm_act_backward(grad_out, input, mean, rstd, num_groups, weight=None
 # The calls below are checked once for each set of shapes, strides, types and devices: what a plan
 # is kept by says all that its checks look at, and no address or value is among it.
 
+_DENSE = torch.contiguous_format
+
+
+def _dense_like(t, dtype=None):
+    """A new dense tensor of t's shape (the cheapest way to one on the host)."""
+    return torch.empty_like(t, memory_format=_DENSE) if dtype is None else \
+        torch.empty_like(t, dtype=dtype, memory_format=_DENSE)
+
+
+def _scratch(workspace, nbytes: int, like):
+    """The address of the caller's workspace after checks, or of a fresh one, and what keeps it alive."""
+    if workspace is not None:
+        workspace = _workspace(workspace, nbytes, like.device)
+    elif nbytes:
+        workspace = like.new_empty(nbytes // like.element_size())    # (a multiple of 256 bytes)
+    return workspace.data_ptr() if nbytes else None, workspace
+
+
 def _raw(name: str, *args) -> None:
     rc = getattr(load_library(), name)(*args)
     if rc != OK:
@@ -1021,7 +1039,7 @@ def rotary_positions(input, positions, frequencies, sections, layout="halves", o
     _, desc = _rotary_plan(_look(input), _look(positions), _look(frequencies), tuple(map(int, sections)), layout)
     device = input.device
     if out is None:
-        out = torch.empty(input.shape, dtype=input.dtype, device=device)
+        out = _dense_like(input)
     else:
         _check_out(out, input.shape, input.dtype, device)
     _call("dcn_rotary", device, desc, input.data_ptr(), positions.data_ptr(), frequencies.data_ptr(), out.data_ptr())
@@ -1047,8 +1065,8 @@ def rotary_positions_backward(grad_out, positions, frequencies, sections, layout
                            layout)
     if not grad_out.is_contiguous():
         raise ValueError("grad_out must be contiguous")
-    gx = torch.empty(grad_out.shape, dtype=grad_out.dtype, device=device)
-    gp = None if input is None else torch.empty(positions.shape, dtype=torch.float32, device=device)
+    gx = torch.empty_like(grad_out)
+    gp = None if input is None else _dense_like(positions, torch.float32)
     _call("dcn_rotary_backward", device, desc, grad_out.data_ptr(), positions.data_ptr(), frequencies.data_ptr(),
           _ptr(input), gx.data_ptr(), _ptr(gp))
     return gx if gp is None else (gx, gp)
@@ -1176,11 +1194,10 @@ def residual_norm_backward(grad_out, grad_next, input, branch, stats, gate=None,
     gx, gy = torch.empty_like(input), torch.empty_like(input)
     params = [None if t is None else torch.empty_like(t)
               for t in (gate, scale, branch_weight, branch_bias, next_weight, next_bias)]
-    if nbytes or workspace is not None:
-        workspace = _workspace(workspace, nbytes, device)
+    scratch, keep = _scratch(workspace, nbytes, input)
     _call("dcn_residual_norm_backward", device, desc, input.data_ptr(), branch.data_ptr(), _ptr(gate), _ptr(scale),
           _ptr(branch_weight), _ptr(branch_bias), _ptr(next_weight), stats.data_ptr(), _ptr(grad_out), _ptr(grad_next),
-          gx.data_ptr(), gy.data_ptr(), *map(_ptr, params), workspace.data_ptr() if nbytes else None, nbytes)
+          gx.data_ptr(), gy.data_ptr(), *map(_ptr, params), scratch, nbytes)
     return gx, gy, *params
 
 
@@ -1273,7 +1290,7 @@ def paged_append(key, value, key_pages, value_pages, page_table, starts, counts=
                            tuple(map(int, sections)), layout)
     device = key.device
     lengths = torch.empty_like(starts)
-    out = None if query is None else torch.empty(query.shape, dtype=query.dtype, device=device)
+    out = None if query is None else _dense_like(query)
     _call("dcn_paged_append", device, desc, _ptr(query), key.data_ptr(), value.data_ptr(), _ptr(positions),
           _ptr(frequencies), page_table.data_ptr(), starts.data_ptr(), _ptr(counts), _ptr(out), key_pages.data_ptr(),
           value_pages.data_ptr(), lengths.data_ptr())
@@ -1325,13 +1342,11 @@ def paged_attention(query, key_pages, value_pages, page_table, lengths, scale=No
                                   None if scale is None else float(scale))
     device = query.device
     if out is None:
-        out = torch.empty(query.shape, dtype=query.dtype, device=device)
+        out = _dense_like(query)
     else:
         _check_out(out, query.shape, query.dtype, device)
     lse = torch.empty(query.shape[:2], dtype=torch.float32, device=device) if return_lse else None
-    if nbytes or workspace is not None:
-        workspace = _workspace(workspace, nbytes, device)
+    scratch, keep = _scratch(workspace, nbytes, query)
     _call("dcn_paged_attention", device, desc, query.data_ptr(), key_pages.data_ptr(), value_pages.data_ptr(),
-          page_table.data_ptr(), lengths.data_ptr(), out.data_ptr(), _ptr(lse), workspace.data_ptr() if nbytes else None,
-          nbytes)
+          page_table.data_ptr(), lengths.data_ptr(), out.data_ptr(), _ptr(lse), scratch, nbytes)
     return (out, lse) if return_lse else out

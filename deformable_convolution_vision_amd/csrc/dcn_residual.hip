@@ -13,11 +13,15 @@
 //   grad_scale = sum d gate z, grad_gate = d scale z (summed over the positions where they share it).
 //
 // A row stays in the registers of the threads that take it (8 channels each), so everything is read
-// once; a row of up to 512 channels is part of a wave, wider ones are a workgroup's.  In the gradients
-// a workgroup takes a run of rows and adds its channels' sums in registers; the runs' parts are
-// added by a second launch, in order.  Where a gate is shared by a batch element's positions a run
+// once; a row of up to 512 channels is part of a wave, wider ones are whole waves, and a workgroup takes several
+// rows at a time.  In the gradients a workgroup takes a run of rows and adds its channels' sums in registers; the
+// runs' parts are added by a second launch, in order.  Where a gate is shared by a batch element's positions a run
 // ends with the batch element, and its sums are of d z, d v and d alone: the gate comes in when the
 // parts are added.
+//
+// Rows of any width are read 16 bytes at a time, wherever they start (the memory takes 16-byte accesses at any
+// element): the last vector of a row that is no whole number of them is moved back to end with the row, and the
+// elements that it then shares with the one before are taken as zeros in its thread and not written.
 //
 // Arithmetic: fp32, every output rounded once.
 
@@ -48,6 +52,7 @@ struct Args {
   int64_t per_run;               // rows of a run
   int runs;                      // of a batch element where a gate is shared by its positions, else of all rows
   int P, C, B;
+  int waves;                     // of a row, where it has whole ones
   int n1, n2, gkind;
   int sums, sum_of[kSums];       // sums over the rows that are wanted
   float eps, inv;                // 1 / C
@@ -64,69 +69,124 @@ __device__ __forceinline__ uint16_t narrow<uint16_t>(float v) {
   return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));   // nearest even
 }
 
-// V adjacent elements in one access
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Vec {
-  T e[V];
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// 16 bytes in memory, wherever an element may start
+template <typename T>
+struct Memory;
+template <>
+struct Memory<uint16_t> { typedef u32x4 vec __attribute__((aligned(2))); };
+template <>
+struct Memory<float> { typedef u32x4 vec __attribute__((aligned(4))); };
+
+// A thread's 8 channels of a row, as read.
+template <typename T>
+struct Raw {
+  static constexpr int V = 16 / static_cast<int>(sizeof(T)), K = kE / V;   // elements of a vector, vectors
+  u32x4 v[K];
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t w = v[i / V][i % V * sizeof(T) / 4];
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+    return __uint_as_float(i % 2 == 0 ? w << 16 : w & 0xffff0000u);
+  }
 };
 
-// A thread's 8 channels of a row, as read: kE / V vectors, TR vectors apart.
-template <typename T, int V>
-struct Raw {
-  Vec<T, V> v[kE / V];
-};
-// Its place in rows of C channels: vector i starts at channel (i * tr + t) * V, where that is below C.
+// How rows lie on threads: 8 channels for every thread, some threads with fewer, or fewer than 8 in all.
+enum Fit { kExact, kRagged, kTiny };
+
+// A thread's place in rows of C channels, `tr` threads to a row: vector i starts at channel at[i], and elements that
+// are another thread's, or none's, are told apart by own (the thread has all 8 where FIT is kExact).
+template <typename T, Fit FIT>
 struct Lane {
-  int t, tr, C;
-  template <int V>
-  __device__ __forceinline__ int at(int i) const { return (i * tr + t) * V; }
-};
-template <typename T, int V>
-__device__ __forceinline__ Raw<T, V> load(const void* p, int64_t row, const Lane& l) {
-  Raw<T, V> r;
-  const T* base = static_cast<const T*>(p) + row * l.C;
+  static constexpr int V = Raw<T>::V, K = Raw<T>::K;
+  int t, C;
+  int at[K];
+  uint32_t own;    // bit i: element i of the thread's 8 is its own
+  __device__ __forceinline__ Lane(int thread, int tr, int channels) : t(thread), C(channels) {
+    const int n = (C + V - 1) / V;
+    own = 0;
 #pragma unroll
-  for (int i = 0; i < kE / V; ++i) {
-    const int c = l.at<V>(i);
-    if (c < l.C) {
-      r.v[i] = *reinterpret_cast<const Vec<T, V>*>(base + c);
-    } else {
+    for (int i = 0; i < K; ++i) {
+      const int v = i * tr + t;
+      at[i] = v * V;
+      int dead = 0;
+      if (FIT == kRagged) {
+        dead = v < n ? max(0, at[i] + V - C) : V;
+        at[i] = v < n ? min(at[i], C - V) : 0;       // (a thread without a vector reads the first)
+      }
 #pragma unroll
-      for (int j = 0; j < V; ++j) r.v[i].e[j] = T(0);
+      for (int j = 0; j < V; ++j) own |= j >= dead && at[i] + j < C ? 1u << (i * V + j) : 0u;
     }
   }
-  return r;
-}
-template <typename T, int V>
-__device__ __forceinline__ void floats(const Raw<T, V>& r, float (&f)[kE]) {
-#pragma unroll
-  for (int i = 0; i < kE; ++i) f[i] = widen(r.v[i / V].e[i % V]);
-}
-template <typename T, int V>
-__device__ __forceinline__ void store(void* p, int64_t row, const Lane& l, const float (&f)[kE]) {
-  T* base = static_cast<T*>(p) + row * l.C;
-#pragma unroll
-  for (int i = 0; i < kE / V; ++i) {
-    const int c = l.at<V>(i);
-    Vec<T, V> v;
-#pragma unroll
-    for (int j = 0; j < V; ++j) v.e[j] = narrow<T>(f[i * V + j]);
-    if (c < l.C) *reinterpret_cast<Vec<T, V>*>(base + c) = v;
-  }
-}
-// A parameter's 8 channels, or `none` where there is none.
-template <typename T, int V>
-__device__ __forceinline__ void param(const void* p, int64_t row, const Lane& l, float none, float (&f)[kE]) {
-  if (p != nullptr) {
-    floats<T, V>(load<T, V>(p, row, l), f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kE; ++i) f[i] = none;
-  }
-}
+  __device__ __forceinline__ bool has(int i) const { return FIT == kExact || ((own >> i) & 1u); }
+  __device__ __forceinline__ int channel(int i) const { return at[i / V] + i % V; }
 
-// Sums of N values over the threads of a row, in every one of them: TR lanes of a wave, or (TR 0) the waves of
-// the workgroup, which leave their sums in the LDS.
+  // of the row that starts `o` elements after p
+  __device__ __forceinline__ Raw<T> load(const void* p, int64_t o) const {
+    Raw<T> r;
+    const T* base = static_cast<const T*>(p) + o;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      if (FIT == kTiny) {
+        T e[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) e[j] = has(i * V + j) ? base[at[i] + j] : T(0);
+        __builtin_memcpy(&r.v[i], e, 16);
+      } else {
+        r.v[i] = *reinterpret_cast<const typename Memory<T>::vec*>(base + at[i]);
+      }
+    }
+    return r;
+  }
+  // what is not the thread's own becomes 0, whatever it was
+  __device__ __forceinline__ void clear(float (&f)[kE]) const {
+    if (FIT == kExact) return;
+#pragma unroll
+    for (int i = 0; i < kE; ++i)
+      f[i] = __uint_as_float(__float_as_uint(f[i]) & static_cast<uint32_t>(static_cast<int32_t>(own << (31 - i)) >> 31));
+  }
+  __device__ __forceinline__ void floats(const Raw<T>& r, float (&f)[kE]) const {
+#pragma unroll
+    for (int i = 0; i < kE; ++i) f[i] = r.at(i);
+  }
+  // a parameter's 8 channels, or `none` where there is none
+  __device__ __forceinline__ void param(const void* p, int64_t o, float none, float (&f)[kE]) const {
+    if (p != nullptr) {
+      floats(load(p, o), f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kE; ++i) f[i] = none;
+    }
+  }
+  __device__ __forceinline__ void store(void* p, int64_t o, const float (&f)[kE]) const {
+    T* base = static_cast<T*>(p) + o;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const uint32_t mine = (own >> (i * V)) & ((1u << V) - 1u);
+      if (FIT == kExact || mine == (1u << V) - 1u) {
+        u32x4 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (sizeof(T) == 4) {
+            v[j] = __float_as_uint(f[4 * i + j]);
+          } else {
+            typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+            typedef float f32x2 __attribute__((ext_vector_type(2)));
+            const f32x2 pair = {f[8 * i + 2 * j], f[8 * i + 2 * j + 1]};
+            v[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(pair, bf16x2));   // nearest even
+          }
+        }
+        *reinterpret_cast<typename Memory<T>::vec*>(base + at[i]) = v;
+      } else if (mine != 0) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (has(i * V + j)) base[at[i] + j] = narrow<T>(f[i * V + j]);
+      }
+    }
+  }
+};
+
+// Sums of N values over the threads of a row, in every one of them: TR lanes of a wave, or (TR 0) several waves,
+// which leave their sums in the LDS.
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
@@ -150,220 +210,301 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 // red: two places of 16 waves for N values, used in turn (a wave may be at the next sum while another
-// still reads this one; the barrier of the next keeps it from the one after).
+// still reads this one; the barrier of the next keeps it from the one after).  With TR 0 every thread of the
+// workgroup has to come here.
 template <int TR, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float* red, int& turn) {
+__device__ __forceinline__ void row_sums(float (&v)[N], float* red, int& turn, int waves) {
 #pragma unroll
   for (int n = 0; n < N; ++n) v[n] = lanes_sum<TR == 0 ? 64 : TR>(v[n]);
   if constexpr (TR == 0) {
     float* r = red + (turn & 1) * 32;
     ++turn;
-    const int waves = blockDim.x >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), first = wave / waves * waves;
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-      for (int n = 0; n < N; ++n) r[n * 16 + (threadIdx.x >> 6)] = v[n];
+      for (int n = 0; n < N; ++n) r[n * 16 + wave] = v[n];
     }
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       float s = 0.f;
-      for (int w = 0; w < waves; ++w) s += r[n * 16 + w];
+      for (int w = 0; w < waves; ++w) s += r[n * 16 + first + w];
       v[n] = s;
     }
   }
 }
 
 // The norm of a row's channels, in place: mean and 1 / deviation, from the squares about the mean.
-template <int V, int TR>
-__device__ __forceinline__ void normalise(float (&f)[kE], int kind, const Args& a, const Lane& l, float* red, int& turn,
+template <int TR, typename L>
+__device__ __forceinline__ void normalise(float (&f)[kE], int kind, const Args& a, const L& l, float* red, int& turn,
                                           float& mean, float& rstd) {
   mean = 0.f;
   rstd = 1.f;
   if (kind == DCN_NORM_NONE) return;
+  l.clear(f);
   if (kind == DCN_NORM_LAYER) {
     float s[1] = {0.f};
 #pragma unroll
-    for (int i = 0; i < kE; ++i) s[0] += f[i];     // (channels beyond C are 0)
-    row_sums<TR>(s, red, turn);
+    for (int i = 0; i < kE; ++i) s[0] += f[i];
+    row_sums<TR>(s, red, turn, a.waves);
     mean = s[0] * a.inv;
 #pragma unroll
-    for (int i = 0; i < kE; ++i) f[i] = l.at<V>(i / V) < l.C ? f[i] - mean : 0.f;
+    for (int i = 0; i < kE; ++i) f[i] -= mean;
+    l.clear(f);
   }
   float q[1] = {0.f};
 #pragma unroll
   for (int i = 0; i < kE; ++i) q[0] = fmaf(f[i], f[i], q[0]);
-  row_sums<TR>(q, red, turn);
+  row_sums<TR>(q, red, turn, a.waves);
   rstd = 1.f / sqrtf(fmaf(q[0], a.inv, a.eps));
 #pragma unroll
   for (int i = 0; i < kE; ++i) f[i] *= rstd;
 }
 
-// TR: threads of a row (8 to 64 lanes of a wave; 0: the whole workgroup).
-template <typename T, int V, int TR>
+// Which of a workgroup's rows a thread is at: TR threads of a wave, or (TR 0) a.waves waves, to a row.
+struct Seat {
+  int thread, threads, group, groups;
+};
+template <int TR>
+__device__ __forceinline__ Seat seat_of(const Args& a) {
+  const int tid = threadIdx.x;
+  if constexpr (TR > 0) return {tid % TR, TR, tid / TR, static_cast<int>(blockDim.x) / TR};
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = wave / a.waves;
+  return {tid - g * a.waves * 64, a.waves * 64, g, static_cast<int>(blockDim.x >> 6) / a.waves};
+}
+
+// In the loops of both kernels a thread is at `row`, whose elements start at `o`.  Rows of part of a wave end where
+// they end; where they are whole waves all threads of a workgroup make the same turns (they wait for each other in
+// the sums), and `live` tells whether there is a row.
+template <int TR>
+__device__ __forceinline__ bool more(int64_t row, const Seat& seat, int64_t end) {
+  return TR > 0 ? row < end : row - seat.group < end;
+}
+
+template <typename T, int TR, Fit FIT>
 __global__ __launch_bounds__(TR == 0 ? 1024 : 256) void residual_norm_kernel(Args a) {
   __shared__ float red[TR == 0 ? 64 : 1];
-  const Lane l = {TR == 0 ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) % (TR == 0 ? 1 : TR),
-                  TR == 0 ? static_cast<int>(blockDim.x) : TR, a.C};
-  const int step = TR == 0 ? 1 : 256 / (TR == 0 ? 1 : TR), mine = TR == 0 ? 0 : threadIdx.x / (TR == 0 ? 1 : TR);
+  const Seat seat = seat_of<TR>(a);
+  const Lane<T, FIT> l(seat.thread, seat.threads, a.C);
   int turn = 0;
-  const int64_t r1 = min(a.rows, (static_cast<int64_t>(blockIdx.x) + 1) * a.per_run);
+  const int64_t r0 = blockIdx.x * a.per_run, r1 = min(a.rows, r0 + a.per_run);
   float w1[kE], b1[kE], w2[kE], b2[kE], sc[kE];
-  param<T, V>(a.w1, 0, l, 1.f, w1);
-  param<T, V>(a.b1, 0, l, 0.f, b1);
-  param<T, V>(a.w2, 0, l, 1.f, w2);
-  param<T, V>(a.b2, 0, l, 0.f, b2);
-  param<T, V>(a.scale, 0, l, 1.f, sc);
-  Raw<T, V> x, y, gt;
-  const auto fetch = [&](int64_t row) {
-    y = load<T, V>(a.y, row, l);
-    x = load<T, V>(a.x, row, l);
-    if (a.gkind != DCN_GATE_NONE) gt = load<T, V>(a.gate, a.gkind == DCN_GATE_FULL ? row : row / a.P, l);
+  l.param(a.w1, 0, 1.f, w1);
+  l.param(a.b1, 0, 0.f, b1);
+  l.param(a.w2, 0, 1.f, w2);
+  l.param(a.b2, 0, 0.f, b2);
+  l.param(a.scale, 0, 1.f, sc);
+  int64_t row = r0 + seat.group, o = row * a.C;
+  const int64_t step = static_cast<int64_t>(seat.groups) * a.C;
+  Raw<T> x = {}, y = {}, gt = {};
+  const auto fetch = [&](int64_t row, int64_t o) {
+    if (row >= r1) return;
+    y = l.load(a.y, o);
+    x = l.load(a.x, o);
+    if (a.gkind == DCN_GATE_FULL) gt = l.load(a.gate, o);
+    else if (a.gkind == DCN_GATE_BATCH) gt = l.load(a.gate, row / a.P * a.C);
   };
-  const int64_t r0 = blockIdx.x * a.per_run + mine;
-  if (r0 < r1) fetch(r0);
-  for (int64_t row = r0; row < r1; row += step) {
-    float f[kE], o[kE], g[kE];
-    floats<T, V>(y, f);
-    floats<T, V>(x, o);
-    floats<T, V>(gt, g);
-    if (row + step < r1) fetch(row + step);     // the next row's loads are under way over this one's sums
+  fetch(row, o);
+  for (; more<TR>(row, seat, r1); row += seat.groups, o += step) {
+    const bool live = TR > 0 || row < r1;
+    float f[kE], s[kE];
+    l.floats(y, f);
+    l.floats(x, s);
+    const Raw<T> g = gt;
+    fetch(row + seat.groups, o + step);     // the next row's loads are under way over this one's sums
     float m1, r1s, m2, r2s;
-    normalise<V, TR>(f, a.n1, a, l, red, turn, m1, r1s);
+    normalise<TR>(f, a.n1, a, l, red, turn, m1, r1s);
+    if (a.gkind == DCN_GATE_NONE) {
 #pragma unroll
-    for (int i = 0; i < kE; ++i) {
-      const float z = fmaf(f[i], w1[i], b1[i]);
-      o[i] = fmaf(a.gkind != DCN_GATE_NONE ? g[i] * sc[i] : sc[i], z, o[i]);
-      if (l.at<V>(i / V) >= l.C) o[i] = 0.f;
+      for (int i = 0; i < kE; ++i) s[i] = fmaf(sc[i], fmaf(f[i], w1[i], b1[i]), s[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kE; ++i) s[i] = fmaf(g.at(i) * sc[i], fmaf(f[i], w1[i], b1[i]), s[i]);
     }
-    store<T, V>(a.out, row, l, o);
-    normalise<V, TR>(o, a.n2, a, l, red, turn, m2, r2s);
+    if (live) l.store(a.out, o, s);
+    normalise<TR>(s, a.n2, a, l, red, turn, m2, r2s);
     if (a.n2 != DCN_NORM_NONE) {
 #pragma unroll
-      for (int i = 0; i < kE; ++i) o[i] = fmaf(o[i], w2[i], b2[i]);
-      store<T, V>(a.next, row, l, o);
+      for (int i = 0; i < kE; ++i) s[i] = fmaf(s[i], w2[i], b2[i]);
+      if (live) l.store(a.next, o, s);
     }
-    if (a.stats != nullptr && l.t == 0) *reinterpret_cast<float4*>(a.stats + row * 4) = make_float4(m1, r1s, m2, r2s);
+    if (a.stats != nullptr && l.t == 0 && live)
+      *reinterpret_cast<float4*>(a.stats + row * 4) = make_float4(m1, r1s, m2, r2s);
   }
 }
 
-// (NT: the most threads of a workgroup.  Rows of up to 4096 channels are taken by 512, whose registers hold
-// everything; with 1024 some of it goes to memory.)
-template <typename T, int V, int TR, int NT>
+// What there is on the branch's side: nothing (its gradient is the stream's, and only the next norm's sums are
+// kept), a norm, scale or gate of the channels, or a gate of every element.
+enum Side { kBare, kPlain, kGated };
+
+// NT: the most threads of a workgroup.  AHEAD: the next row's loads are under way over this one's sums and the
+// parameters stay in registers (a workgroup of 1024 threads has none to spare for that).
+template <typename T, int TR, int NT, Side SIDE, Fit FIT, bool AHEAD>
 __global__ __launch_bounds__(NT) void residual_grad_kernel(Args a) {
-  constexpr int STEP = TR == 0 ? 1 : 256 / (TR == 0 ? 1 : TR);
-  __shared__ float red[TR == 0 ? 64 : 256 * kE];
-  const Lane l = {TR == 0 ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) % (TR == 0 ? 1 : TR),
-                  TR == 0 ? static_cast<int>(blockDim.x) : TR, a.C};
-  const int mine = TR == 0 ? 0 : threadIdx.x / (TR == 0 ? 1 : TR);
-  const bool shared_gate = a.gkind == DCN_GATE_BATCH;
+  constexpr int SUMS = SIDE == kBare ? 2 : kSums;
+  __shared__ float red[TR == 0 ? 64 : 1];
+  __shared__ float add[NT > 512 ? 1 : NT * kE];
+  const Seat seat = seat_of<TR>(a);
+  const Lane<T, FIT> l(seat.thread, seat.threads, a.C);
+  const bool shared_gate = SIDE == kPlain && a.gkind == DCN_GATE_BATCH;
   int turn = 0;
   // the rows of this run: of a batch element where its positions share a gate
   const int b = shared_gate ? blockIdx.x / a.runs : 0;
-  const int64_t first = shared_gate ? static_cast<int64_t>(b) * a.P : 0, end = shared_gate ? first + a.P : a.rows;
-  const int64_t r0 = first + (blockIdx.x - static_cast<int64_t>(b) * a.runs) * a.per_run, r1 = min(end, r0 + a.per_run);
-  float w1[kE], b1[kE], w2[kE], sc[kE], sum[kSums][kE], g[kE];
-  param<T, V>(a.w1, 0, l, 1.f, w1);
-  param<T, V>(a.b1, 0, l, 0.f, b1);
-  param<T, V>(a.w2, 0, l, 1.f, w2);
-  param<T, V>(a.scale, 0, l, 1.f, sc);
-  param<T, V>(shared_gate ? a.gate : nullptr, b, l, 1.f, g);
+  const int64_t begin = shared_gate ? static_cast<int64_t>(b) * a.P : 0, end = shared_gate ? begin + a.P : a.rows;
+  const int64_t r0 = begin + (blockIdx.x - static_cast<int64_t>(b) * a.runs) * a.per_run, r1 = min(end, r0 + a.per_run);
+  // fs: gate and scale (kGated: scale); fw: that times the branch's weight.  Only a row's sums need what is not
+  // the thread's own to be 0: the channels' sums and the gradients leave it out when they are written.
+  float w1[kE], b1[kE], w2[kE], fs[kE], fw[kE], sum[SUMS][kE];
+  const auto params = [&] {
+    l.param(a.w2, 0, 1.f, w2);
+    if constexpr (SIDE != kBare) {
+      l.param(a.w1, 0, 1.f, w1);
+      l.param(a.b1, 0, 0.f, b1);
+      l.param(a.scale, 0, 1.f, fs);
+      if constexpr (SIDE == kPlain) {
+        l.param(shared_gate ? a.gate : nullptr, static_cast<int64_t>(b) * a.C, 1.f, fw);
 #pragma unroll
-  for (int n = 0; n < kSums; ++n)
+        for (int i = 0; i < kE; ++i) {
+          fs[i] *= fw[i];
+          fw[i] = fs[i] * w1[i];
+        }
+      }
+    }
+  };
+  if constexpr (AHEAD) params();
+#pragma unroll
+  for (int n = 0; n < SUMS; ++n)
 #pragma unroll
     for (int i = 0; i < kE; ++i) sum[n][i] = 0.f;
-  Raw<T, V> ry, rx, rgo, rgn, rg;
+  int64_t row = r0 + seat.group, o = row * a.C;
+  const int64_t step = static_cast<int64_t>(seat.groups) * a.C;
+  const bool then = a.n2 != DCN_NORM_NONE;
+  // (what is not given stays 0)
+  Raw<T> ry = {}, rx = {}, rgo = {}, rgn = {}, rg = {};
   float4 rst = make_float4(0.f, 1.f, 0.f, 1.f);
-  const auto fetch = [&](int64_t row) {
-    ry = load<T, V>(a.y, row, l);
-    if (a.n2 != DCN_NORM_NONE) {
-      rx = load<T, V>(a.x, row, l);
-      rgn = a.gn != nullptr ? load<T, V>(a.gn, row, l) : Raw<T, V>{};
-    }
-    rgo = a.go != nullptr ? load<T, V>(a.go, row, l) : Raw<T, V>{};
-    if (a.gkind == DCN_GATE_FULL) rg = load<T, V>(a.gate, row, l);
+  const auto fetch = [&](int64_t row, int64_t o) {
+    if (row >= r1) return;
+    ry = l.load(a.y, o);
+    if (then) rx = l.load(a.x, o);
+    if (a.gn != nullptr) rgn = l.load(a.gn, o);
+    if (a.go != nullptr) rgo = l.load(a.go, o);
+    if constexpr (SIDE == kGated) rg = l.load(a.gate, o);
     rst = *reinterpret_cast<const float4*>(a.stats + row * 4);
   };
-  if (r0 + mine < r1) fetch(r0 + mine);
-  for (int64_t row = r0 + mine; row < r1; row += STEP) {
-    const float4 st = rst;
-    float v[kE], u[kE], d[kE], z[kE], gn[kE];
-    floats<T, V>(ry, v);
-    floats<T, V>(rx, u);
-    floats<T, V>(rgn, gn);
-    floats<T, V>(rgo, d);
-    if (a.gkind == DCN_GATE_FULL) floats<T, V>(rg, g);
-    if (row + STEP < r1) fetch(row + STEP);     // the next row's loads are under way over this one's sums
-#pragma unroll
-    for (int i = 0; i < kE; ++i) {
-      v[i] = l.at<V>(i / V) < l.C ? (v[i] - st.x) * st.y : 0.f;
-      z[i] = fmaf(v[i], w1[i], b1[i]);
+  if constexpr (AHEAD) fetch(row, o);
+  for (; more<TR>(row, seat, r1); row += seat.groups, o += step) {
+    const bool live = TR > 0 || row < r1;
+    if constexpr (!AHEAD) {
+      fetch(row, o);
+      params();
     }
-    if (a.n2 != DCN_NORM_NONE) {
-      float s[2] = {0.f, 0.f};
+    const float4 st = rst;
+    float v[kE], u[kE], d[kE], z[kE], gn[kE], g[kE];
+    l.floats(ry, v);
+    l.floats(rgo, d);
+    if (then) {
+      l.floats(rx, u);
+      l.floats(rgn, gn);
+    }
+    if constexpr (SIDE == kGated) l.floats(rg, g);
+    if constexpr (AHEAD) fetch(row + seat.groups, o + step);
+    if constexpr (SIDE != kBare) {
 #pragma unroll
       for (int i = 0; i < kE; ++i) {
-        u[i] = l.at<V>(i / V) < l.C ? (fmaf(g[i] * sc[i], z[i], u[i]) - st.z) * st.w : 0.f;
-        sum[0][i] = fmaf(gn[i], u[i], sum[0][i]);
-        sum[1][i] += gn[i];
+        v[i] = (v[i] - st.x) * st.y;
+        z[i] = fmaf(v[i], w1[i], b1[i]);
+      }
+    }
+    if (then) {
+#pragma unroll
+      for (int i = 0; i < kE; ++i) {
+        if constexpr (SIDE == kBare) u[i] += v[i];
+        else u[i] = fmaf(SIDE == kGated ? g[i] * fs[i] : fs[i], z[i], u[i]);
+        u[i] = (u[i] - st.z) * st.w;
+      }
+      if (live) {
+#pragma unroll
+        for (int i = 0; i < kE; ++i) {
+          sum[0][i] = fmaf(gn[i], u[i], sum[0][i]);
+          sum[1][i] += gn[i];
+        }
+      }
+      float s[2] = {0.f, 0.f};
+      l.clear(gn);
+#pragma unroll
+      for (int i = 0; i < kE; ++i) {
         gn[i] *= w2[i];
         s[0] += gn[i];
         s[1] = fmaf(gn[i], u[i], s[1]);
       }
-      row_sums<TR>(s, red, turn);
+      row_sums<TR>(s, red, turn, a.waves);
       const float mg = a.n2 == DCN_NORM_LAYER ? s[0] * a.inv : 0.f, mu = s[1] * a.inv;
 #pragma unroll
-      for (int i = 0; i < kE; ++i) d[i] = fmaf(st.w, gn[i] - mg - u[i] * mu, d[i]);
+      for (int i = 0; i < kE; ++i) d[i] = fmaf(st.w, fmaf(-u[i], mu, gn[i] - mg), d[i]);
     }
-    if (a.out != nullptr) store<T, V>(a.out, row, l, d);
-    if (a.gkind == DCN_GATE_FULL && a.ggate != nullptr) {
-      float gg[kE];
+    if (live && a.out != nullptr) l.store(a.out, o, d);
+    if constexpr (SIDE == kBare) {
+      if (live && a.next != nullptr) l.store(a.next, o, d);
+    } else {
+      if (SIDE == kGated && live && a.ggate != nullptr) {
+        float gg[kE];
 #pragma unroll
-      for (int i = 0; i < kE; ++i) gg[i] = d[i] * z[i] * sc[i];
-      store<T, V>(a.ggate, row, l, gg);
-    }
-    float s[2] = {0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < kE; ++i) {
-      if (l.at<V>(i / V) >= l.C) d[i] = 0.f;
-      const float e = a.gkind == DCN_GATE_FULL ? d[i] * g[i] : d[i];
-      sum[2][i] = fmaf(e, z[i], sum[2][i]);
-      sum[3][i] = fmaf(e, v[i], sum[3][i]);
-      sum[4][i] += e;
-      d[i] *= g[i] * sc[i] * w1[i];       // gv
-      s[0] += d[i];
-      s[1] = fmaf(d[i], v[i], s[1]);
-    }
-    if (a.next != nullptr) {
-      if (a.n1 != DCN_NORM_NONE) {
-        row_sums<TR>(s, red, turn);
-        const float mg = a.n1 == DCN_NORM_LAYER ? s[0] * a.inv : 0.f, mv = s[1] * a.inv;
-#pragma unroll
-        for (int i = 0; i < kE; ++i) d[i] = st.y * (d[i] - mg - v[i] * mv);
+        for (int i = 0; i < kE; ++i) gg[i] = d[i] * z[i] * fs[i];
+        l.store(a.ggate, o, gg);
       }
-      store<T, V>(a.next, row, l, d);
+      if constexpr (SIDE == kGated) {
+#pragma unroll
+        for (int i = 0; i < kE; ++i) d[i] *= g[i];
+      }
+      if (live) {
+#pragma unroll
+        for (int i = 0; i < kE; ++i) {
+          sum[2][i] = fmaf(d[i], z[i], sum[2][i]);
+          sum[3][i] = fmaf(d[i], v[i], sum[3][i]);
+          sum[4][i] += d[i];
+        }
+      }
+      if (a.next != nullptr) {
+        float s[2] = {0.f, 0.f};
+        l.clear(d);
+#pragma unroll
+        for (int i = 0; i < kE; ++i) {
+          d[i] *= SIDE == kGated ? fs[i] * w1[i] : fw[i];       // gv
+          s[0] += d[i];
+          s[1] = fmaf(d[i], v[i], s[1]);
+        }
+        if (a.n1 != DCN_NORM_NONE) {
+          row_sums<TR>(s, red, turn, a.waves);
+          const float mg = a.n1 == DCN_NORM_LAYER ? s[0] * a.inv : 0.f, mv = s[1] * a.inv;
+#pragma unroll
+          for (int i = 0; i < kE; ++i) d[i] = st.y * fmaf(-v[i], mv, d[i] - mg);
+        }
+        if (live) l.store(a.next, o, d);
+      }
     }
   }
   if (a.part == nullptr) return;
   // this run's sums: the workgroup's rows of threads are added in order
   float* part = a.part + static_cast<int64_t>(blockIdx.x) * kSums * a.C;
-  if constexpr (TR == 0) {
+  if (seat.groups == 1) {
 #pragma unroll
-    for (int n = 0; n < kSums; ++n)
+    for (int n = 0; n < SUMS; ++n)
 #pragma unroll
-      for (int i = 0; i < kE; ++i) {
-        const int c = l.at<V>(i / V) + i % V;
-        if (c < a.C) part[n * a.C + c] = sum[n][i];
-      }
-  } else {
-    for (int n = 0; n < kSums; ++n) {
+      for (int i = 0; i < kE; ++i)
+        if (l.has(i)) part[n * a.C + l.channel(i)] = sum[n][i];
+  } else if constexpr (NT <= 512) {
+    const int pitch = seat.threads * kE;
+#pragma unroll
+    for (int n = 0; n < SUMS; ++n) {
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < kE; ++i) red[mine * TR * kE + l.at<V>(i / V) + i % V] = sum[n][i];
+      for (int i = 0; i < kE; ++i)
+        if (l.has(i)) add[seat.group * pitch + l.channel(i)] = sum[n][i];
       __syncthreads();
-      for (int c = threadIdx.x; c < a.C; c += 256) {
+      for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
         float s = 0.f;
 #pragma unroll 4
-        for (int r = 0; r < STEP; ++r) s += red[r * TR * kE + c];
+        for (int r = 0; r < seat.groups; ++r) s += add[r * pitch + c];
         part[n * a.C + c] = s;
       }
     }
@@ -420,25 +561,35 @@ int check(const dcn_residual_desc* d) {
   return DCN_OK;
 }
 
-// Threads of a row (0: whole workgroups of `threads`).
-struct Shape {
-  int tr, threads, step;   // step: rows at a time
-};
-Shape shape_of(int64_t C) {
-  const int lanes = static_cast<int>((C + kE - 1) / kE);
-  if (lanes > 64) return {0, (lanes + 63) / 64 * 64, 1};
-  const int tr = lanes <= 8 ? 8 : lanes <= 16 ? 16 : lanes <= 32 ? 32 : 64;
-  return {tr, 256, 256 / tr};
-}
+constexpr int64_t kForwardWaves = 4096;    // four on each SIMD
 
-constexpr int64_t kRuns = 512, kForwardRuns = 1024;   // workgroups at most: 2 and 4 a CU
-// Runs of the gradients: two workgroups for each CU at most, and whole steps of rows.
+// Threads of a row (0: `waves` whole waves of them), of a workgroup, and rows of it at a time.
+struct Shape {
+  int tr, waves, threads, groups;
+  Fit fit;
+};
+// most: threads of a workgroup of rows that are parts of a wave, or that several such rows fit.
+Shape shape_of(int64_t C, int most) {
+  const int lanes = static_cast<int>((C + kE - 1) / kE);
+  if (lanes > 64) {
+    const int waves = (lanes + 63) / 64, groups = std::max(1, most / (64 * waves));
+    return {0, waves, waves * 64 * groups, groups, C == waves * 64 * kE ? kExact : kRagged};
+  }
+  const int tr = lanes <= 8 ? 8 : lanes <= 16 ? 16 : lanes <= 32 ? 32 : 64;
+  return {tr, 1, most, most / tr, C == tr * kE ? kExact : C < kE ? kTiny : kRagged};
+}
+Shape forward_shape(int64_t C) { return shape_of(C, 256); }
+Shape backward_shape(int64_t C) { return shape_of(C, 512); }
+
+// Runs of the gradients, each of whole steps of rows: one round of the workgroups that the chip holds at two waves
+// a SIMD (registers allow no more; four of those of 1024 threads).
 void runs_of(const dcn_residual_desc* d, const Shape& s, int* runs, int64_t* per_run) {
   const bool shared_gate = d->gate == DCN_GATE_BATCH;
   const int64_t rows = shared_gate ? d->positions : d->batch * d->positions;
-  int64_t n = shared_gate ? std::max<int64_t>(1, kRuns / std::max<int64_t>(1, d->batch)) : kRuns;
+  const int64_t most = 256 * std::max(1, 8 / (s.threads / 64));
+  const int64_t n = shared_gate ? std::max<int64_t>(1, most / std::max<int64_t>(1, d->batch)) : most;
   *per_run = std::max<int64_t>(1, (rows + n - 1) / n);
-  *per_run = (*per_run + s.step - 1) / s.step * s.step;
+  *per_run = (*per_run + s.groups - 1) / s.groups * s.groups;
   *runs = static_cast<int>((rows + *per_run - 1) / *per_run);
 }
 
@@ -454,50 +605,43 @@ void fill(const dcn_residual_desc* d, Args* a) {
   a->inv = 1.f / static_cast<float>(d->channels);
 }
 
-template <typename T, int V>
+template <typename T, Fit FIT>
 const void* fwd_kernel(int tr) {
   switch (tr) {
-    case 8: return reinterpret_cast<const void*>(&residual_norm_kernel<T, V, 8>);
-    case 16: return reinterpret_cast<const void*>(&residual_norm_kernel<T, V, 16>);
-    case 32: return reinterpret_cast<const void*>(&residual_norm_kernel<T, V, 32>);
-    case 64: return reinterpret_cast<const void*>(&residual_norm_kernel<T, V, 64>);
-    default: return reinterpret_cast<const void*>(&residual_norm_kernel<T, V, 0>);
+    case 8: return reinterpret_cast<const void*>(&residual_norm_kernel<T, 8, FIT>);
+    case 16: return reinterpret_cast<const void*>(&residual_norm_kernel<T, 16, FIT>);
+    case 32: return reinterpret_cast<const void*>(&residual_norm_kernel<T, 32, FIT>);
+    case 64: return reinterpret_cast<const void*>(&residual_norm_kernel<T, 64, FIT>);
+    default: return reinterpret_cast<const void*>(&residual_norm_kernel<T, 0, FIT>);
   }
 }
-template <typename T, int V>
+template <typename T>
+const void* fwd_kernel(const Shape& s) {
+  return s.fit == kTiny    ? reinterpret_cast<const void*>(&residual_norm_kernel<T, 8, kTiny>)
+         : s.fit == kExact ? fwd_kernel<T, kExact>(s.tr)
+                           : fwd_kernel<T, kRagged>(s.tr);
+}
+template <typename T, Side SIDE, Fit FIT>
 const void* bwd_kernel(const Shape& s) {
   switch (s.tr) {
-    case 8: return reinterpret_cast<const void*>(&residual_grad_kernel<T, V, 8, 256>);
-    case 16: return reinterpret_cast<const void*>(&residual_grad_kernel<T, V, 16, 256>);
-    case 32: return reinterpret_cast<const void*>(&residual_grad_kernel<T, V, 32, 256>);
-    case 64: return reinterpret_cast<const void*>(&residual_grad_kernel<T, V, 64, 256>);
+    case 8: return reinterpret_cast<const void*>(&residual_grad_kernel<T, 8, 512, SIDE, FIT, true>);
+    case 16: return reinterpret_cast<const void*>(&residual_grad_kernel<T, 16, 512, SIDE, FIT, true>);
+    case 32: return reinterpret_cast<const void*>(&residual_grad_kernel<T, 32, 512, SIDE, FIT, true>);
+    case 64: return reinterpret_cast<const void*>(&residual_grad_kernel<T, 64, 512, SIDE, FIT, true>);
     default:
-      return s.threads <= 512 ? reinterpret_cast<const void*>(&residual_grad_kernel<T, V, 0, 512>)
-                              : reinterpret_cast<const void*>(&residual_grad_kernel<T, V, 0, 1024>);
+      return s.threads <= 512 ? reinterpret_cast<const void*>(&residual_grad_kernel<T, 0, 512, SIDE, FIT, true>)
+                              : reinterpret_cast<const void*>(&residual_grad_kernel<T, 0, 1024, SIDE, FIT, SIDE == kBare>);
   }
 }
-const void* kernel_of(bool bf16, int width, const Shape& s, bool backward) {
-  if (bf16) {
-    if (width == 8) return backward ? bwd_kernel<uint16_t, 8>(s) : fwd_kernel<uint16_t, 8>(s.tr);
-    if (width == 2) return backward ? bwd_kernel<uint16_t, 2>(s) : fwd_kernel<uint16_t, 2>(s.tr);
-    return backward ? bwd_kernel<uint16_t, 1>(s) : fwd_kernel<uint16_t, 1>(s.tr);
-  }
-  if (width == 4) return backward ? bwd_kernel<float, 4>(s) : fwd_kernel<float, 4>(s.tr);
-  if (width == 2) return backward ? bwd_kernel<float, 2>(s) : fwd_kernel<float, 2>(s.tr);
-  return backward ? bwd_kernel<float, 1>(s) : fwd_kernel<float, 1>(s.tr);
+template <typename T, Side SIDE>
+const void* bwd_kernel(const Shape& s) {
+  return s.fit == kTiny    ? reinterpret_cast<const void*>(&residual_grad_kernel<T, 8, 512, SIDE, kTiny, true>)
+         : s.fit == kExact ? bwd_kernel<T, SIDE, kExact>(s)
+                           : bwd_kernel<T, SIDE, kRagged>(s);
 }
-
-// The widest vectors that fit the channels and every address.
-template <size_t N>
-int width_of(const dcn_residual_desc* d, const void* const (&ptrs)[N]) {
-  const bool bf16 = d->dtype == DCN_BF16;
-  const int es = bf16 ? 2 : 4;
-  for (int w : {16 / es, 2}) {
-    bool ok = d->channels % w == 0;
-    for (const void* p : ptrs) ok = ok && reinterpret_cast<uintptr_t>(p) % (static_cast<unsigned>(w) * es) == 0;
-    if (ok) return w;
-  }
-  return 1;
+template <typename T>
+const void* bwd_kernel(const Shape& s, Side side) {
+  return side == kBare ? bwd_kernel<T, kBare>(s) : side == kPlain ? bwd_kernel<T, kPlain>(s) : bwd_kernel<T, kGated>(s);
 }
 
 bool launch(const void* fn, dim3 groups, int threads, Args* a, hipStream_t stream) {
@@ -547,14 +691,13 @@ extern "C" int dcn_residual_norm(const dcn_residual_desc* d, const void* x, cons
   }
   a.out = out;
   a.stats = stats;
-  const int w = width_of(d, {a.x, a.y, a.gate, a.scale, a.w1, a.b1, a.w2, a.b2, static_cast<const void*>(a.out),
-                             static_cast<const void*>(a.next)});
-  const Shape s = shape_of(d->channels);
+  const Shape s = forward_shape(d->channels);
+  a.waves = s.waves;
   // runs of several steps share a thread's parameters
-  const int64_t steps = (a.rows + s.step - 1) / s.step;
-  a.per_run = std::max<int64_t>(1, (steps + kForwardRuns - 1) / kForwardRuns) * s.step;
-  return launch(kernel_of(d->dtype == DCN_BF16, w, s, false), dim3((a.rows + a.per_run - 1) / a.per_run), s.threads, &a,
-                stream)
+  const int64_t steps = (a.rows + s.groups - 1) / s.groups, most = std::max<int64_t>(1, kForwardWaves / (s.threads / 64));
+  a.per_run = std::max<int64_t>(1, (steps + most - 1) / most) * s.groups;
+  return launch(d->dtype == DCN_BF16 ? fwd_kernel<uint16_t>(s) : fwd_kernel<float>(s),
+                dim3((a.rows + a.per_run - 1) / a.per_run), s.threads, &a, stream)
              ? DCN_OK
              : DCN_E_HIP;
 }
@@ -568,8 +711,9 @@ extern "C" int dcn_residual_norm_backward_workspace_bytes(const dcn_residual_des
   if (d->batch == 0 || d->positions == 0) return DCN_OK;
   int runs;
   int64_t per_run;
-  runs_of(d, shape_of(d->channels), &runs, &per_run);
-  *bytes = static_cast<size_t>(runs) * (d->gate == DCN_GATE_BATCH ? d->batch : 1) * kSums * d->channels * sizeof(float);
+  runs_of(d, backward_shape(d->channels), &runs, &per_run);
+  const size_t need = static_cast<size_t>(runs) * (d->gate == DCN_GATE_BATCH ? d->batch : 1) * kSums * d->channels * sizeof(float);
+  *bytes = (need + 255) / 256 * 256;
   return DCN_OK;
 }
 
@@ -616,7 +760,8 @@ extern "C" int dcn_residual_norm_backward(const dcn_residual_desc* d, const void
   a.gb2 = grad_next_bias;
   const bool bf16 = d->dtype == DCN_BF16;
   const int64_t outputs = wanted_sums(&a);
-  const Shape s = shape_of(d->channels);
+  const Shape s = backward_shape(d->channels);
+  a.waves = s.waves;
   if (any) {
     runs_of(d, s, &a.runs, &a.per_run);
     const int64_t groups = static_cast<int64_t>(a.runs) * (d->gate == DCN_GATE_BATCH ? a.B : 1);
@@ -628,10 +773,12 @@ extern "C" int dcn_residual_norm_backward(const dcn_residual_desc* d, const void
         return DCN_E_WORKSPACE;
       a.part = static_cast<float*>(workspace);
     }
-    const int w = width_of(d, {a.x, a.y, a.gate, a.scale, a.w1, a.b1, a.w2, a.go, a.gn, static_cast<const void*>(a.out),
-                               static_cast<const void*>(a.next),
-                               d->gate == DCN_GATE_FULL ? static_cast<const void*>(a.ggate) : nullptr});
-    if (!launch(kernel_of(bf16, w, s, true), dim3(groups), s.threads, &a, stream)) return DCN_E_HIP;
+    const Side side = d->gate == DCN_GATE_FULL ? kGated
+                      : d->branch_norm != DCN_NORM_NONE || d->gate != DCN_GATE_NONE || scale != nullptr || grad_scale != nullptr
+                          ? kPlain
+                          : kBare;
+    const void* fn = bf16 ? bwd_kernel<uint16_t>(s, side) : bwd_kernel<float>(s, side);
+    if (!launch(fn, dim3(groups), s.threads, &a, stream)) return DCN_E_HIP;
   }
   if (outputs > 0 &&
       !launch(bf16 ? reinterpret_cast<const void*>(&residual_params_kernel<uint16_t>)

@@ -448,8 +448,7 @@ int dcn_rotary_backward(const dcn_rotary_desc* desc, const void* grad_out, const
  * a norm that is NONE are not read.  stats [B][P][4] float32 where not NULL: mean and 1 / deviation of the
  * branch's row, then of out's (0 and 1 where there is none), which the backward takes.  Everything is dense
  * in desc->dtype; out may be x or branch, next may be branch (out and next differ).  Arithmetic: fp32, the
- * variance about the mean, out and next rounded once.  Rows are read 16, 4 bytes (fp32: 16, 8) or an
- * element at a time, the widest that fits C and the addresses.
+ * variance about the mean, out and next rounded once.  Rows are read 16 bytes at a time wherever they start.
  * DCN_E_ARG: an invalid descriptor (a negative size, no channel, eps negative or not finite, an unknown
  * norm or gate) or a NULL required pointer; DCN_E_UNSUPPORTED: another dtype, more than 8192 channels,
  * 2^31 rows, or more than 65530 batch elements with DCN_GATE_BATCH; DCN_E_HIP as elsewhere; all checked before any
