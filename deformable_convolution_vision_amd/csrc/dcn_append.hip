@@ -185,11 +185,7 @@ extern "C" int dcn_paged_append(const dcn_append_desc* d, const void* q, const v
   a.t = turns_of(d->axes, d->sections, d->layout, d->position_type, d->position_stride, positions, frequencies);
   const bool bf16 = d->dtype == DCN_BF16;
   const int es = bf16 ? 2 : 4;
-  int w = 16 / es;
-  while (w > 1 && d->head_dim % w != 0) w = narrower(w, es);
-  for (const void* p : {k, v, static_cast<const void*>(key_pages), static_cast<const void*>(value_pages)}) w = fit(w, es, p);
-  for (const int64_t* s : {a.ks, a.vs, a.kps, a.vps}) w = fit(w, es, s, 3);
-  if (a.Hq > 0) w = fit(fit(fit(w, es, q), es, q_out), es, a.qs, 3);
+  const int w = vector_of(d->head_dim, es);
   const int pv = pairs_at_once(a.t, d->sections, w, es);
   a.cut = cut_of(w, pv, es, a.t.pairs, d->head_dim, a.rows, a.Hq + 2 * a.Hkv);
   a.cut.rows = std::min(a.cut.rows, kRows);

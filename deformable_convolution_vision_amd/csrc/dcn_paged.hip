@@ -75,9 +75,10 @@ __device__ __forceinline__ f32x4 zero_acc4() {
   return z;
 }
 
-// 16 bytes of memory (said to be memory, for a generic address would be waited for as an LDS read too)
+// 16 bytes of memory, which takes them wherever an element may start (said to be memory, for a generic address would
+// be waited for as an LDS read too)
 __device__ __forceinline__ uint4 load16(const void* p) {
-  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
   const u32x4 v = *(const __attribute__((address_space(1))) u32x4*)(p);
   return make_uint4(v.x, v.y, v.z, v.w);
 }
@@ -167,8 +168,8 @@ __device__ __forceinline__ Share share_of(const PagedArgs& a, int index) {
 
 __device__ uint4 paged_zero_row[32];   // what positions without a row read: 512 bytes, a row of 128 fp32
 
-// How rows are read: 16 bytes at a time and no wider than they are (the head is the padded one), 16 bytes at a
-// time where they have them, or element by element.
+// How rows are read: 16 bytes at a time all the padded head's width, 16 bytes at a time where the head has them, or
+// (heads of another size) element by element.
 enum Rows { kWhole, kVectors, kElements };
 
 template <typename T, int DP, int W, Rows ROWS>
@@ -204,24 +205,6 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
   };
   Where next = entry(part.first + wave);
 
-  // the query head of this lane's column
-  const int row = tile * 16 + col;
-  const bool live = row < a.g;
-  Frag<T> qf[KS];
-  {
-    const T* qp = static_cast<const T*>(a.q) + part.b * a.qs[0] + (hk * a.g + (live ? row : 0)) * a.qs[1];
-#pragma unroll
-    for (int i = 0; i < KS; ++i)
-#pragma unroll
-      for (int h = 0; h < 8 / KV; ++h) {
-        const uint4 u = load_vec<T, ROWS != kElements>(qp, 0, 32 * i + 8 * quad + KV * h, a.D, live).u;
-        __builtin_memcpy(reinterpret_cast<char*>(&qf[i]) + 16 * h, &u, 16);
-      }
-  }
-
-  Frag<T> kf[2][KS];
-  Vec16<T> vf[VL];
-  uint32_t kept = 0;   // of the block in kf, vf: positions that count
   const T* const zeros = reinterpret_cast<const T*>(paged_zero_row);
   // 16 bytes of a row from element d on; zeros beyond D
   const auto take = [&](const T* r, int d) {
@@ -229,6 +212,25 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
     if constexpr (ROWS == kVectors) return load16(d < a.D ? r + d : zeros);
     return load_vec<T, false>(r, 0, d, a.D, true).u;
   };
+
+  // the query head of this lane's column
+  const int row = tile * 16 + col;
+  const bool live = row < a.g;
+  Frag<T> qf[KS];
+  {
+    const T* qp = live ? static_cast<const T*>(a.q) + part.b * a.qs[0] + (hk * a.g + row) * a.qs[1] : zeros;
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+#pragma unroll
+      for (int h = 0; h < 8 / KV; ++h) {
+        const uint4 u = take(qp, 32 * i + 8 * quad + KV * h);
+        __builtin_memcpy(reinterpret_cast<char*>(&qf[i]) + 16 * h, &u, 16);
+      }
+  }
+
+  Frag<T> kf[2][KS];
+  Vec16<T> vf[VL];
+  uint32_t kept = 0;   // of the block in kf, vf: positions that count
   const auto fetch = [&](const Where& w) {
     const bool ok = w.page >= 0 && w.page < a.num_pages;
     kept = static_cast<uint32_t>(__ballot(ok));
@@ -558,13 +560,6 @@ bool launch_paged(const void* fn, int64_t n, int threads, void** args, PagedArgs
   return true;
 }
 
-bool vec_rows(const void* p, const int64_t* s, int n, int64_t D, int es) {
-  const int64_t v = 16 / es;
-  bool ok = reinterpret_cast<uintptr_t>(p) % 16 == 0 && D % v == 0;
-  for (int i = 0; i < n; ++i) ok = ok && s[i] % v == 0;
-  return ok;
-}
-
 }  // namespace
 }  // namespace attn
 }  // namespace dcn
@@ -631,9 +626,7 @@ extern "C" int dcn_paged_attention(const dcn_paged_desc* d, const void* q, const
   a.c = d->scale * kLog2e;
   const bool bf16 = d->dtype == DCN_BF16;
   const int es = bf16 ? 2 : 4;
-  const bool vec = vec_rows(q, d->q_stride, 2, d->head_dim, es) && vec_rows(key_pages, d->key_page_stride, 3, d->head_dim, es) &&
-                   vec_rows(value_pages, d->value_page_stride, 3, d->head_dim, es);
-  const Rows rows = !vec ? kElements : a.D == p.dp ? kWhole : kVectors;
+  const Rows rows = a.D == p.dp ? kWhole : a.D % (16 / es) == 0 ? kVectors : kElements;
   if (d->page_size > 1) {
     // of positions below 2^31: with 2^s >= page_size, 2^(31 + s) / page_size rounded up is off by less than 2^-31 of it
     int s = 0;

@@ -190,15 +190,35 @@ struct Cut {
 // Orders a wave's LDS accesses of different lanes (no instruction: a wave's are carried out in order).
 __device__ __forceinline__ void wave_order() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
-// So many bytes in one register access.
-template <int BYTES>
+// So many bytes in one access, and the same in memory, which takes them wherever an element may start.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <int BYTES, int ELEMENT>
 struct Bytes;
 template <>
-struct Bytes<16> { typedef uint32_t type __attribute__((ext_vector_type(4))); };
+struct Bytes<16, 2> {
+  typedef u32x4 type;
+  typedef u32x4 memory __attribute__((aligned(2)));
+};
 template <>
-struct Bytes<4> { using type = uint32_t; };
+struct Bytes<16, 4> {
+  typedef u32x4 type;
+  typedef u32x4 memory __attribute__((aligned(4)));
+};
 template <>
-struct Bytes<2> { using type = uint16_t; };
+struct Bytes<4, 2> {
+  typedef uint32_t type;
+  typedef uint32_t memory __attribute__((aligned(2)));
+};
+template <>
+struct Bytes<4, 4> {
+  typedef uint32_t type;
+  typedef uint32_t memory;
+};
+template <>
+struct Bytes<2, 2> {
+  typedef uint16_t type;
+  typedef uint16_t memory;
+};
 
 // Moves heads 0 .. n-1 of a workgroup, at_once of them by each wave in turn, from from(i) to to(i) (null: not
 // written), turned by the angles of row turned(i) (below 0: not turned).  WV: elements of a vector of memory; PV:
@@ -208,7 +228,8 @@ template <typename T, int WV, int PV, bool ADJ, typename From, typename To, type
 __device__ __forceinline__ void turn_heads(const Turns& t, const Cut& c, int n, T* lds, const float2* cs, From from, To to,
                                            Turned turned, Between between) {
   constexpr int NV = held_by(WV * static_cast<int>(sizeof(T))) / (64 * WV * static_cast<int>(sizeof(T)));
-  using M = typename Bytes<WV * static_cast<int>(sizeof(T))>::type;
+  using M = typename Bytes<WV * static_cast<int>(sizeof(T)), static_cast<int>(sizeof(T))>::type;
+  using InMemory = typename Bytes<WV * static_cast<int>(sizeof(T)), static_cast<int>(sizeof(T))>::memory;
   using V = Vec<T, PV>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), step = 4 * c.at_once,
             vectors = c.at_once * c.vectors, chunks = c.at_once * c.chunks, D = c.vectors * WV;
@@ -219,7 +240,7 @@ __device__ __forceinline__ void turn_heads(const Turns& t, const Cut& c, int n, 
       const int v = k * 64 + lane, g = c.by_vectors.of(v);
       if (v >= vectors || i0 + g >= n) continue;
       const T* x = from(i0 + g);
-      if (x != nullptr) held[k] = *reinterpret_cast<const M*>(x + (v - g * c.vectors) * WV);
+      if (x != nullptr) held[k] = *reinterpret_cast<const InMemory*>(x + (v - g * c.vectors) * WV);
     }
   };
   const int first = wave * c.at_once;
@@ -256,7 +277,7 @@ __device__ __forceinline__ void turn_heads(const Turns& t, const Cut& c, int n, 
       const int v = k * 64 + lane, g = c.by_vectors.of(v);
       if (v >= vectors || i0 + g >= n) continue;
       T* y = to(i0 + g);
-      if (y != nullptr) *reinterpret_cast<M*>(y + (v - g * c.vectors) * WV) = *reinterpret_cast<const M*>(lds + v * WV);
+      if (y != nullptr) *reinterpret_cast<InMemory*>(y + (v - g * c.vectors) * WV) = *reinterpret_cast<const M*>(lds + v * WV);
     }
   }
 }
@@ -295,16 +316,11 @@ inline Turns turns_of(int32_t axes, const int32_t* sections, int32_t layout, int
   return t;
 }
 
-// Elements of the vectors that fit memory at an address or along strides, of those that there are kernels for:
-// 16 bytes, 4 (bf16), one element.
+// Elements of a vector of memory: 16 bytes, 4 (bf16) or one element, the most that a head is a whole number of.
 inline int narrower(int w, int es) { return es == 2 && w > 2 ? 2 : 1; }
-inline int fit(int w, int es, const void* p) {
-  while (w > 1 && reinterpret_cast<uintptr_t>(p) % (static_cast<unsigned>(w) * es) != 0) w = narrower(w, es);
-  return w;
-}
-inline int fit(int w, int es, const int64_t* strides, int n) {
-  for (int i = 0; i < n; ++i)
-    while (w > 1 && strides[i] % w != 0) w = narrower(w, es);
+inline int vector_of(int64_t head_dim, int es) {
+  int w = 16 / es;
+  while (w > 1 && head_dim % w != 0) w = narrower(w, es);
   return w;
 }
 // Pairs of a chunk: as many as a vector of memory has elements, if every run of the layout is whole chunks.

@@ -77,12 +77,24 @@ __global__ __launch_bounds__(256) void rotary_kernel(Args a) {
       });
 }
 
-// Chunks of a thread under way at a time.
-constexpr int kUnits = 2;
+template <typename T, int PV>
+__device__ __forceinline__ Vec<T, PV> in_memory(const T* p) {
+  using B = Bytes<PV * static_cast<int>(sizeof(T)), static_cast<int>(sizeof(T))>;
+  return __builtin_bit_cast(Vec<T, PV>, static_cast<typename B::type>(*reinterpret_cast<const typename B::memory*>(p)));
+}
+template <typename T, int PV>
+__device__ __forceinline__ void to_memory(T* p, const Vec<T, PV>& v) {
+  using B = Bytes<PV * static_cast<int>(sizeof(T)), static_cast<int>(sizeof(T))>;
+  *reinterpret_cast<typename B::memory*>(p) = __builtin_bit_cast(typename B::type, v);
+}
+
+// Chunks of a thread under way at a time, by the bytes of a vector.
+constexpr int units_of(int bytes) { return bytes == 16 ? 2 : 4; }
 
 template <typename T, int PV, bool ADJ>
 __global__ __launch_bounds__(256) void rotary_grad_kernel(Args a) {
   using V = Vec<T, PV>;
+  constexpr int kUnits = units_of(sizeof(V));
   extern __shared__ float2 cs[];
   __shared__ float red[4 * kUnits * 256];
   const int tid = threadIdx.x;
@@ -119,12 +131,12 @@ __global__ __launch_bounds__(256) void rotary_grad_kernel(Args a) {
         const Place p = place(n.chunk);
         const Row w = row_of(b0, l0, n.r, a.L);
         const T* x = static_cast<const T*>(a.x) + w.b * a.xs[0] + w.l * a.xs[1] + n.h * a.xs[2];
-        v1[k] = *reinterpret_cast<const V*>(x + p.e1);
-        if (p.e2 < a.D) v2[k] = *reinterpret_cast<const V*>(x + p.e2);
+        v1[k] = in_memory<T, PV>(x + p.e1);
+        if (p.e2 < a.D) v2[k] = in_memory<T, PV>(x + p.e2);
         if (n.chunk < a.turned) {
           const T* x0 = static_cast<const T*>(a.x0) + w.b * a.x0s[0] + w.l * a.x0s[1] + n.h * a.x0s[2];
-          w1[k] = *reinterpret_cast<const V*>(x0 + p.e1);
-          w2[k] = *reinterpret_cast<const V*>(x0 + p.e2);
+          w1[k] = in_memory<T, PV>(x0 + p.e1);
+          w2[k] = in_memory<T, PV>(x0 + p.e2);
         }
       }
       if (h0 == 0 && u0 == 0) {
@@ -163,8 +175,8 @@ __global__ __launch_bounds__(256) void rotary_grad_kernel(Args a) {
           }
           if (a.out != nullptr) {
             T* y = static_cast<T*>(a.out) + (static_cast<int64_t>(row0 + n.r) * a.H + n.h) * a.D;
-            *reinterpret_cast<V*>(y + p.e1) = v1[k];
-            if (p.e2 < a.D) *reinterpret_cast<V*>(y + p.e2) = v2[k];
+            to_memory<T, PV>(y + p.e1, v1[k]);
+            if (p.e2 < a.D) to_memory<T, PV>(y + p.e2, v2[k]);
           }
         }
 #pragma unroll
@@ -208,13 +220,13 @@ const void* grad_kernel(bool bf16, int pv, bool adjacent) {
   return pv == 4 ? grad_kernel<float, 4>(adjacent) : grad_kernel<float, 1>(adjacent);
 }
 
-// Rows of rotary_grad_kernel: as many as give each thread two chunks, fewer where that leaves fewer than four
+// Rows of rotary_grad_kernel: as many as give each thread its chunks at a time, fewer where that leaves fewer than four
 // workgroups a CU, down to a chunk for each thread.
-void grad_cut(Args* a, int pv) {
+void grad_cut(Args* a, int pv, int es) {
   Cut& c = a->cut;
   a->turned = a->t.pairs / pv;
   c.chunks = a->turned + (a->D - 2 * a->t.pairs + 2 * pv - 1) / (2 * pv);
-  const int most = kUnits * 256;
+  const int most = units_of(pv * es) * 256;
   c.heads = std::max(1, std::min(a->H, most / c.chunks));
   const int per = c.heads * c.chunks;
   int rows = std::min(most / per, kTurns / a->t.pairs);
@@ -249,14 +261,11 @@ int run(const dcn_rotary_desc* d, Args* a, const void* positions, const float* f
   a->H = static_cast<int>(d->heads);
   a->D = static_cast<int>(d->head_dim);
   a->rows = static_cast<int>(d->batch * d->length);
-  int w = 16 / es;
-  while (w > 1 && d->head_dim % w != 0) w = narrower(w, es);
-  w = fit(fit(fit(w, es, a->x), es, a->out), es, a->xs, 3);
-  if (a->x0 != nullptr) w = fit(fit(w, es, a->x0), es, a->x0s, 3);
+  const int w = vector_of(d->head_dim, es);
   const int pv = pairs_at_once(a->t, d->sections, w, es);
   const void* fn;
   if (a->gp != nullptr) {
-    grad_cut(a, pv);
+    grad_cut(a, pv, es);
     a->cut.groups = 1;
     fn = grad_kernel(bf16, pv, adjacent);
   } else {

@@ -407,8 +407,8 @@ int dcn_group_norm_backward(const dcn_norm_desc* desc, const void* x, const void
  *  - Arithmetic: angles and their reduction in 64 bits, so that far positions keep their digits (an angle
  *    is off by 2^-51 of itself, 5e-7 at 2^30); cosines and sines are within 2^-23, products and sums in
  *    fp32, out rounded once.
- *  - Memory is read and written 16 bytes, 4 or an element at a time, the widest that fits the addresses,
- *    strides and head_dim.
+ *  - Memory is read and written 16 bytes, 4 or an element at a time, the widest that divides a head,
+ *    wherever it starts.
  * DCN_E_ARG: an invalid descriptor (a negative size or stride, no head, axes outside 1 .. 4, a section
  * below 1, 2 pairs > head_dim, an unknown layout or position type) or a NULL required pointer;
  * DCN_E_UNSUPPORTED: another dtype, head_dim above 512 or 2^31 rows of heads; DCN_E_HIP as elsewhere;
