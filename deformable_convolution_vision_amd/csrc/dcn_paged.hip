@@ -42,8 +42,9 @@ struct PagedArgs {
   const int32_t *table, *lengths;
   void* out;
   float* lse;
-  float* part;             // [part][16][DP]
-  float* part_ml;          // [part][16][2]
+  float* part;             // [key head's tile][slot][16][DP]: parts of sequences that have several,
+  float* part_ml;          // [..][16][2]
+  int4 *shares, *joins;    // of many sequences: paged_shares_kernel's lists (else null)
   int64_t qs[2], ks[3], vs[3], ts;
   int B, Hq, Hkv, g, D;
   int tiles;               // of 16 rows, of a key head
@@ -51,7 +52,7 @@ struct PagedArgs {
   int split;               // whether sequences may have several parts
   int aim;                 // parts of a key head's tile that the division aims at,
   int least;               // of so many blocks at least
-  int grid;                // workgroups of a key head's tile (the most parts that there can be)
+  int grid, slots;         // workgroups of a key head's tile (the most parts that there can be); slots
   uint32_t first;          // workgroups of launches before this one
   uint32_t page_m;         // position / page_size is the upper half of position * page_m, shifted by page_s
   int page_s;              // (page_m 0: pages of one position)
@@ -101,10 +102,11 @@ __device__ __forceinline__ float sum_of_4(float x) {
 // ---- which workgroup has what
 
 __device__ __forceinline__ int length_of(const PagedArgs& a, int b) { return min(max(a.lengths[b], 0), a.capacity); }
-// blocks of sequence b0 + lane (0 where there is none)
-__device__ __forceinline__ int blocks_of(const PagedArgs& a, int b0) {
-  const int b = b0 + (threadIdx.x & 63);
-  return b < a.B ? (length_of(a, b) + kKeys - 1) / kKeys : 0;
+__device__ __forceinline__ int blocks_of(const PagedArgs& a, int b) { return (length_of(a, b) + kKeys - 1) / kKeys; }
+// of sequence `lane` (0 where there is none)
+__device__ __forceinline__ int blocks_of_lane(const PagedArgs& a) {
+  const int b = threadIdx.x & 63;
+  return b < a.B ? blocks_of(a, b) : 0;
 }
 __device__ __forceinline__ int parts_of(int blocks, int quota) { return max(1, (blocks + quota - 1) / quota); }
 
@@ -124,46 +126,93 @@ __device__ __forceinline__ int running_sum(int v) {
 }
 __device__ __forceinline__ int lanes_total(int v) { return __builtin_amdgcn_readlane(running_sum(v), 63); }
 
+// Up to kLanes sequences: one for each lane, and every workgroup of both launches finds its part on its own.
+constexpr int kLanes = 64;
+
 // Blocks of a part: the fewest with which all sequences together have at most `aim` parts (aim is at least
-// as many as there are sequences, so the search ends: it grows until one part holds the longest).  The same in all
-// workgroups of both launches.  mine: blocks_of(a, 0).
+// as many as there are sequences, so the search ends: it grows until one part holds the longest).  mine:
+// blocks_of_lane.
 __device__ __forceinline__ int quota_of(const PagedArgs& a, int mine) {
-  float total = 0.f;     // (as near as the search's first guess needs)
-  for (int b0 = 0; b0 < a.B; b0 += 64) total += static_cast<float>(lanes_total(b0 == 0 ? mine : blocks_of(a, b0)));
+  // (as near as the search's first guess needs; in two sums, for 64 of 2^26 blocks pass 32 bits)
+  const float total = static_cast<float>(lanes_total(mine >> 8)) * 256.f + static_cast<float>(lanes_total(mine & 255));
   int quota = max(a.least, static_cast<int>(total / static_cast<float>(a.aim)));
-  while (true) {
-    int parts = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 64) {
-      const int n = b0 == 0 ? mine : blocks_of(a, b0);
-      parts += lanes_total(b0 + static_cast<int>(threadIdx.x & 63) < a.B ? parts_of(n, quota) : 0);
-    }
-    if (parts <= a.aim) return quota;
-    quota += max(1, quota / 16);
-  }
+  while (lanes_total(static_cast<int>(threadIdx.x & 63) < a.B ? parts_of(mine, quota) : 0) > a.aim) quota += max(1, quota / 16);
+  return quota;
 }
 
-// The part of workgroup `index` of a key head's tile: blocks first .. last - 1 of sequence b, one of `parts`
-// parts, which follow `before` parts of the sequences before it.  b < 0: no part is left for this workgroup.
+// The part of workgroup `index` of a key head's tile: blocks first .. last - 1 of sequence b, in slot `slot` where the
+// sequence has several parts (-1: it has one).  b < 0: no part is left for this workgroup.
 struct Share {
-  int b, first, last, parts, number;
+  int b, first, last, slot;
 };
 __device__ __forceinline__ Share share_of(const PagedArgs& a, int index) {
-  if (a.split == 0) return {index, 0, (length_of(a, index) + kKeys - 1) / kKeys, 1, index};
-  const int lane = threadIdx.x & 63, mine = blocks_of(a, 0), quota = quota_of(a, mine);
-  int before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 64) {
-    const int n = b0 == 0 ? mine : blocks_of(a, b0), parts = b0 + lane < a.B ? parts_of(n, quota) : 0;
-    const int upto = running_sum(parts), at = index - before;
-    const uint64_t hit = __ballot(at < upto && at >= upto - parts);
-    if (hit != 0) {
-      const int who = __builtin_ctzll(hit), blocks = __builtin_amdgcn_readlane(n, who),
-                have = __builtin_amdgcn_readlane(parts, who), part = at - (__builtin_amdgcn_readlane(upto, who) - have);
-      const int first = part * quota;
-      return {b0 + who, first, min(blocks, first + quota), have, index};
-    }
-    before += __builtin_amdgcn_readlane(upto, 63);
+  if (a.split == 0) return {index, 0, blocks_of(a, index), -1};
+  if (a.shares != nullptr) {
+    const int4 e = a.shares[index];
+    return {e.x, e.y, e.z, e.w};
   }
-  return {-1, 0, 0, 1, index};
+  const int lane = threadIdx.x & 63, mine = blocks_of_lane(a), quota = quota_of(a, mine),
+            parts = lane < a.B ? parts_of(mine, quota) : 0, upto = running_sum(parts);
+  const uint64_t hit = __ballot(index < upto && index >= upto - parts);
+  if (hit == 0) return {-1, 0, 0, -1};
+  const int who = __builtin_ctzll(hit), blocks = __builtin_amdgcn_readlane(mine, who),
+            have = __builtin_amdgcn_readlane(parts, who), part = index - (__builtin_amdgcn_readlane(upto, who) - have);
+  const int first = part * quota;
+  return {who, first, min(blocks, first + quota), have > 1 ? index : -1};
+}
+
+// More sequences: one workgroup makes lists first, for a search over all of them in every workgroup takes longer than its
+// part (8 heads of 64, lengths to 4096: 512 sequences 762 us, from the lists 465, a copy of the bytes 434; 2048 sequences
+// 7217, 1723 and 1767).  With a quota of total / (aim - B) blocks at least, the parts beyond one of each sequence
+// are at most aim - B, sequences with several fewer than that, and their parts fewer than twice that.
+__global__ __launch_bounds__(1024) void paged_shares_kernel(PagedArgs a) {
+  __shared__ int64_t totals[16];
+  __shared__ int sums[3][16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, spare = a.aim - a.B;
+  const int64_t per = (static_cast<int64_t>(a.B) + 1023) / 1024;      // a thread has as many sequences, side by side
+  const int b0 = static_cast<int>(min<int64_t>(a.B, tid * per)), b1 = static_cast<int>(min<int64_t>(a.B, (tid + 1) * per));
+  int64_t total = 0;
+  for (int b = b0; b < b1; ++b) total += blocks_of(a, b);
+#pragma unroll
+  for (int n = 32; n > 0; n /= 2) total += __shfl_xor(total, n, 64);
+  if (lane == 0) totals[wave] = total;
+  __syncthreads();
+  total = 0;
+  for (int w = 0; w < 16; ++w) total += totals[w];
+  const int quota = static_cast<int>(min<int64_t>(max<int64_t>(a.least, (total + spare - 1) / spare), 0x7fffffff));
+  int have[3] = {0, 0, 0};       // parts, sequences with several, slots
+  for (int b = b0; b < b1; ++b) {
+    const int n = blocks_of(a, b), parts = n > quota ? (n - 1) / quota + 1 : 1;
+    have[0] += parts;
+    if (parts > 1) {
+      ++have[1];
+      have[2] += parts;
+    }
+  }
+  int before[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int upto = running_sum(have[i]);
+    before[i] = upto - have[i];
+    if (lane == 63) sums[i][wave] = upto;
+  }
+  __syncthreads();
+  int all[2] = {0, 0};
+  for (int w = 0; w < 16; ++w) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      if (w < wave) before[i] += sums[i][w];
+      if (i < 2) all[i] += sums[i][w];
+    }
+  }
+  for (int b = b0; b < b1; ++b) {
+    const int n = blocks_of(a, b), parts = n > quota ? (n - 1) / quota + 1 : 1;
+    if (parts > 1) a.joins[before[1]++] = make_int4(b, before[2], parts, 0);
+    for (int k = 0; k < parts; ++k)
+      a.shares[before[0]++] = make_int4(b, k * quota, min(n, (k + 1) * quota), parts > 1 ? before[2]++ : -1);
+  }
+  for (int i = all[0] + tid; i < a.grid; i += 1024) a.shares[i] = make_int4(-1, 0, 0, -1);
+  for (int i = all[1] + tid; i < spare; i += 1024) a.joins[i] = make_int4(-1, 0, 0, 0);
 }
 
 __device__ uint4 paged_zero_row[32];   // what positions without a row read: 512 bytes, a row of 128 fp32
@@ -359,7 +408,7 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
   const int rr = lane / 4, d0 = (lane & 3) * 4, to = tile * 16 + rr, head = hk * a.g + to;
   const bool writes = wave < CD && to < a.g;
   float f[W], mm = kNegInf, ll = 0.f, inv = 1.f;
-  const int64_t prow = (static_cast<int64_t>(ht) * a.grid + part.number) * 16 + rr;
+  const int64_t prow = (static_cast<int64_t>(ht) * a.slots + part.slot) * 16 + rr;
 #pragma unroll
   for (int i = 0; i < DT; i += CD) {
     if (i > 0) __syncthreads();
@@ -379,7 +428,7 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
         ll = fmaf(f[j], ls[j * 16 + rr], ll);
       }
       const bool once = wave == 0 && d0 == 0;
-      if (part.parts > 1) {
+      if (part.slot >= 0) {
         if (once) *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(mm, ll);
       } else {
         inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);      // no position: zeros; a NaN sum stays NaN
@@ -397,7 +446,7 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
       acc.w = fmaf(f[j], v.w, acc.w);
     }
     const int d = 16 * (i + wave) + d0;
-    if (part.parts > 1) {
+    if (part.slot >= 0) {
       *reinterpret_cast<float4*>(a.part + prow * DP + d) = acc;
     } else {
       T* op = static_cast<T*>(a.out) + (static_cast<int64_t>(part.b) * a.Hq + head) * a.D;
@@ -409,7 +458,8 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
   }
 }
 
-// Adds the parts of a sequence that was split: one workgroup for each sequence and query head; 8 threads of
+// Adds the parts of a sequence that was split: one workgroup for each such sequence (with up to kLanes of them, for
+// each sequence) and query head; 8 threads of
 // every 4 elements (16, 32 for smaller heads) take its parts in turn.
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a) {
@@ -417,17 +467,22 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a) {
   __shared__ float4 acc_of[S][V4 + 1];
   __shared__ float2 ml_of[S];
   const uint32_t at = a.first + blockIdx.x;
-  const int b = at / a.Hq, head = at - b * a.Hq, hk = head / a.g, row = head % a.g,
-            tile = row / 16, rr = row % 16;
-  // the same division into parts as the first launch's: this sequence's first part
-  const int mine = blocks_of(a, 0), quota = quota_of(a, mine), splits = parts_of((length_of(a, b) + kKeys - 1) / kKeys, quota);
-  if (splits == 1) return;
-  int before = 0;
-  for (int b0 = 0; b0 < b; b0 += 64) {
-    const int n = b0 == 0 ? mine : blocks_of(a, b0);
-    before += lanes_total(b0 + static_cast<int>(threadIdx.x & 63) < b ? parts_of(n, quota) : 0);
+  const int number = at / a.Hq, head = at - number * a.Hq, hk = head / a.g, row = head % a.g, tile = row / 16, rr = row % 16;
+  int b = number, splits, before;
+  if (a.joins != nullptr) {
+    const int4 e = a.joins[number];
+    b = e.x;
+    if (b < 0) return;
+    before = e.y;
+    splits = e.z;
+  } else {       // the same division into parts as the first launch's: this sequence's first part
+    const int lane = threadIdx.x & 63, mine = blocks_of_lane(a), quota = quota_of(a, mine),
+              parts = lane < a.B ? parts_of(mine, quota) : 0;
+    splits = __builtin_amdgcn_readlane(parts, b);
+    if (splits == 1) return;
+    before = __builtin_amdgcn_readlane(running_sum(parts), b) - splits;
   }
-  const int64_t p0 = ((static_cast<int64_t>(hk) * a.tiles + tile) * a.grid + before) * 16 + rr;
+  const int64_t p0 = ((static_cast<int64_t>(hk) * a.tiles + tile) * a.slots + before) * 16 + rr;
   const int d = threadIdx.x % V4, k = threadIdx.x / V4;
   float m = kNegInf, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -495,8 +550,8 @@ constexpr int waves_for(int es, int dp, bool wide) {
 }
 
 struct PagedPlan {
-  int dp, waves, tiles, aim, least, grid;
-  bool split, wide, rounds;
+  int dp, waves, tiles, aim, least, grid, slots;
+  bool split, wide, rounds, listed;
 };
 // The division into parts.  A sequence has several only where its blocks may be more than kChain for each wave of a
 // wide workgroup: below, the launch that joins them costs more than it saves (one sequence, 8 heads of 64:
@@ -520,14 +575,26 @@ PagedPlan plan_of(const dcn_paged_desc* d) {
   p.aim = static_cast<int>(p.rounds ? d->batch + kRounds * 2 * room : room);
   p.least = (p.rounds ? kLeast : 1) * p.waves;
   p.grid = p.split ? p.aim : static_cast<int>(d->batch);
+  p.listed = p.split && d->batch > kLanes;     // (these have rounds: aim is beyond the batch)
+  p.slots = p.listed ? 2 * (p.aim - static_cast<int>(d->batch)) : p.aim;
   return p;
 }
-size_t workspace_of(const dcn_paged_desc* d, const PagedPlan& p, size_t* ml_at) {
-  *ml_at = 0;
-  if (!p.split) return 0;
-  const size_t rows = static_cast<size_t>(d->key_heads) * p.tiles * p.grid * 16;
-  *ml_at = rows * p.dp * 4;
-  return (*ml_at + rows * 8 + 255) / 256 * 256;
+// The workspace: parts, their maxima and sums, the lists.
+struct Layout {
+  size_t ml, shares, joins, bytes;
+};
+Layout layout_of(const dcn_paged_desc* d, const PagedPlan& p) {
+  Layout l{};
+  if (!p.split) return l;
+  const size_t rows = static_cast<size_t>(d->key_heads) * p.tiles * p.slots * 16;
+  l.ml = rows * p.dp * 4;
+  l.shares = l.joins = l.bytes = l.ml + rows * 8;
+  if (p.listed) {
+    l.joins = l.shares + static_cast<size_t>(p.grid) * sizeof(int4);
+    l.bytes = l.joins + static_cast<size_t>(p.aim - d->batch) * sizeof(int4);
+  }
+  l.bytes = (l.bytes + 255) / 256 * 256;
+  return l;
 }
 
 template <typename T, int DP, int W>
@@ -569,8 +636,7 @@ extern "C" int dcn_paged_attention_workspace_bytes(const dcn_paged_desc* d, size
   if (bytes == nullptr) return DCN_E_ARG;
   const int rc = check(d);
   if (rc != DCN_OK) return rc;
-  size_t at;
-  *bytes = d->batch == 0 ? 0 : workspace_of(d, plan_of(d), &at);
+  *bytes = d->batch == 0 ? 0 : layout_of(d, plan_of(d)).bytes;
   return DCN_OK;
 }
 
@@ -587,8 +653,8 @@ extern "C" int dcn_paged_attention(const dcn_paged_desc* d, const void* q, const
       (cache && (key_pages == nullptr || value_pages == nullptr || page_table == nullptr)))
     return DCN_E_ARG;
   const PagedPlan p = plan_of(d);
-  size_t ml_at;
-  const size_t need = workspace_of(d, p, &ml_at);
+  const Layout l = layout_of(d, p);
+  const size_t need = l.bytes;
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 256 != 0))
     return DCN_E_WORKSPACE;
   PagedArgs a{};
@@ -600,8 +666,13 @@ extern "C" int dcn_paged_attention(const dcn_paged_desc* d, const void* q, const
   a.out = out;
   a.lse = lse;
   if (need > 0) {
-    a.part = static_cast<float*>(workspace);
-    a.part_ml = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + ml_at);
+    unsigned char* const w = static_cast<unsigned char*>(workspace);
+    a.part = reinterpret_cast<float*>(w);
+    a.part_ml = reinterpret_cast<float*>(w + l.ml);
+    if (p.listed) {
+      a.shares = reinterpret_cast<int4*>(w + l.shares);
+      a.joins = reinterpret_cast<int4*>(w + l.joins);
+    }
   }
   for (int i = 0; i < 2; ++i) a.qs[i] = d->q_stride[i];
   for (int i = 0; i < 3; ++i) {
@@ -623,6 +694,7 @@ extern "C" int dcn_paged_attention(const dcn_paged_desc* d, const void* q, const
   a.aim = p.aim;
   a.least = p.least;
   a.grid = p.grid;
+  a.slots = p.slots;
   a.c = d->scale * kLog2e;
   const bool bf16 = d->dtype == DCN_BF16;
   const int es = bf16 ? 2 : 4;
@@ -635,12 +707,13 @@ extern "C" int dcn_paged_attention(const dcn_paged_desc* d, const void* q, const
     a.page_s = s - 1;
   }
   void* args[] = {&a};
+  if (p.listed && !launch_paged(reinterpret_cast<const void*>(&paged_shares_kernel), 1, 1024, args, &a, stream)) return DCN_E_HIP;
   if (!launch_paged(bf16 ? paged_fn<uint16_t>(p, rows) : paged_fn<float>(p, rows),
                     static_cast<int64_t>(p.grid) * a.Hkv * a.tiles, 64 * p.waves, args, &a, stream))
     return DCN_E_HIP;
   if (p.split) {
-    if (!launch_paged(bf16 ? join_fn<uint16_t>(p.dp) : join_fn<float>(p.dp), static_cast<int64_t>(a.B) * a.Hq, 256,
-                      args, &a, stream))
+    const int64_t several = p.listed ? p.aim - a.B : a.B;
+    if (!launch_paged(bf16 ? join_fn<uint16_t>(p.dp) : join_fn<float>(p.dp), several * a.Hq, 256, args, &a, stream))
       return DCN_E_HIP;
   }
   return DCN_OK;

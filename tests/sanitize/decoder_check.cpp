@@ -153,7 +153,15 @@ void paged(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page, int64_t 
   expect(dcn_paged_attention(&d, p, p, p, n, n, p, f, p, nb, nullptr) == DCN_OK, "status");
   const int64_t tiles = (Hq / Hkv + 15) / 16;
   expect(groups >= B * Hkv * tiles, "a workgroup for each sequence and key head at least");
-  if (nb > 0) expect(nb >= static_cast<size_t>(groups - B * Hq) * 16 * (D + 2) * 4, "a part for each workgroup");
+  if (nb == 0) return;
+  if (B <= 64) {
+    expect(nb >= static_cast<size_t>(groups - B * Hq) * 16 * (D + 2) * 4, "a part for each workgroup");
+  } else {   // one workgroup makes lists of G workgroups of each tile and of G - B sequences that are joined, 16 bytes each
+    const int64_t heads = Hkv * tiles, G = (groups - 1 + B * Hq) / (heads + Hq);
+    expect(1 + G * heads + (G - B) * Hq == groups && G > B, "workgroups of the lists");
+    expect(nb >= static_cast<size_t>(heads) * 2 * (G - B) * 16 * (D + 2) * 4 + static_cast<size_t>(2 * G - B) * 16,
+           "two parts for each workgroup beyond the sequences, and the lists");
+  }
 }
 
 }  // namespace

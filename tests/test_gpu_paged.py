@@ -51,6 +51,11 @@ ATTENTION = {
     "head_96": ([300, 40], 6, 2, 96, 32),
     "many_short": ([(7 * i) % 50 for i in range(150)], 2, 1, 32, 16),
     "more_sequences_than_fill": ([40 + (13 * i) % 700 for i in range(70)], 8, 8, 64, 32),
+    # more sequences than a wave has lanes, with tables for long ones: lists of the parts
+    "lists": ([(131 * i) % 1700 for i in range(130)], 4, 2, 64, 32),
+    "lists_65_one_long": ([5] * 40 + [7000] + [0] * 24, 1, 1, 128, 16),
+    "lists_two_a_thread": ([(17 * i) % 40 for i in range(1500)] + [2500, 2000], 2, 1, 32, 8),
+    "lists_more_heads_than_fill": ([(7 * i) % 30 for i in range(70)] + [1800], 270, 270, 8, 64),
 }
 
 
@@ -110,6 +115,15 @@ def test_attention(name, dtype):
     assert torch.equal(again, out), "the same call gave other bits"
     args = make(name, dtype, heads_first=True)
     compare(args, dtype, name + " heads first", scale=0.31)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_lists_of_equal_and_of_no_lengths(dtype):
+    """Equal long ones (a quota that every sequence reaches), all empty, and lengths beyond the table."""
+    q, k, v, table, _ = make("lists", dtype)
+    width = table.shape[1] * k.shape[1]
+    for n in (0, 1, width, width + 1000):
+        compare((q, k, v, table, torch.full((len(q),), n, dtype=torch.int32, device="cuda")), dtype, f"{n} each")
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -371,10 +385,10 @@ def test_a_prompt_and_tokens(dtype):
         check(f64(wl[:, :, 0]), ref[2], ref[3], "dense lse")
 
 
-def test_on_a_side_stream_and_in_graphs():
+@pytest.mark.parametrize("name", ["one_long_among_short", "lists"])
+def test_on_a_side_stream_and_in_graphs(name):
     """A token's step (append, then attention) on another stream, and in two graphs that share a workspace;
     starts and lengths are read on the device at every replay."""
-    name = "one_long_among_short"
     q, kp, vp, table, lengths = make(name, "bf16")
     B, hq, d = q.shape
     hkv = kp.shape[2]
