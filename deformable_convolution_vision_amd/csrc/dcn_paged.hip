@@ -47,6 +47,7 @@ struct PagedArgs {
   int4 *shares, *joins;    // of many sequences: paged_shares_kernel's lists (else null)
   int64_t qs[2], ks[3], vs[3], ts;
   int B, Hq, Hkv, g, D;
+  int columns, tail, back; // of the output (see Rows): D, D and 0 where no vector is moved
   int tiles;               // of 16 rows, of a key head
   int num_pages, page_size, max_pages, capacity;
   int split;               // whether sequences may have several parts
@@ -217,9 +218,28 @@ __global__ __launch_bounds__(1024) void paged_shares_kernel(PagedArgs a) {
 
 __device__ uint4 paged_zero_row[32];   // what positions without a row read: 512 bytes, a row of 128 fp32
 
-// How rows are read: 16 bytes at a time all the padded head's width, 16 bytes at a time where the head has them, or
-// (heads of another size) element by element.
-enum Rows { kWhole, kVectors, kElements };
+// The first `back` elements of the 16 bytes that start at element `tail` of a fragment (of 8; elsewhere none) become 0.
+__device__ __forceinline__ void clear_first(Frag<uint16_t>& f, int tail, int back) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) f.w[w] &= tail != 0 || 2 * w >= back ? ~0u : 2 * w + 1 >= back ? 0xffff0000u : 0u;
+}
+__device__ __forceinline__ void clear_first(Frag<float>& f, int tail, int back) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (tail == e / 4 * 4 && e % 4 < back) f.f[e] = 0.f;
+}
+
+// How rows are read: 16 bytes at a time all the padded head's width; 16 bytes at a time where the head has them; heads
+// of another size the same, with the last 16 bytes moved back to end with the row; or (heads below 16 bytes) element by
+// element.  What the moved vector shares with the one before it is left out of the scores, and comes twice, alike, in
+// the output, whose columns from `tail` on are those of the row `back` elements before.
+enum Rows { kWhole, kVectors, kEnds, kElements };
+__device__ __forceinline__ void put(const PagedArgs& a, uint16_t* row, int c, float v) {
+  if (c < a.columns) row[c - (c >= a.tail ? a.back : 0)] = narrow<uint16_t>(v);
+}
+__device__ __forceinline__ void put(const PagedArgs& a, float* row, int c, float v) {
+  if (c < a.columns) row[c - (c >= a.tail ? a.back : 0)] = v;
+}
 
 template <typename T, int DP, int W, Rows ROWS>
 __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
@@ -259,9 +279,16 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
   const auto take = [&](const T* r, int d) {
     if constexpr (ROWS == kWhole) return load16(r + d);
     if constexpr (ROWS == kVectors) return load16(d < a.D ? r + d : zeros);
+    if constexpr (ROWS == kEnds) return load16(d < a.D ? r + min(d, a.D - KV) : zeros);
     return load_vec<T, false>(r, 0, d, a.D, true).u;
   };
 
+  // of a fragment at element 32 i on: what a moved vector shares with the one before becomes 0 (infinities, too)
+  const auto own = [&](Frag<T>& f, int i) {
+    if constexpr (ROWS == kEnds) {
+      if (i == a.tail / 32) clear_first(f, a.tail - 32 * i - 8 * quad, a.back);
+    }
+  };
   // the query head of this lane's column
   const int row = tile * 16 + col;
   const bool live = row < a.g;
@@ -275,6 +302,8 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
         const uint4 u = take(qp, 32 * i + 8 * quad + KV * h);
         __builtin_memcpy(reinterpret_cast<char*>(&qf[i]) + 16 * h, &u, 16);
       }
+#pragma unroll
+    for (int i = 0; i < KS; ++i) own(qf[i], i);
   }
 
   Frag<T> kf[2][KS];
@@ -320,7 +349,10 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
     for (int t = 0; t < 2; ++t) {
       s[t] = zero_acc4();
 #pragma unroll
-      for (int i = 0; i < KS; ++i) s[t] = mma16(kf[t][i], qf[i], s[t]);
+      for (int i = 0; i < KS; ++i) {
+        own(kf[t][i], i);
+        s[t] = mma16(kf[t][i], qf[i], s[t]);
+      }
     }
     wave_order();            // the last block's values have been read
 #pragma unroll
@@ -452,8 +484,7 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
       T* op = static_cast<T*>(a.out) + (static_cast<int64_t>(part.b) * a.Hq + head) * a.D;
       const float vals[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (d + j < a.D) op[d + j] = narrow<T>(vals[j]);
+      for (int j = 0; j < 4; ++j) put(a, op, d + j, vals[j]);
     }
   }
 }
@@ -519,8 +550,7 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a) {
   T* op = static_cast<T*>(a.out) + (static_cast<int64_t>(b) * a.Hq + head) * a.D;
   const float vals[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (4 * d + j < a.D) op[4 * d + j] = narrow<T>(vals[j]);
+  for (int j = 0; j < 4; ++j) put(a, op, 4 * d + j, vals[j]);
   if (d == 0 && a.lse != nullptr)
     a.lse[static_cast<int64_t>(b) * a.Hq + head] = ll == 0.f ? kNegInf : fmaf(ms, kLn2, logf(ll));
 }
@@ -599,9 +629,11 @@ Layout layout_of(const dcn_paged_desc* d, const PagedPlan& p) {
 
 template <typename T, int DP, int W>
 const void* paged_fn(Rows rows) {
+  if constexpr (DP == 32)
+    if (rows == kElements) return reinterpret_cast<const void*>(&paged_kernel<T, DP, W, kElements>);
   return rows == kWhole     ? reinterpret_cast<const void*>(&paged_kernel<T, DP, W, kWhole>)
          : rows == kVectors ? reinterpret_cast<const void*>(&paged_kernel<T, DP, W, kVectors>)
-                            : reinterpret_cast<const void*>(&paged_kernel<T, DP, W, kElements>);
+                            : reinterpret_cast<const void*>(&paged_kernel<T, DP, W, kEnds>);
 }
 template <typename T, int DP>
 const void* paged_fn(bool wide, Rows rows) {
@@ -698,7 +730,14 @@ extern "C" int dcn_paged_attention(const dcn_paged_desc* d, const void* q, const
   a.c = d->scale * kLog2e;
   const bool bf16 = d->dtype == DCN_BF16;
   const int es = bf16 ? 2 : 4;
-  const Rows rows = a.D == p.dp ? kWhole : a.D % (16 / es) == 0 ? kVectors : kElements;
+  const int kv = 16 / es;
+  const Rows rows = a.D == p.dp ? kWhole : a.D % kv == 0 ? kVectors : a.D > kv ? kEnds : kElements;
+  a.columns = a.tail = a.D;
+  if (rows == kEnds) {
+    a.tail = a.D / kv * kv;
+    a.columns = a.tail + kv;
+    a.back = a.columns - a.D;
+  }
   if (d->page_size > 1) {
     // of positions below 2^31: with 2^s >= page_size, 2^(31 + s) / page_size rounded up is off by less than 2^-31 of it
     int s = 0;

@@ -47,6 +47,14 @@ ATTENTION = {
     "sixteen_heads": ([513, 129], 16, 1, 128, 32),
     "odd_head": ([130, 77], 4, 2, 37, 16),                   # no vector fits a row
     "head_20": ([130, 77], 4, 2, 20, 16),
+    "head_9": ([40, 3], 2, 2, 9, 16),
+    "head_5": ([40, 3], 2, 1, 5, 16),                        # less than a vector in bf16
+    "head_1": ([70], 2, 1, 1, 16),
+    "head_33": ([90], 3, 1, 33, 8),
+    "head_67": ([130, 77, 0], 8, 2, 67, 16),
+    "head_98": ([90], 2, 1, 98, 16),
+    "head_127": ([513, 31], 8, 4, 127, 32),
+    "head_45_in_parts": ([2000, 30, 2900], 3, 3, 45, 16),
     "head_8": ([70], 2, 2, 8, 16),
     "head_96": ([300, 40], 6, 2, 96, 32),
     "many_short": ([(7 * i) % 50 for i in range(150)], 2, 1, 32, 16),
@@ -173,6 +181,21 @@ def test_not_finite_values_in_the_sequence():
     out = dcn.paged_attention(q, k, v, table, lengths)
     assert torch.all(out[0, 2:4, 5] == float("inf")) and torch.isfinite(out[0, :2]).all()
     assert torch.isnan(out[3, :2]).all() and torch.isfinite(out[3, 2:]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_key_of_minus_infinity_in_any_element(dtype):
+    """The position has a weight of zero, whichever element of an odd head it is (reads of 16 bytes overlap there)."""
+    for name in ("head_5", "head_9", "odd_head", "head_67"):
+        q, k, v, table, lengths = make(name, dtype)
+        q = q.abs() + 0.5
+        for e in range(q.shape[2]):
+            kk, vv = k.clone(), v.clone()
+            kk[int(table[0, 0]), 3, :, e] = -float("inf")
+            vv[int(table[0, 0]), 3] = 100.0
+            out = dcn.paged_attention(q, kk, vv, table, lengths)
+            vv[int(table[0, 0]), 3] = -100.0
+            assert torch.isfinite(out).all() and torch.equal(out, dcn.paged_attention(q, kk, vv, table, lengths)), (name, e)
 
 
 def test_strides():
