@@ -24,6 +24,14 @@
 // elements that it then shares with the one before are taken as zeros in its thread and not written.
 //
 // Arithmetic: fp32, every output rounded once.
+//
+// Memory bounds it.  8 x 16800 rows of 256 channels, bf16, two layer norms: 48.3 us for 275 MB, 5.7 TB/s (some of it
+// stays in the caches from call to call; 61 us between other work, a copy of as many bytes 55).
+// The gradients of 2 x 16800 rows, the gate shared by an image: 22.6 us for 104 MB, 4.6 TB/s, and 4.0 for the second
+// launch.  Rows of 1030 channels in fp32, gated element by element, 3 x 517 of them: 20.9 us for 51 MB, four steps of
+// two rows in each of 194 workgroups of six waves, which is what their registers (222) leave room for; rows of three
+// waves, of which the third has one lane, and 3.03 rounds of the chip in four steps are what they lose.  Without the next
+// row under way the first two took 65.3 and 47.2 us.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -338,12 +346,15 @@ __global__ __launch_bounds__(TR == 0 ? 1024 : 256) void residual_norm_kernel(Arg
 enum Side { kBare, kPlain, kGated };
 
 // NT: the most threads of a workgroup.  AHEAD: the next row's loads are under way over this one's sums and the
-// parameters stay in registers (a workgroup of 1024 threads has none to spare for that).
+// parameters stay in registers.  Else (a workgroup of 1024 threads has 128 registers a thread) a row is fetched when
+// it is at hand, the parameters with it, and all of the channels' sums but one are kept in the LDS, each thread's where
+// it alone reads them (2 x 525 rows of 8192, two layer norms, bf16: in registers, which spilled, 127 us, so 64).
 template <typename T, int TR, int NT, Side SIDE, Fit FIT, bool AHEAD>
 __global__ __launch_bounds__(NT) void residual_grad_kernel(Args a) {
   constexpr int SUMS = SIDE == kBare ? 2 : kSums;
   __shared__ float red[TR == 0 ? 64 : 1];
   __shared__ float add[NT > 512 ? 1 : NT * kE];
+  __shared__ float4 kept[AHEAD ? 1 : (kSums - 1) * 2 * NT];
   const Seat seat = seat_of<TR>(a);
   const Lane<T, FIT> l(seat.thread, seat.threads, a.C);
   const bool shared_gate = SIDE == kPlain && a.gkind == DCN_GATE_BATCH;
@@ -354,9 +365,8 @@ __global__ __launch_bounds__(NT) void residual_grad_kernel(Args a) {
   const int64_t r0 = begin + (blockIdx.x - static_cast<int64_t>(b) * a.runs) * a.per_run, r1 = min(end, r0 + a.per_run);
   // fs: gate and scale (kGated: scale); fw: that times the branch's weight.  Only a row's sums need what is not
   // the thread's own to be 0: the channels' sums and the gradients leave it out when they are written.
-  float w1[kE], b1[kE], w2[kE], fs[kE], fw[kE], sum[SUMS][kE];
+  float w1[kE], b1[kE], w2[kE], fs[kE], fw[kE], sum[AHEAD ? SUMS : 2][kE];   // (sum[0] of !AHEAD is not used)
   const auto params = [&] {
-    l.param(a.w2, 0, 1.f, w2);
     if constexpr (SIDE != kBare) {
       l.param(a.w1, 0, 1.f, w1);
       l.param(a.b1, 0, 0.f, b1);
@@ -371,11 +381,40 @@ __global__ __launch_bounds__(NT) void residual_grad_kernel(Args a) {
       }
     }
   };
-  if constexpr (AHEAD) params();
+  const auto then_params = [&] { l.param(a.w2, 0, 1.f, w2); };
+  if constexpr (AHEAD) {
+    params();
+    then_params();
+  }
 #pragma unroll
-  for (int n = 0; n < SUMS; ++n)
+  for (int n = 0; n < (AHEAD ? SUMS : 2); ++n)
 #pragma unroll
     for (int i = 0; i < kE; ++i) sum[n][i] = 0.f;
+  // adds p q to sum n; what is kept of it
+  const auto keep = [&](int n, int half) -> float4& { return kept[((n > 1 ? n - 1 : 0) * 2 + half) * NT + threadIdx.x]; };
+  const auto accumulate = [&](int n, const float (&p)[kE], const float (&q)[kE]) {
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int i = 0; i < kE; ++i) sum[n][i] = fmaf(p[i], q[i], sum[n][i]);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float4 k = keep(n, h);
+        k.x = fmaf(p[4 * h], q[4 * h], k.x);
+        k.y = fmaf(p[4 * h + 1], q[4 * h + 1], k.y);
+        k.z = fmaf(p[4 * h + 2], q[4 * h + 2], k.z);
+        k.w = fmaf(p[4 * h + 3], q[4 * h + 3], k.w);
+        keep(n, h) = k;
+      }
+    }
+  };
+  if constexpr (!AHEAD) {
+#pragma unroll
+    for (int n = 0; n < kSums; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (n != 1) keep(n, h) = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   int64_t row = r0 + seat.group, o = row * a.C;
   const int64_t step = static_cast<int64_t>(seat.groups) * a.C;
   const bool then = a.n2 != DCN_NORM_NONE;
@@ -423,14 +462,16 @@ __global__ __launch_bounds__(NT) void residual_grad_kernel(Args a) {
         u[i] = (u[i] - st.z) * st.w;
       }
       if (live) {
+        accumulate(0, gn, u);
 #pragma unroll
-        for (int i = 0; i < kE; ++i) {
-          sum[0][i] = fmaf(gn[i], u[i], sum[0][i]);
-          sum[1][i] += gn[i];
-        }
+        for (int i = 0; i < kE; ++i) sum[1][i] += gn[i];
       }
       float s[2] = {0.f, 0.f};
       l.clear(gn);
+      if constexpr (!AHEAD) {
+        __builtin_amdgcn_sched_barrier(0);   // (not sooner: registers)
+        then_params();
+      }
 #pragma unroll
       for (int i = 0; i < kE; ++i) {
         gn[i] *= w2[i];
@@ -443,6 +484,12 @@ __global__ __launch_bounds__(NT) void residual_grad_kernel(Args a) {
       for (int i = 0; i < kE; ++i) d[i] = fmaf(st.w, fmaf(-u[i], mu, gn[i] - mg), d[i]);
     }
     if (live && a.out != nullptr) l.store(a.out, o, d);
+    if constexpr (!AHEAD) {
+      __builtin_amdgcn_sched_barrier(0);
+      params();
+#pragma unroll
+      for (int i = 0; i < kE; ++i) z[i] = fmaf(v[i], w1[i], b1[i]);
+    }
     if constexpr (SIDE == kBare) {
       if (live && a.next != nullptr) l.store(a.next, o, d);
     } else {
@@ -457,12 +504,10 @@ __global__ __launch_bounds__(NT) void residual_grad_kernel(Args a) {
         for (int i = 0; i < kE; ++i) d[i] *= g[i];
       }
       if (live) {
-#pragma unroll
-        for (int i = 0; i < kE; ++i) {
-          sum[2][i] = fmaf(d[i], z[i], sum[2][i]);
-          sum[3][i] = fmaf(d[i], v[i], sum[3][i]);
-          sum[4][i] += d[i];
-        }
+        const float ones[kE] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+        accumulate(2, d, z);
+        accumulate(3, d, v);
+        accumulate(4, d, ones);
       }
       if (a.next != nullptr) {
         float s[2] = {0.f, 0.f};
@@ -488,10 +533,15 @@ __global__ __launch_bounds__(NT) void residual_grad_kernel(Args a) {
   float* part = a.part + static_cast<int64_t>(blockIdx.x) * kSums * a.C;
   if (seat.groups == 1) {
 #pragma unroll
-    for (int n = 0; n < SUMS; ++n)
+    for (int n = 0; n < SUMS; ++n) {
+      float f[kE];
 #pragma unroll
-      for (int i = 0; i < kE; ++i)
-        if (l.has(i)) part[n * a.C + l.channel(i)] = sum[n][i];
+      for (int i = 0; i < kE; ++i) {
+        if constexpr (AHEAD) f[i] = sum[n][i];
+        else f[i] = n == 1 ? sum[1][i] : reinterpret_cast<const float*>(&keep(n, i / 4))[i % 4];
+        if (l.has(i)) part[n * a.C + l.channel(i)] = f[i];
+      }
+    }
   } else if constexpr (NT <= 512) {
     const int pitch = seat.threads * kE;
 #pragma unroll

@@ -445,12 +445,13 @@ int dcn_rotary_backward(const dcn_rotary_desc* desc, const void* grad_out, const
  * Norms: DCN_NORM_NONE, DCN_NORM_RMS x / sqrt(mean x^2 + eps), DCN_NORM_LAYER (x - mean) / sqrt(var + eps)
  * (var over C values).  next_norm NONE: next is not written (and may be NULL).  gate: DCN_GATE_NONE,
  * DCN_GATE_BATCH [B][C], DCN_GATE_FULL [B][P][C].  scale, weights and biases [C], NULL for 1 and 0; those of
- * a norm that is NONE are not read.  stats [B][P][4] float32 where not NULL: mean and 1 / deviation of the
- * branch's row, then of out's (0 and 1 where there is none), which the backward takes.  Everything is dense
+ * a norm that is NONE are not read.  stats [B][P][4] float32, 16-byte aligned, where not NULL: mean and 1 /
+ * deviation of the branch's row, then of out's (0 and 1 where there is none), which the backward takes.
+ * A row of zeros with eps 0 gives NaN, as the formula does.  Everything is dense
  * in desc->dtype; out may be x or branch, next may be branch (out and next differ).  Arithmetic: fp32, the
  * variance about the mean, out and next rounded once.  Rows are read 16 bytes at a time wherever they start.
  * DCN_E_ARG: an invalid descriptor (a negative size, no channel, eps negative or not finite, an unknown
- * norm or gate) or a NULL required pointer; DCN_E_UNSUPPORTED: another dtype, more than 8192 channels,
+ * norm or gate), a NULL required pointer or stats off their alignment; DCN_E_UNSUPPORTED: another dtype, more than 8192 channels,
  * 2^31 rows, or more than 65530 batch elements with DCN_GATE_BATCH; DCN_E_HIP as elsewhere; all checked before any
  * launch.  No rows: nothing is launched. */
 enum dcn_row_norm { DCN_NORM_NONE = 0, DCN_NORM_RMS = 1, DCN_NORM_LAYER = 2 };
@@ -528,7 +529,9 @@ int dcn_paged_append(const dcn_append_desc* desc, const void* q, const void* k, 
  * cache holds behind a sequence's length, infinities and NaN included, does not matter.  Long sequences are
  * split over workgroups by the lengths on the device, and the parts joined in order: equal calls give equal
  * bits.  Arithmetic as for dcn_cross_attention, but for bf16 a weight enters the second product as two bf16
- * operands (2^-15 of it is lost).  The workspace (256-byte aligned, 0 bytes for short tables) holds the parts.
+ * operands (2^-15 of it is lost).  The workspace (256-byte aligned, 0 bytes for short tables) holds the parts; its
+ * size goes by the descriptor alone, not by the lengths.  Heads of 16 bytes and more are read 16 bytes at a time
+ * wherever they start.
  * DCN_E_ARG, DCN_E_UNSUPPORTED (head_dim > 128, sizes as for dcn_paged_append), DCN_E_WORKSPACE, DCN_E_HIP
  * as for dcn_cross_attention.  batch 0: nothing is launched. */
 typedef struct dcn_paged_desc {

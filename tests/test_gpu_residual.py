@@ -36,6 +36,9 @@ CASES = {
     "odd_wider": ((2, 9, 2047), "layer", "layer", "batch", True, True),
     "wide_512_threads": ((1, 9, 4096), "layer", "layer", "full", True, True),
     "most_channels": ((2, 3, 8192), "layer", "layer", "batch", True, True),
+    "wide_runs": ((2, 300, 4100), "layer", "rms", None, True, True),     # several rows of 1024 threads in turn
+    "wide_runs_gated": ((1, 517, 5001), "rms", "layer", "full", True, True),
+    "wide_runs_shared": ((2, 300, 8192), "layer", "layer", "batch", True, True),
     "most_odd_channels": ((1, 3, 8191), "layer", "rms", "full", True, True),
     "map": ((2, 50, 84, 256), "layer", "layer", "batch", True, True),
     "batch_600": ((600, 3, 32), "layer", "layer", "batch", True, True),
