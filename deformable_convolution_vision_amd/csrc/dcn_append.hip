@@ -9,10 +9,10 @@
 // A table entry that is no page of the cache, or a position outside the table, drops the row: the
 // check stands before the address is formed.
 //
-// Memory bounds a prompt: 8 x 4200 rows, ragged, of 16 + 4 + 4 heads of 128, bf16, take 84.2 us for 340.7 MB, 4.0 TB/s (a
-// large copy 4.99: the heads go to three places, and a workgroup's 4 rows form 64 pairs' angles for 20 heads).  Whole
-// turns of a workgroup's waves (cut_of) took as many rows without gaps from 108 us to 90, rows without tokens that are
-// not read the ragged ones from 86 to 84.  One token of eight sequences takes 5.4 us, a chain from its start and table
+// Memory bounds a prompt: 8 x 4200 rows, ragged, of 16 + 4 + 4 heads of 128, bf16, take 73 us for 340.7 MB, 4.7 TB/s (a
+// large copy 4.99).  Whole turns of a workgroup's waves (cut_of) took as many rows without gaps from 108 us to 90, rows
+// without tokens that are not read the ragged ones from 86 to 84, addresses in 24-bit products (apart) these to 73 and
+// those to 82.  One token of eight sequences takes 5.4 us, a chain from its start and table
 // entry to its address.
 
 #include <hip/hip_runtime.h>
@@ -42,38 +42,60 @@ struct AppendArgs {
   int L, per;              // rows of a sequence, and max(L, 1)
   int Hq, Hkv, D;
   int num_pages, page_size, max_pages;
+  bool near;               // near_by of q's, k's and v's strides, and of the pages' heads
 };
+
+// One of two values, both at hand (choosing between places of them would put the kernel's arguments into memory).
+template <typename V>
+__device__ __forceinline__ V pick(bool first, V x, V y) {
+  return first ? x : y;
+}
 
 template <typename T, int WV, int PV, bool ADJ>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
   extern __shared__ float2 cs[];
   __shared__ __attribute__((aligned(16))) unsigned char held[4 * kWave];
-  __shared__ int pages[kRows], places[kRows];      // of the rows; page -1: the row has none
+  __shared__ int64_t places[2][kRows];      // of the rows in the key and value pages, in elements; -1: the row has none
   const uint32_t at = a.first + blockIdx.x, block = at / a.cut.groups;
   const int row0 = static_cast<int>(block) * a.cut.rows, rows = min(a.cut.rows, a.rows - row0);
   const int b0 = static_cast<int>(static_cast<uint32_t>(row0) / static_cast<uint32_t>(a.per)), l0 = row0 - b0 * a.per;
   const int h0 = static_cast<int>(at - block * a.cut.groups) * a.cut.heads, heads = min(a.cut.heads, a.Hq + 2 * a.Hkv - h0);
   // (a ragged batch: all rows behind the tokens of their sequence; only their queries are read)
   const bool dead = a.counts != nullptr && l0 + rows <= a.per && l0 >= a.counts[b0];
+  const bool flat = a.near && l0 + rows <= a.per;      // (rows of one sequence)
+  const T* const q = static_cast<const T*>(a.q) + b0 * a.qs[0] + l0 * a.qs[1];
+  const T* const k = static_cast<const T*>(a.k) + b0 * a.ks[0] + l0 * a.ks[1];
+  const T* const v = static_cast<const T*>(a.v) + b0 * a.vs[0] + l0 * a.vs[1];
+  T* const out = static_cast<T*>(a.qo) + (static_cast<int64_t>(row0) * a.Hq + h0) * a.D;
+  T *const kp = static_cast<T*>(a.kp), *const vp = static_cast<T*>(a.vp);
+  const int64_t qs0 = a.qs[0], qs1 = a.qs[1], qs2 = a.qs[2], ks0 = a.ks[0], ks1 = a.ks[1], ks2 = a.ks[2], vs0 = a.vs[0],
+                vs1 = a.vs[1], vs2 = a.vs[2], kps2 = a.kps[2], vps2 = a.vps[2];
   turn_heads<T, WV, PV, ADJ>(
       a.t, a.cut, a.L > 0 ? rows * a.cut.heads : 0, reinterpret_cast<T*>(held + (threadIdx.x >> 6) * kWave), cs,
       [&](int n) {
         const int r = a.cut.by_heads.of(n), h = h0 + min(n - r * a.cut.heads, heads - 1);
-        const Row w = row_of(b0, l0, r, a.per);
-        const int b = w.b, i = w.l;
         if (dead && h >= a.Hq) return static_cast<const T*>(nullptr);
-        return h < a.Hq           ? static_cast<const T*>(a.q) + b * a.qs[0] + i * a.qs[1] + h * a.qs[2]
-               : h < a.Hq + a.Hkv ? static_cast<const T*>(a.k) + b * a.ks[0] + i * a.ks[1] + (h - a.Hq) * a.ks[2]
-                                  : static_cast<const T*>(a.v) + b * a.vs[0] + i * a.vs[1] + (h - a.Hq - a.Hkv) * a.vs[2];
+        const bool of_q = h < a.Hq, of_k = h < a.Hq + a.Hkv;
+        const T* const p = pick(of_q, q, pick(of_k, k, v));
+        const int hh = h - pick(of_q, 0, pick(of_k, a.Hq, a.Hq + a.Hkv));
+        const int64_t s0 = pick(of_q, qs0, pick(of_k, ks0, vs0)), s1 = pick(of_q, qs1, pick(of_k, ks1, vs1)),
+                      s2 = pick(of_q, qs2, pick(of_k, ks2, vs2));
+        if (flat) return p + apart(r, static_cast<int>(s1), hh, static_cast<int>(s2));
+        const Row w = row_of(b0, l0, r, a.per);
+        return p + (w.b - b0) * s0 + (w.l - l0) * s1 + hh * s2;
       },
       [&](int n) -> T* {
         const int r = a.cut.by_heads.of(n), i = n - r * a.cut.heads, h = h0 + i;
         if (i >= heads) return nullptr;
-        if (h < a.Hq) return static_cast<T*>(a.qo) + (static_cast<int64_t>(row0 + r) * a.Hq + h) * a.D;
-        const int page = pages[r], place = places[r];
-        if (page < 0) return nullptr;
-        return h < a.Hq + a.Hkv ? static_cast<T*>(a.kp) + page * a.kps[0] + place * a.kps[1] + (h - a.Hq) * a.kps[2]
-                                : static_cast<T*>(a.vp) + page * a.vps[0] + place * a.vps[1] + (h - a.Hq - a.Hkv) * a.vps[2];
+        // (a workgroup has a few thousand heads at most, one row where a row has several groups)
+        if (h < a.Hq) return out + __umul24(__umul24(r, a.Hq) + i, a.D);
+        const bool of_k = h < a.Hq + a.Hkv;
+        const int64_t place = places[of_k ? 0 : 1][r];
+        if (place < 0) return nullptr;
+        T* const to = pick(of_k, kp, vp);
+        const int hh = h - pick(of_k, a.Hq, a.Hq + a.Hkv);
+        const int64_t s2 = pick(of_k, kps2, vps2);
+        return to + place + (a.near ? apart(0, 0, hh, static_cast<int>(s2)) : hh * s2);
       },
       [&](int n) {
         const int r = a.cut.by_heads.of(n);
@@ -92,8 +114,9 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
             place = static_cast<int>(s) - n * a.page_size;
             page = a.table[b * a.ts + n];
           }
-          pages[r] = page >= 0 && page < a.num_pages ? page : -1;
-          places[r] = place;
+          const bool ok = page >= 0 && page < a.num_pages;
+          places[0][r] = ok ? page * a.kps[0] + place * a.kps[1] : -1;
+          places[1][r] = ok ? page * a.vps[0] + place * a.vps[1] : -1;
         }
         if (a.L > 0)
           form_turns(a.t, a.cut.log_pairs, rows, 1.f, cs, [&](int r, int axis) {
@@ -195,6 +218,8 @@ extern "C" int dcn_paged_append(const dcn_append_desc* d, const void* q, const v
   const int pv = pairs_at_once(a.t, d->sections, w, es);
   a.cut = cut_of(w, pv, es, a.t.pairs, d->head_dim, a.rows, a.Hq + 2 * a.Hkv);
   a.cut.rows = std::min(a.cut.rows, kRows);
+  a.near = near_by(a.cut.rows, a.qs[1], a.Hq, a.qs[2]) && near_by(a.cut.rows, a.ks[1], a.Hkv, a.ks[2]) &&
+           near_by(a.cut.rows, a.vs[1], a.Hkv, a.vs[2]) && near_by(1, 0, a.Hkv, a.kps[2]) && near_by(1, 0, a.Hkv, a.vps[2]);
   void* args[] = {&a};
   return launch(kernel_of(bf16, w, pv, d->layout == DCN_ROTARY_ADJACENT),
                 (static_cast<int64_t>(a.rows) + a.cut.rows - 1) / a.cut.rows * a.cut.groups, args,

@@ -151,6 +151,13 @@ __device__ __forceinline__ Row row_of(int b0, int l0, int r, int L) {
   return w;
 }
 
+// Elements from a workgroup's first row and head to another of its own: in products of 24 bits, which cost a quarter of
+// 32-bit ones (near_by says that they are enough; with 64-bit strides in every lane the addresses were most of the
+// instructions: 83 us where 73 now for 8 x 4200 ragged rows of an append, 20 where 16 for 4 x 4200 rows of heads of 37).
+__device__ __forceinline__ uint32_t apart(int r, int s1, int h, int s2) {
+  return __umul24(static_cast<uint32_t>(r), static_cast<uint32_t>(s1)) + __umul24(static_cast<uint32_t>(h), static_cast<uint32_t>(s2));
+}
+
 // Cosines and sines of the rows' angles into the LDS, [row][pair], by all 256 threads: a thread keeps its pair and
 // takes rows in turn, four positions on their way at a time.  position(row): of the pair's axis.
 template <typename P>
@@ -362,6 +369,12 @@ inline Cut cut_of(int wv, int pv, int es, int pairs, int64_t head_dim, int64_t r
   c.by_chunks = div_by(c.chunks);
   while (c.log_pairs < 8 && (1 << c.log_pairs) < pairs) ++c.log_pairs;
   return c;
+}
+
+// Whether `apart` serves so many rows and heads with these strides.
+inline bool near_by(int64_t rows, int64_t s1, int64_t heads, int64_t s2) {
+  constexpr int64_t kMost = int64_t{1} << 24;
+  return rows < kMost && s1 < kMost && heads < kMost && s2 < kMost && rows * s1 + heads * s2 < (int64_t{1} << 31);
 }
 
 // Launches n workgroups of 256 threads; a dispatch counts its threads in 32 bits, so beyond 2^23 of them

@@ -16,8 +16,8 @@
 // rotary_grad_kernel: a workgroup has all heads of its rows, a thread takes chunks of pairs straight from memory and
 // leaves each one's sum for each axis in the LDS, where one thread for each row and axis adds them in order.
 //
-// Memory bounds it: 8 x 16800 rows of 8 heads of 32, bf16, take 28.8 us for 137.8 MB, 4.8 TB/s of the 4.99 that a large
-// copy reaches, and 2 x 8400 rows of 8 heads of 64 10.3 us for 34.5 MB, a round and a start of the chip.  Chunks of
+// Memory bounds it: 8 x 16800 rows of 8 heads of 32, bf16, take 29.1 us for 137.8 MB, 4.7 TB/s of the 4.99 that a large
+// copy reaches, and 2 x 8400 rows of 8 heads of 64 9.9 us for 34.5 MB, a round and a start of the chip.  Chunks of
 // pairs straight from memory, each lane its two vectors, took 33.0 us for the first, and 64 where a head of 32 turns
 // one pair (26 now): their vectors are as wide as the layout's runs allow, those of whole heads always 16 bytes.
 // The positions' gradient of 2 x 900 rows takes 6.4 us, one round of 225 workgroups, each the chain of its loads,
@@ -48,6 +48,7 @@ struct Args {
   int rows;                // B * L
   int L, H, D;
   float sign;              // 1, or -1 to turn back
+  bool near;               // near_by of x's strides
   // rotary_grad_kernel: chunks of a head, `turned` of them of pairs and the others copied
   int turned;
   Div by_row;              // chunks of a row
@@ -61,6 +62,9 @@ __global__ __launch_bounds__(256) void rotary_kernel(Args a) {
   const int row0 = static_cast<int>(block) * a.cut.rows, rows = min(a.cut.rows, a.rows - row0);
   const int h0 = static_cast<int>(at - block * a.cut.groups) * a.cut.heads, heads = min(a.cut.heads, a.H - h0);
   const int b0 = static_cast<int>(static_cast<uint32_t>(row0) / static_cast<uint32_t>(a.L)), l0 = row0 - b0 * a.L;
+  const bool flat = a.near && l0 + rows <= a.L;        // (rows of one batch element)
+  const T* const x = static_cast<const T*>(a.x) + b0 * a.xs[0] + l0 * a.xs[1] + h0 * a.xs[2];
+  T* const out = static_cast<T*>(a.out) + (static_cast<int64_t>(row0) * a.H + h0) * a.D;
   // head i of the workgroup: its row and place there (the last group of heads may be smaller than the others)
   const auto row = [&](int i) { return a.cut.by_heads.of(i); };
   const auto head = [&](int i, int r) { return i - r * a.cut.heads; };
@@ -68,12 +72,14 @@ __global__ __launch_bounds__(256) void rotary_kernel(Args a) {
       a.t, a.cut, rows * a.cut.heads, reinterpret_cast<T*>(held + (threadIdx.x >> 6) * kWave), cs,
       [&](int i) {
         const int r = row(i), h = min(head(i, r), heads - 1);
+        if (flat) return x + apart(r, static_cast<int>(a.xs[1]), h, static_cast<int>(a.xs[2]));
         const Row w = row_of(b0, l0, r, a.L);
         return static_cast<const T*>(a.x) + w.b * a.xs[0] + w.l * a.xs[1] + (h0 + h) * a.xs[2];
       },
       [&](int i) {
         const int r = row(i), h = head(i, r);
-        return h < heads ? static_cast<T*>(a.out) + (static_cast<int64_t>(row0 + r) * a.H + h0 + h) * a.D : nullptr;
+        // (a workgroup has a few thousand heads at most, one row where a row has several groups)
+        return h < heads ? out + __umul24(__umul24(r, a.H) + h, a.D) : nullptr;
       },
       row,
       [&] {
@@ -278,6 +284,7 @@ int run(const dcn_rotary_desc* d, Args* a, const void* positions, const float* f
     fn = grad_kernel(bf16, pv, adjacent);
   } else {
     a->cut = cut_of(w, pv, es, a->t.pairs, d->head_dim, a->rows, d->heads);
+    a->near = near_by(a->cut.rows, a->xs[1], a->cut.heads, a->xs[2]);
     fn = turning_kernel(bf16, w, pv, adjacent);
   }
   void* args[] = {a};

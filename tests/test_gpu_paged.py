@@ -501,3 +501,31 @@ def test_refusals():
             f(k, v, kp, vp, table, starts, **bad)
     with pytest.raises(TypeError):
         f(k, v.bfloat16(), kp, vp, table, starts)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_append_of_heads_far_apart(dtype):
+    """Strides of heads at and beyond 2^24 elements, of the tokens and of the pages: the same bits as dense."""
+    g = torch.Generator().manual_seed(4)
+    t = DT[dtype]
+    q, k, v = (torch.randn((2, 5, n, 16), generator=g).to(t).cuda() for n in (4, 2, 2))
+    freq = torch.rand(8, generator=g).cuda()
+    table = torch.tensor([[2, 0], [3, 1]], dtype=torch.int32, device="cuda")
+    starts = torch.tensor([1, 3], dtype=torch.int32, device="cuda")
+
+    def run(q, k, v, kp, vp):
+        return dcn.paged_append(k, v, kp, vp, table, starts, query=q, frequencies=freq, sections=(8,))
+
+    kp, vp = (torch.zeros((4, 4, 2, 16), dtype=t, device="cuda") for _ in range(2))
+    want = run(q, k, v, kp, vp)
+    for step in ((1 << 24) - 1, 1 << 24):
+        def far(x):
+            a, b, n, d = x.shape
+            y = torch.empty(n * step + a * b * d, dtype=t, device="cuda").as_strided(x.shape, (b * d, d, step, 1))
+            return y.copy_(x)
+
+        for tokens, pages in ((True, False), (False, True), (True, True)):
+            args = [far(x) if tokens else x for x in (q, k, v)]
+            fk, fv = (far(torch.zeros_like(kp)) if pages else torch.zeros_like(kp) for _ in range(2))
+            got = run(*args, fk, fv)
+            assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(fk, kp) and torch.equal(fv, vp)

@@ -234,3 +234,23 @@ def test_refusals():
         dcn.rotary_positions_backward(go[:, ::2], pos[:, ::2], freq, sections)
     with pytest.raises(ValueError):
         dcn.rotary_positions_backward(go, pos, freq, sections, input=x[:1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_heads_and_rows_far_apart(dtype):
+    """Strides at and beyond 2^24 elements, at which addresses are formed in other products: the same bits as dense."""
+    g = torch.Generator().manual_seed(3)
+    t = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    x = torch.randn((2, 5, 3, 24), generator=g).to(t).cuda()
+    freq = torch.rand(12, generator=g).cuda()
+    at = torch.arange(10, dtype=torch.int32, device="cuda").view(2, 5, 1)
+    want = dcn.rotary_positions(x, at, freq, (12,))
+    for step in ((1 << 24) - 1, 1 << 24, (1 << 24) + 8):
+        flat = torch.empty(3 * step + 2 * 5 * 24, dtype=t, device="cuda")
+        far = flat.as_strided((2, 5, 3, 24), (5 * 24, 24, step, 1))
+        far.copy_(x)
+        assert torch.equal(dcn.rotary_positions(far, at, freq, (12,)), want), step
+        flat = torch.empty(5 * step + 2 * 3 * 24, dtype=t, device="cuda")
+        far = flat.as_strided((2, 5, 3, 24), (3 * 24, step, 24, 1))
+        far.copy_(x)
+        assert torch.equal(dcn.rotary_positions(far, at, freq, (12,)), want), step
