@@ -957,6 +957,11 @@ def _bytes(name: str, desc) -> int:
     return n.value
 
 
+def _copied(desc):
+    """A descriptor for the caller, who may alter it: the plan's own stays what its checks saw."""
+    return type(desc).from_buffer_copy(desc)
+
+
 def _element_type(dtype) -> int:
     known = _DTYPES.get(dtype)
     if known is None:
@@ -1020,7 +1025,7 @@ def _rotary_plan(x, positions, frequencies, sections, layout):
 
 def rotary_desc(input, positions, frequencies, sections, layout="halves") -> RotaryDesc:
     """Descriptor of a rotation, for the raw entry points."""
-    return _rotary_plan(_look(input), _look(positions), _look(frequencies), tuple(map(int, sections)), layout)[0]
+    return _copied(_rotary_plan(_look(input), _look(positions), _look(frequencies), tuple(map(int, sections)), layout)[0])
 
 
 def dcn_rotary(desc: RotaryDesc, x, positions, frequencies, out, stream=None) -> None:
@@ -1127,8 +1132,8 @@ def _residual_key(x, branch, gate, scale, branch_norm, branch_weight, branch_bia
 def residual_desc(input, branch, gate=None, scale=None, branch_norm="none", branch_weight=None, branch_bias=None,
                   next_norm="layer", next_weight=None, next_bias=None, eps=1e-5) -> ResidualDesc:
     """Descriptor of a join of two blocks, for the raw entry points."""
-    return _residual_key(input, branch, gate, scale, branch_norm, branch_weight, branch_bias, next_norm, next_weight,
-                         next_bias, eps)[0]
+    return _copied(_residual_key(input, branch, gate, scale, branch_norm, branch_weight, branch_bias, next_norm,
+                                 next_weight, next_bias, eps)[0])
 
 
 def dcn_residual_norm(desc: ResidualDesc, x, branch, gate, scale, branch_weight, branch_bias, next_weight, next_bias,
@@ -1264,8 +1269,8 @@ def _append_plan(key, value, key_pages, value_pages, table, starts, counts, quer
 def append_desc(key, value, key_pages, value_pages, page_table, starts, counts=None, query=None, positions=None,
                 frequencies=None, sections=(), layout="halves") -> AppendDesc:
     """Descriptor of an append to a paged cache, for the raw entry points."""
-    return _append_plan(*map(_look, (key, value, key_pages, value_pages, page_table, starts, counts, query, positions,
-                                     frequencies)), tuple(map(int, sections)), layout)[0]
+    return _copied(_append_plan(*map(_look, (key, value, key_pages, value_pages, page_table, starts, counts, query,
+                                             positions, frequencies)), tuple(map(int, sections)), layout)[0])
 
 
 def dcn_paged_append(desc: AppendDesc, q, k, v, positions, frequencies, page_table, starts, counts, q_out, key_pages,
@@ -1316,8 +1321,8 @@ def _paged_plan(query, key_pages, value_pages, table, lengths, scale):
 
 def paged_desc(query, key_pages, value_pages, page_table, lengths, scale=None) -> PagedDesc:
     """Descriptor of an attention to a paged cache, for the raw entry points."""
-    return _paged_plan(_look(query), _look(key_pages), _look(value_pages), _look(page_table), _look(lengths),
-                       None if scale is None else float(scale))[0]
+    return _copied(_paged_plan(_look(query), _look(key_pages), _look(value_pages), _look(page_table), _look(lengths),
+                               None if scale is None else float(scale))[0])
 
 
 def dcn_paged_attention_workspace_bytes(desc: PagedDesc) -> int:
