@@ -26,9 +26,8 @@
 // blocks for each wave one after the other; in fp32 13 sequences to 2777, 6 heads of 40 on 3, 8.4 us (and the join 4.0)
 // for 5.5 MB: the division, a look-up and one or two blocks for each wave.
 //
-// Arithmetic: as dcn_attention.hip, but for bf16 the weights enter the second product as two operands, 2^-15
-// of the weight in all: the matrix units wait for memory here, and the output is then as near the exact one
-// as its own rounding.
+// Arithmetic: as dcn_attention.hip, but for bf16 the weights enter the second product as three operands, which hold all
+// of their 24 bits: the matrix units wait for memory here, and the output is then that of fp32 weights, rounded once.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -400,15 +399,24 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
         }
       if constexpr (sizeof(T) == 2) {
         typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-        // A weight as two operands: its upper 16 bits, lowered a little first so that something is left, and the
-        // rest, rounded (2^-15 of the weight).  Both are positive, for a rest of 0 or below would make an infinite
-        // value's product NaN.
-        Frag<T> pf, pr;
+        // A weight as three operands, which together are the weight: each is the upper 16 bits of what the ones before
+        // leave, less one in the last of its 32 bits, so that something of it is always left.  All of them are positive,
+        // for a rest of 0 or below would make an infinite value's product NaN.
+        Frag<T> pf[3];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t h0 = __float_as_uint(p[2 * j] * 0.9921875f), h1 = __float_as_uint(p[2 * j + 1] * 0.9921875f);
-          pf.w[j] = __builtin_amdgcn_perm(h1, h0, 0x07060302);
-          pr.w[j] = pack_bf16(p[2 * j] - __uint_as_float(h0 & 0xffff0000u), p[2 * j + 1] - __uint_as_float(h1 & 0xffff0000u));
+          float r0 = p[2 * j], r1 = p[2 * j + 1];
+#pragma unroll
+          for (int n = 0; n < 3; ++n) {
+            uint32_t h0 = __float_as_uint(r0), h1 = __float_as_uint(r1);
+            if (n < 2) {                       // (the last is what is left, 8 bits at most)
+              h0 = __builtin_elementwise_sub_sat(h0, 1u);
+              h1 = __builtin_elementwise_sub_sat(h1, 1u);
+              r0 -= __uint_as_float(h0 & 0xffff0000u);
+              r1 -= __uint_as_float(h1 & 0xffff0000u);
+            }
+            pf[n].w[j] = __builtin_amdgcn_perm(h1, h0, 0x07060302);
+          }
         }
 #pragma unroll
         for (int i = 0; i < DT; ++i) {
@@ -417,8 +425,8 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
           for (int t = 0; t < 2; ++t)
             vt.s[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                 (lds_s16x4*)(lds + Tile<T, DP>::at(16 * t + 4 * quad + (col >> 2), 16 * i + 4 * (col & 3))));
-          o[i] = mma16(vt, pf, o[i]);
-          o[i] = mma16(vt, pr, o[i]);
+#pragma unroll
+          for (int n = 0; n < 3; ++n) o[i] = mma16(vt, pf[n], o[i]);
         }
       } else {
 #pragma unroll

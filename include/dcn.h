@@ -528,8 +528,8 @@ int dcn_paged_append(const dcn_append_desc* desc, const void* q, const void* k, 
  * page of the cache are left out; a sequence with no position left gets zeros and lse -infinity.  What the
  * cache holds behind a sequence's length, infinities and NaN included, does not matter.  Long sequences are
  * split over workgroups by the lengths on the device, and the parts joined in order: equal calls give equal
- * bits.  Arithmetic as for dcn_cross_attention, but for bf16 a weight enters the second product as two bf16
- * operands (2^-15 of it is lost).  The workspace (256-byte aligned, 0 bytes for short tables) holds the parts; its
+ * bits.  Arithmetic as for dcn_cross_attention, but for bf16 a weight enters the second product with all of its fp32
+ * bits (as three bf16 operands).  The workspace (256-byte aligned, 0 bytes for short tables) holds the parts; its
  * size goes by the descriptor alone, not by the lengths.  Heads of 16 bytes and more are read 16 bytes at a time
  * wherever they start.
  * DCN_E_ARG, DCN_E_UNSUPPORTED (head_dim > 128, sizes as for dcn_paged_append), DCN_E_WORKSPACE, DCN_E_HIP
