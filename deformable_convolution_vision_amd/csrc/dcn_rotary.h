@@ -49,22 +49,24 @@ struct alignas(sizeof(T) * N) Vec {
 };
 
 // cos and sin of pos * f.  The angle is formed in quarter turns in 64 bits and reduced there to the
-// nearest quarter, |x| <= pi / 4; the remainder's sine and cosine are their Taylor polynomials of degree
-// 9 and 10 (the first terms left out are 1.8e-9 and 1.2e-10 there, below 2^-24 of the value).
+// nearest quarter, |x| <= pi / 4; the remainder's sine and cosine are their Taylor polynomials of degree 11 and 12 (the
+// first terms left out are below 2^-33), with the upper terms in 32 bits (their sum is below 2^-7 of a term that is
+// there in 64) and the others in 64, so that both are off by their one rounding to fp32 and 2^-30.
 __device__ __forceinline__ void cos_sin(double pos, float f, float& c, float& s) {
   const double q = pos * (static_cast<double>(f) * 0.636619772367581343);
   const double n = __builtin_rint(q);
-  const float x = static_cast<float>((q - n) * 1.57079632679489662), y = x * x;
-  const int k = static_cast<int>(4.0 * __builtin_amdgcn_fract(0.25 * n));
-  float ps = fmaf(y, 2.75573192e-6f, -1.98412698e-4f);
-  ps = fmaf(ps, y, 8.33333333e-3f);
-  ps = fmaf(ps, y, -0.166666667f);
-  ps = fmaf(ps * y, x, x);
-  float pc = fmaf(y, -2.75573192e-7f, 2.48015873e-5f);
-  pc = fmaf(pc, y, -1.38888889e-3f);
-  pc = fmaf(pc, y, 4.16666667e-2f);
-  pc = fmaf(pc, y, -0.5f);
-  pc = fmaf(pc, y, 1.f);
+  const double x = (q - n) * 1.57079632679489662, y = x * x;
+  // n's last two bits stand at the end of this sum's (from 2^51 quarter turns on they are any, as the angle is)
+  const int k = __double2loint(n + 6755399441055744.);
+  const float z = static_cast<float>(y);
+  float us = fmaf(z, -2.50521084e-8f, 2.75573192e-6f);
+  us = fmaf(us, z, -1.98412698e-4f);
+  us = fmaf(us, z, 8.33333333e-3f);
+  float uc = fmaf(z, 2.08767570e-9f, -2.75573192e-7f);
+  uc = fmaf(uc, z, 2.48015873e-5f);
+  uc = fmaf(uc, z, -1.38888889e-3f);
+  const float ps = static_cast<float>(fma(x, y * (static_cast<double>(us * z) - 1. / 6.), x));
+  const float pc = static_cast<float>(fma(fma(static_cast<double>(uc * z) + 1. / 24., y, -0.5), y, 1.));
   const float a = (k & 1) != 0 ? ps : pc, b = (k & 1) != 0 ? pc : ps;
   c = ((k + 1) & 2) != 0 ? -a : a;
   s = (k & 2) != 0 ? -b : b;

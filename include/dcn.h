@@ -405,8 +405,8 @@ int dcn_group_norm_backward(const dcn_norm_desc* desc, const void* x, const void
  *    [B][L][axes] of position_type, axes adjacent, strides of batch and position the descriptor's (0
  *    repeats); frequencies [pairs] float32, radians a unit of position.
  *  - Arithmetic: angles and their reduction in 64 bits, so that far positions keep their digits (an angle
- *    is off by 2^-51 of itself, 5e-7 at 2^30); cosines and sines are within 2^-23, products and sums in
- *    fp32, out rounded once.
+ *    is off by 2^-51 of itself, 5e-7 at 2^30); cosines and sines are rounded to fp32 once, and off by 2^-30
+ *    besides; products and sums in fp32, out rounded once.
  *  - Memory is read and written 16 bytes, 4 or an element at a time, the widest that divides a head,
  *    wherever it starts.
  * DCN_E_ARG: an invalid descriptor (a negative size or stride, no head, axes outside 1 .. 4, a section
