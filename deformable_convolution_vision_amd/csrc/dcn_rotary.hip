@@ -118,92 +118,90 @@ __global__ __launch_bounds__(256) void rotary_grad_kernel(Args a) {
   float sum = 0.f;
   // the heads in groups, one after the other
   for (int h0 = 0; h0 < a.H; h0 += a.cut.heads) {
-    for (int u0 = 0; u0 < units; u0 += kUnits * 256) {
-      V v1[kUnits], v2[kUnits], w1[kUnits], w2[kUnits];
-      // unit k of this thread: its row of the workgroup, its head and chunk; false: none
-      struct Unit {
-        int r, h, chunk;
-      };
-      const auto unit = [&](int k, Unit& n) {
-        const int u = u0 + k * 256 + tid;
-        n.r = a.by_row.of(u);
-        const int in_row = u - n.r * per;
-        n.h = a.cut.by_chunks.of(in_row);
-        n.chunk = in_row - n.h * a.cut.chunks;
-        n.h += h0;
-        return u < units && n.h < a.H;
-      };
-      const auto place = [&](int chunk) {
-        if (chunk < a.turned) return place_of<PV>(a.t, chunk * PV);
-        const int e = 2 * a.t.pairs + (chunk - a.turned) * 2 * PV;
-        return Place{e, e + PV};
-      };
+    V v1[kUnits], v2[kUnits], w1[kUnits], w2[kUnits];
+    // unit k of this thread: its row of the workgroup, its head and chunk; false: none
+    struct Unit {
+      int r, h, chunk;
+    };
+    const auto unit = [&](int k, Unit& n) {
+      const int u = k * 256 + tid;
+      n.r = a.by_row.of(u);
+      const int in_row = u - n.r * per;
+      n.h = a.cut.by_chunks.of(in_row);
+      n.chunk = in_row - n.h * a.cut.chunks;
+      n.h += h0;
+      return u < units && n.h < a.H;
+    };
+    const auto place = [&](int chunk) {
+      if (chunk < a.turned) return place_of<PV>(a.t, chunk * PV);
+      const int e = 2 * a.t.pairs + (chunk - a.turned) * 2 * PV;
+      return Place{e, e + PV};
+    };
 #pragma unroll
-      for (int k = 0; k < kUnits; ++k) {
-        Unit n;
-        if (!unit(k, n)) continue;
-        const Place p = place(n.chunk);
-        const Row w = row_of(b0, l0, n.r, a.L);
-        const T* x = static_cast<const T*>(a.x) + w.b * a.xs[0] + w.l * a.xs[1] + n.h * a.xs[2];
-        v1[k] = in_memory<T, PV>(x + p.e1);
-        if (p.e2 < a.D) v2[k] = in_memory<T, PV>(x + p.e2);
-        if (n.chunk < a.turned) {
-          const T* x0 = static_cast<const T*>(a.x0) + w.b * a.x0s[0] + w.l * a.x0s[1] + n.h * a.x0s[2];
-          w1[k] = in_memory<T, PV>(x0 + p.e1);
-          w2[k] = in_memory<T, PV>(x0 + p.e2);
-        }
+    for (int k = 0; k < kUnits; ++k) {
+      Unit n;
+      if (!unit(k, n)) continue;
+      const Place p = place(n.chunk);
+      const Row w = row_of(b0, l0, n.r, a.L);
+      const T* x = static_cast<const T*>(a.x) + w.b * a.xs[0] + w.l * a.xs[1] + n.h * a.xs[2];
+      v1[k] = in_memory<T, PV>(x + p.e1);
+      if (p.e2 < a.D) v2[k] = in_memory<T, PV>(x + p.e2);
+      if (n.chunk < a.turned) {
+        const T* x0 = static_cast<const T*>(a.x0) + w.b * a.x0s[0] + w.l * a.x0s[1] + n.h * a.x0s[2];
+        w1[k] = in_memory<T, PV>(x0 + p.e1);
+        w2[k] = in_memory<T, PV>(x0 + p.e2);
       }
-      if (h0 == 0 && u0 == 0) {
-        form_turns(a.t, a.cut.log_pairs, rows, a.sign, cs, [&](int r, int axis) {
-          const Row w = row_of(b0, l0, r, a.L);
-          return position_of(a.t, w.b, w.l, axis);
-        });
-        __syncthreads();
-      }
-#pragma unroll
-      for (int k = 0; k < kUnits; ++k) {
-        Unit n;
-        const bool live = unit(k, n);
-        float moved[4] = {0.f, 0.f, 0.f, 0.f};
-        if (live) {
-          const Place p = place(n.chunk);
-          if (n.chunk < a.turned) {
-            float c[PV], s[PV], x1[PV], x2[PV], y1[PV], y2[PV];
-            const float2* turns = cs + n.r * a.t.pairs + n.chunk * PV;
-#pragma unroll
-            for (int j = 0; j < PV; ++j) {
-              c[j] = turns[j].x;
-              s[j] = turns[j].y;
-            }
-            pairs_of<T, PV, ADJ>(v1[k], v2[k], x1, x2);
-            turn<PV>(c, s, x1, x2, y1, y2);
-            pairs_of<T, PV, ADJ>(w1[k], w2[k], x1, x2);
-#pragma unroll
-            for (int j = 0; j < PV; ++j) {
-              const int pair = n.chunk * PV + j, axis = axis_of(a.t, pair);
-              const float m = a.t.freq[pair] * (y2[j] * x1[j] - y1[j] * x2[j]);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) moved[i] += axis == i ? m : 0.f;
-            }
-            vectors_of<T, PV, ADJ>(y1, y2, v1[k], v2[k]);
-          }
-          if (a.out != nullptr) {
-            T* y = static_cast<T*>(a.out) + (static_cast<int64_t>(row0 + n.r) * a.H + n.h) * a.D;
-            to_memory<T, PV>(y + p.e1, v1[k]);
-            if (p.e2 < a.D) to_memory<T, PV>(y + p.e2, v2[k]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i < a.t.axes) red[i * kUnits * 256 + k * 256 + tid] = moved[i];
-      }
-      // thread i adds up row i / axes, axis i % axes: the units of this turn that are the row's
-      __syncthreads();
-      const int r = tid / a.t.axes, n = tid - r * a.t.axes;
-      if (r < rows)
-        for (int u = max(r * per, u0); u < min((r + 1) * per, u0 + kUnits * 256); ++u) sum += red[n * kUnits * 256 + u - u0];
+    }
+    if (h0 == 0) {
+      form_turns(a.t, a.cut.log_pairs, rows, a.sign, cs, [&](int r, int axis) {
+        const Row w = row_of(b0, l0, r, a.L);
+        return position_of(a.t, w.b, w.l, axis);
+      });
       __syncthreads();
     }
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      Unit n;
+      const bool live = unit(k, n);
+      float moved[4] = {0.f, 0.f, 0.f, 0.f};
+      if (live) {
+        const Place p = place(n.chunk);
+        if (n.chunk < a.turned) {
+          float c[PV], s[PV], x1[PV], x2[PV], y1[PV], y2[PV];
+          const float2* turns = cs + n.r * a.t.pairs + n.chunk * PV;
+#pragma unroll
+          for (int j = 0; j < PV; ++j) {
+            c[j] = turns[j].x;
+            s[j] = turns[j].y;
+          }
+          pairs_of<T, PV, ADJ>(v1[k], v2[k], x1, x2);
+          turn<PV>(c, s, x1, x2, y1, y2);
+          pairs_of<T, PV, ADJ>(w1[k], w2[k], x1, x2);
+#pragma unroll
+          for (int j = 0; j < PV; ++j) {
+            const int pair = n.chunk * PV + j, axis = axis_of(a.t, pair);
+            const float m = a.t.freq[pair] * (y2[j] * x1[j] - y1[j] * x2[j]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) moved[i] += axis == i ? m : 0.f;
+          }
+          vectors_of<T, PV, ADJ>(y1, y2, v1[k], v2[k]);
+        }
+        if (a.out != nullptr) {
+          T* y = static_cast<T*>(a.out) + (static_cast<int64_t>(row0 + n.r) * a.H + n.h) * a.D;
+          to_memory<T, PV>(y + p.e1, v1[k]);
+          if (p.e2 < a.D) to_memory<T, PV>(y + p.e2, v2[k]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < a.t.axes) red[i * kUnits * 256 + k * 256 + tid] = moved[i];
+    }
+    // thread i adds up row i / axes, axis i % axes
+    __syncthreads();
+    const int r = tid / a.t.axes, n = tid - r * a.t.axes;
+    if (r < rows)
+      for (int u = r * per; u < (r + 1) * per; ++u) sum += red[n * kUnits * 256 + u];
+    __syncthreads();
   }
   if (tid < rows * a.t.axes) a.gp[static_cast<int64_t>(row0) * a.t.axes + tid] = sum;
 }
@@ -234,7 +232,8 @@ const void* grad_kernel(bool bf16, int pv, bool adjacent) {
   return pv == 4 ? grad_kernel<float, 4>(adjacent) : grad_kernel<float, 1>(adjacent);
 }
 
-// Rows of rotary_grad_kernel: as many as give each thread its chunks at a time, fewer where that leaves fewer than four
+// Rows of rotary_grad_kernel: as many as give each thread its chunks at a time (rows, heads of a group and chunks
+// multiply to 256 units_of at most: a head has no more chunks than that), fewer where that leaves fewer than four
 // workgroups a CU, down to a chunk for each thread.
 void grad_cut(Args* a, int pv, int es) {
   Cut& c = a->cut;
