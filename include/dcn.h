@@ -501,8 +501,8 @@ int dcn_residual_norm_backward(const dcn_residual_desc* desc, const void* x, con
  * (it may not be starts or counts).  A position outside the table, or whose table entry is no page of the
  * cache, is not written; other rows of the cache are left as they are.  Two positions that name one row of
  * the cache leave either's elements there.  Arithmetic and reads as for dcn_rotary; values are copied.
- * DCN_E_ARG, DCN_E_UNSUPPORTED (also max_pages * page_size beyond 2^31 - 1, num_pages beyond it), DCN_E_HIP
- * as for dcn_rotary.  batch 0: nothing is launched. */
+ * DCN_E_ARG, DCN_E_UNSUPPORTED (also max_pages * page_size beyond 2^31 - 1, num_pages beyond it; the heads of queries,
+ * keys and values count together), DCN_E_HIP as for dcn_rotary.  batch 0: nothing is launched. */
 typedef struct dcn_append_desc {
   int64_t batch, length;
   int64_t query_heads, key_heads, head_dim;   /* query_heads 0: no queries */
@@ -532,8 +532,10 @@ int dcn_paged_append(const dcn_append_desc* desc, const void* q, const void* k, 
  * bits (as three bf16 operands).  The workspace (256-byte aligned, 0 bytes for short tables) holds the parts; its
  * size goes by the descriptor alone, not by the lengths.  Heads of 16 bytes and more are read 16 bytes at a time
  * wherever they start.
- * DCN_E_ARG, DCN_E_UNSUPPORTED (head_dim > 128, sizes as for dcn_paged_append), DCN_E_WORKSPACE, DCN_E_HIP
- * as for dcn_cross_attention.  batch 0: nothing is launched. */
+ * DCN_E_UNSUPPORTED: another dtype, head_dim above 128 (a cache of wider heads can be appended to, but not attended
+ * to), batch * query_heads from 2^27 on, num_pages from 2^31 on, or max_pages * page_size above 2^31 - 65537 (a little
+ * less than for dcn_paged_append: tables are looked up ahead of the last position).  DCN_E_ARG, DCN_E_WORKSPACE,
+ * DCN_E_HIP as for dcn_cross_attention.  batch 0: nothing is launched. */
 typedef struct dcn_paged_desc {
   int64_t batch, query_heads, key_heads, head_dim;
   int64_t num_pages, page_size, max_pages;
