@@ -119,12 +119,15 @@ __global__ __launch_bounds__(256) void rotary_grad_kernel(Args a) {
   // the heads in groups, one after the other
   for (int h0 = 0; h0 < a.H; h0 += a.cut.heads) {
     V v1[kUnits], v2[kUnits], w1[kUnits], w2[kUnits];
+    // Taken for unknown in every turn: places that were kept from one group of heads to the next cost 150 registers.
+    int first = tid;
+    asm volatile("" : "+v"(first));
     // unit k of this thread: its row of the workgroup, its head and chunk; false: none
     struct Unit {
       int r, h, chunk;
     };
     const auto unit = [&](int k, Unit& n) {
-      const int u = k * 256 + tid;
+      const int u = k * 256 + first;
       n.r = a.by_row.of(u);
       const int in_row = u - n.r * per;
       n.h = a.cut.by_chunks.of(in_row);
