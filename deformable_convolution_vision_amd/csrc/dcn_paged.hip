@@ -20,10 +20,10 @@
 // chip holds.  A sequence of one part is written as it is; others leave their parts (maximum, sum, undivided output),
 // which paged_join_kernel adds in order.
 //
-// Memory bounds long sequences: eight of 4200 to 16800 positions, 16 heads of 128 on 4, bf16, take 34.8 us for 166 MB,
-// 4.8 TB/s (a large copy 4.99), and the join 4.8; 16 of up to 4200, 8 heads of 127 on 4 in vectors that are moved,
-// 33.6 us in all for 93 MB.  A short one is a chain: 1050 positions, 8 heads of 64, 10.1 us in 8 workgroups, three
-// blocks for each wave one after the other; in fp32 13 sequences to 2777, 6 heads of 40 on 3, 8.4 us (and the join 4.0)
+// Memory bounds long sequences: eight of 4200 to 16800 positions, 16 heads of 128 on 4, bf16, take 35.0 us for 166 MB,
+// 4.7 TB/s (a large copy 4.99), and the join 4.8; 16 of up to 4200, 8 heads of 127 on 4 in vectors that are moved,
+// 33.8 us in all for 93 MB.  A short one is a chain: 1050 positions, 8 heads of 64, 10.2 us in 8 workgroups, three
+// blocks for each wave one after the other; in fp32 13 sequences to 2777, 6 heads of 40 on 3, 8.5 us (and the join 3.9)
 // for 5.5 MB: the division, a look-up and one or two blocks for each wave.
 //
 // Arithmetic: as dcn_attention.hip, but for bf16 the weights enter the second product as three operands, which hold all
@@ -599,10 +599,11 @@ struct PagedPlan {
 };
 // The division into parts.  A sequence has several only where its blocks may be more than kChain for each wave of a
 // wide workgroup: below, the launch that joins them costs more than it saves (one sequence, 8 heads of 64:
-// 1050 positions 10.2 us whole, 12.4 in parts; 2100 15.0 and 12.8).  Few sequences: one round of wide workgroups
-// (16800 positions 14.8 us, of narrow ones 15.5).  Many: kRounds rounds of narrow ones, in which their
-// lengths even out, but of kLeast blocks for each wave at least (32 sequences to 4200, 8 heads of 64, in one round
-// 55 us, 48 in two or three; 64 to 2000, 4 of 128: 47.7 us with parts of one block, 46.2 of three, 56 of twelve).
+// 1050 positions 10.2 us whole, 11.1 in parts; 2100 15.1 and 11.3).  Few sequences: one round of wide workgroups
+// (16800 positions 15.3 us, of narrow ones 15.5; of 16 heads of 128 on 4, 16.2 and 16.5).  Many: kRounds rounds of
+// narrow ones, in which their lengths even out, but of kLeast blocks for each wave at least (32 sequences to 4200, 8
+// heads of 64, in one round 53 us, 47 in two or three; 64 to 2000, 4 of 128: 44.8 us with parts of one block, 41.4 of
+// three, 54 of twelve).
 constexpr int kChain = 3, kRounds = 3, kLeast = 3;
 PagedPlan plan_of(const dcn_paged_desc* d) {
   PagedPlan p{};

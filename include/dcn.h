@@ -447,7 +447,8 @@ int dcn_rotary_backward(const dcn_rotary_desc* desc, const void* grad_out, const
  * DCN_GATE_BATCH [B][C], DCN_GATE_FULL [B][P][C].  scale, weights and biases [C], NULL for 1 and 0; those of
  * a norm that is NONE are not read.  stats [B][P][4] float32, 16-byte aligned, where not NULL: mean and 1 /
  * deviation of the branch's row, then of out's (0 and 1 where there is none), which the backward takes.
- * A row of zeros with eps 0 gives NaN, as the formula does.  Everything is dense
+ * A row of zeros with eps 0 gives NaN, as the formula does.  With one position to a batch element DCN_GATE_FULL is the
+ * same as DCN_GATE_BATCH, and its gradients cost far less (they keep sums for each shared gate).  Everything is dense
  * in desc->dtype; out may be x or branch, next may be branch (out and next differ).  Arithmetic: fp32, the
  * variance about the mean, out and next rounded once.  Rows are read 16 bytes at a time wherever they start.
  * DCN_E_ARG: an invalid descriptor (a negative size, no channel, eps negative or not finite, an unknown
