@@ -23,7 +23,7 @@
 // The positions' gradient of 2 x 900 rows takes 5.6 us, one round of 225 workgroups, each the chain of its loads,
 // angles and sums; of 4 x 16800 rows 34 (104.3 MB, 3.1 TB/s: one thread adds a row's values for an axis while the
 // workgroup waits), and 74 where uneven blocks make every chunk one pair, with 128 values to add (in one chain of
-// additions in place of four side by side 93; 2 x 8400 rows of 16 heads of 128 74, now 58).
+// additions in place of four side by side 93; 2 x 8400 rows of 16 heads of 128 74, now 55).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -186,7 +186,7 @@ __global__ __launch_bounds__(256) void rotary_grad_kernel(Args a) {
             const int pair = n.chunk * PV + j, axis = axis_of(a.t, pair);
             const float m = y2[j] * x1[j] - y1[j] * x2[j], f = a.t.freq[pair];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) moved[i] = fmaf(axis == i ? f : 0.f, m, moved[i]);
+            for (int i = 0; i < 4; ++i) moved[i] = axis == i ? fmaf(f, m, moved[i]) : moved[i];   // (0 m could be NaN)
           }
           vectors_of<T, PV, ADJ>(y1, y2, v1[k], v2[k]);
         }

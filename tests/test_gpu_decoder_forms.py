@@ -129,3 +129,24 @@ def test_pages_named_twice():
     keep = torch.ones(5, 16, dtype=torch.bool, device="cuda")
     keep[1, 1] = False
     assert torch.equal(k[keep], before[keep]) and np.isfinite(f64(k)).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_positions_gradient_of_values_that_are_not_finite(dtype):
+    """What is not finite in an axis's pairs reaches that position's gradient, and no other axis's, row's or head's."""
+    for name in ("map", "four_axes", "width_4"):
+        for layout in rotary.LAYOUTS:
+            x, pos, freq, sections, go = rotary.make(name, dtype)
+            want = dcn.rotary_positions_backward(go, pos, freq, sections, layout, input=x)[1]
+            # the second axis's first pair
+            pairs = rotary.rotary_oracle.pairs_of(sections, layout)
+            axis, first, second = pairs[sections[0]]
+            assert axis == 1
+            for tensor, bad in ((x, float("inf")), (go, float("nan")), (x, float("nan"))):
+                was = tensor[1 if len(x) > 1 else 0, 3, -1, first].clone()
+                tensor[1 if len(x) > 1 else 0, 3, -1, first] = bad
+                gp = dcn.rotary_positions_backward(go, pos, freq, sections, layout, input=x)[1]
+                tensor[1 if len(x) > 1 else 0, 3, -1, first] = was
+                hit = torch.zeros_like(gp, dtype=torch.bool)
+                hit[1 if len(x) > 1 else 0, 3, 1] = True
+                assert torch.equal(gp[~hit], want[~hit]) and not torch.isfinite(gp[hit]).any(), (name, layout, bad)
