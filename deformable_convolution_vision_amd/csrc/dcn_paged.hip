@@ -22,7 +22,7 @@
 //
 // Memory bounds long sequences: eight of 4200 to 16800 positions, 16 heads of 128 on 4, bf16, take 35.0 us for 166 MB,
 // 4.7 TB/s (a large copy 4.99), and the join 4.8; 16 of up to 4200, 8 heads of 127 on 4 in vectors that are moved,
-// 33.8 us in all for 93 MB.  A short one is a chain: 1050 positions, 8 heads of 64, 10.2 us in 8 workgroups, three
+// 33.8 us in all for 93 MB.  A short one is a chain: 1050 positions, 8 heads of 64, 10.3 us in 8 workgroups, three
 // blocks for each wave one after the other; in fp32 13 sequences to 2777, 6 heads of 40 on 3, 8.5 us (and the join 3.9)
 // for 5.5 MB: the division, a look-up and one or two blocks for each wave.
 //
@@ -400,23 +400,25 @@ __global__ __launch_bounds__(64 * W) void paged_kernel(PagedArgs a) {
       if constexpr (sizeof(T) == 2) {
         typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
         // A weight as three operands, which together are the weight: each is the upper 16 bits of what the ones before
-        // leave, less one in the last of its 32 bits, so that something of it is always left.  All of them are positive,
-        // for a rest of 0 or below would make an infinite value's product NaN.
+        // leave.  Where they leave nothing it is bf16's least number, 2^-133, for 0 would make an infinite value's
+        // product NaN (of a weight of 0 all three are 0).
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
         Frag<T> pf[3];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float r0 = p[2 * j], r1 = p[2 * j + 1];
+          u16x2 upper[3];
 #pragma unroll
           for (int n = 0; n < 3; ++n) {
-            uint32_t h0 = __float_as_uint(r0), h1 = __float_as_uint(r1);
-            if (n < 2) {                       // (the last is what is left, 8 bits at most)
-              h0 = __builtin_elementwise_sub_sat(h0, 1u);
-              h1 = __builtin_elementwise_sub_sat(h1, 1u);
-              r0 -= __uint_as_float(h0 & 0xffff0000u);
-              r1 -= __uint_as_float(h1 & 0xffff0000u);
-            }
-            pf[n].w[j] = __builtin_amdgcn_perm(h1, h0, 0x07060302);
+            const uint32_t h0 = __float_as_uint(r0), h1 = __float_as_uint(r1);
+            upper[n] = __builtin_bit_cast(u16x2, __builtin_amdgcn_perm(h1, h0, 0x07060302));
+            r0 -= __uint_as_float(h0 & 0xffff0000u);
+            r1 -= __uint_as_float(h1 & 0xffff0000u);
           }
+          const u16x2 least = __builtin_elementwise_min(upper[0], u16x2{1, 1});
+          pf[0].w[j] = __builtin_bit_cast(uint32_t, upper[0]);
+#pragma unroll
+          for (int n = 1; n < 3; ++n) pf[n].w[j] = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(upper[n], least));
         }
 #pragma unroll
         for (int i = 0; i < DT; ++i) {
@@ -599,7 +601,7 @@ struct PagedPlan {
 };
 // The division into parts.  A sequence has several only where its blocks may be more than kChain for each wave of a
 // wide workgroup: below, the launch that joins them costs more than it saves (one sequence, 8 heads of 64:
-// 1050 positions 10.2 us whole, 11.1 in parts; 2100 15.1 and 11.3).  Few sequences: one round of wide workgroups
+// 1050 positions 10.3 us whole, 11.1 in parts; 2100 15.1 and 11.3).  Few sequences: one round of wide workgroups
 // (16800 positions 15.3 us, of narrow ones 15.5; of 16 heads of 128 on 4, 16.2 and 16.5).  Many: kRounds rounds of
 // narrow ones, in which their lengths even out, but of kLeast blocks for each wave at least (32 sequences to 4200, 8
 // heads of 64, in one round 53 us, 47 in two or three; 64 to 2000, 4 of 128: 44.8 us with parts of one block, 41.4 of

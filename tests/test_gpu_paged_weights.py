@@ -93,3 +93,17 @@ def test_infinite_values_under_any_weight():
     lengths = torch.full((B,), 2, dtype=torch.int32, device="cuda")
     out = dcn.paged_attention(*(a.bfloat16().cuda() for a in (q, k, v)), table, lengths, scale=1.0)
     assert torch.all(out[..., ::2] == float("inf")) and torch.isfinite(out[..., 1::2]).all()
+
+
+def test_infinite_values_under_the_least_weights():
+    """Down to fp32's least normal number, below which a weight may be 0."""
+    g = torch.Generator().manual_seed(8)
+    B, page, d = 260, 4, 32
+    table = tables([1] * B, B, 1, g)
+    q, k, v = torch.zeros(B, 2, d), torch.zeros(B, page, 2, d), torch.ones(B, page, 2, d)
+    q[:, :, 0] = 1
+    k[:, 1, :, 0] = -torch.linspace(85, 124.5, B)[:, None] * float(np.log(2))
+    v[:, 1, :, ::2] = float("inf")
+    lengths = torch.full((B,), 2, dtype=torch.int32, device="cuda")
+    out = dcn.paged_attention(*(a.bfloat16().cuda() for a in (q, k, v)), table, lengths, scale=1.0)
+    assert torch.all(out[..., ::2] == float("inf")) and torch.all(out[..., 1::2] == 1)
