@@ -9,10 +9,10 @@
 // A table entry that is no page of the cache, or a position outside the table, drops the row: the
 // check stands before the address is formed.
 //
-// Memory bounds a prompt: 8 x 4200 rows, ragged, of 16 + 4 + 4 heads of 128, bf16, take 73 us for 340.7 MB, 4.7 TB/s (a
+// Memory bounds a prompt: 8 x 4200 rows, ragged, of 16 + 4 + 4 heads of 128, bf16, take 71 to 73 us for 340.7 MB, 4.7 to 4.8 TB/s (a
 // large copy 4.99).  Whole turns of a workgroup's waves (cut_of) took as many rows without gaps from 108 us to 90, rows
 // without tokens that are not read the ragged ones from 86 to 84, addresses in 24-bit products (apart) these to 73 and
-// those to 82.  One token of eight sequences takes 5.2 us, a chain from its start and table
+// those to 82.  One token of eight sequences takes 5.3 us, a chain from its start and table
 // entry to its address.
 
 #include <hip/hip_runtime.h>

@@ -20,10 +20,10 @@
 // chip holds.  A sequence of one part is written as it is; others leave their parts (maximum, sum, undivided output),
 // which paged_join_kernel adds in order.
 //
-// Memory bounds long sequences: eight of 4200 to 16800 positions, 16 heads of 128 on 4, bf16, take 35.0 us for 166 MB,
-// 4.7 TB/s (a large copy 4.99), and the join 4.8; 16 of up to 4200, 8 heads of 127 on 4 in vectors that are moved,
+// Memory bounds long sequences: eight of 4200 to 16800 positions, 16 heads of 128 on 4, bf16, take 34.8 us for 166 MB,
+// 4.8 TB/s (a large copy 4.99), and the join 4.8; 16 of up to 4200, 8 heads of 127 on 4 in vectors that are moved,
 // 33.8 us in all for 93 MB.  A short one is a chain: 1050 positions, 8 heads of 64, 10.3 us in 8 workgroups, three
-// blocks for each wave one after the other; in fp32 13 sequences to 2777, 6 heads of 40 on 3, 8.5 us (and the join 3.9)
+// blocks for each wave one after the other; in fp32 13 sequences to 2777, 6 heads of 40 on 3, 8.4 us (and the join 3.9)
 // for 5.5 MB: the division, a look-up and one or two blocks for each wave.
 //
 // Arithmetic: as dcn_attention.hip, but for bf16 the weights enter the second product as three operands, which hold all

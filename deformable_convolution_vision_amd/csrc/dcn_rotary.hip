@@ -16,8 +16,8 @@
 // rotary_grad_kernel: a workgroup has all heads of its rows, a thread takes chunks of pairs straight from memory and
 // leaves each one's sum for each axis in the LDS, where one thread for each row and axis adds them in order.
 //
-// Memory bounds it: 8 x 16800 rows of 8 heads of 32, bf16, take 29.2 us for 137.8 MB, 4.7 TB/s of the 4.99 that a large
-// copy reaches, and 2 x 8400 rows of 8 heads of 64 10.3 us for 34.5 MB, a round and a start of the chip.  Chunks of
+// Memory bounds it: 8 x 16800 rows of 8 heads of 32, bf16, take 28.6 us for 137.8 MB, 4.8 TB/s of the 4.99 that a large
+// copy reaches, and 2 x 8400 rows of 8 heads of 64 9.9 us for 34.5 MB, a round and a start of the chip.  Chunks of
 // pairs straight from memory, each lane its two vectors, took 33.0 us for the first, and 64 where a head of 32 turns
 // one pair (26 now): their vectors are as wide as the layout's runs allow, those of whole heads always 16 bytes.
 // The positions' gradient of 2 x 900 rows takes 5.6 us, one round of 225 workgroups, each the chain of its loads,
